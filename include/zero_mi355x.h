@@ -45,6 +45,13 @@
  *     the fp16 gradient partition copied down and the fp16 parameters copied
  *     back up.
  *
+ * Next to the step stand the layer operators that produce a block's small
+ * parameter gradients: dropout whose mask is recomputed instead of stored,
+ * layer norm with the gradients of its weights, and the two joined around a
+ * residual sum (zero_dropout_*, zero_layernorm_*, zero_dropout_layernorm_*).
+ * Their weight and bias gradients go to a per-layer tensor the flatten packs,
+ * or straight to their place in the fp16 or fp32 partition.
+ *
  * Conventions for every entry point:
  *   - pointers named dev_* or documented as device memory are HIP device
  *     pointers; everything else is host memory;
@@ -89,6 +96,7 @@ const char* zero_status_string(int code);
 /* ---- element types of a flatten destination ------------------------- */
 #define ZERO_F16 1          /* IEEE binary16, stored as uint16_t bit patterns */
 #define ZERO_F32 2          /* IEEE binary32 */
+#define ZERO_BF16 3         /* bfloat16 (layer operators only) */
 
 /* One piece of a per-layer gradient tensor that lands in the partition:
  * count elements from src[src_off ...] go to dst[dst_off ...].
@@ -551,6 +559,132 @@ int zero_offload_step(zero_host_ctx_t* ctx, const uint16_t* dev_grad16, uint16_t
  * multiple of 64) on the context's workers: the host memory bandwidth
  * reference next to the host step.  Errors: ZERO_EINVAL, ZERO_EALIGN. */
 int zero_host_stream_copy(zero_host_ctx_t* ctx, void* dst, const void* src, uint64_t bytes);
+
+/* ---- layer operators ---------------------------------------------------
+ *
+ * The operators below work on matrices of `rows` rows (tokens) of `cols`
+ * elements (the hidden size), rows * ld elements apart: element (i, j) of x is
+ * x[i * ld_x + j].  Common to all of them:
+ *   - dtype is the type of every matrix: ZERO_F16, ZERO_BF16 or ZERO_F32.
+ *     vec_dtype is the type of w, b and bias, grad_dtype that of dw, db and
+ *     dbias: dtype or ZERO_F32, and not looked at when all of them are NULL;
+ *   - arithmetic and sums are binary32; a stored value is rounded once, to
+ *     nearest even;
+ *   - matrices and vectors are device memory, aligned to their element and no
+ *     more (a vector may be a slice of the flat partition at any offset); ld
+ *     >= cols, and the elements between two rows are neither read nor written
+ *     (one row: ld is not looked at);
+ *   - an output matrix may be one of the call's input matrices (the same
+ *     address and ld); two outputs must differ, and any other overlap of an
+ *     output with another argument gives undefined results;
+ *   - rows may be 0 (then the row sums dw, db, dbias are sums of nothing: 0, or
+ *     with accumulate left as they are);
+ *   - results do not depend on timing: equal calls give equal bits.
+ * Errors of all of them: ZERO_EINVAL (a required pointer NULL with rows > 0,
+ * a bad type, two equal outputs, eps not finite and > 0 in binary32, p not in
+ * [0, 1]), ZERO_EALIGN, ZERO_ERANGE (rows > 2^40, cols > 2^30, cols = 0 for a
+ * norm, ld < cols, rows * ld > 2^56, a workspace too small), ZERO_EHIP. */
+
+/* The state of the dropout generator in DEVICE memory (16 bytes, 8-byte
+ * aligned).  The mask of a call is a function of (seed, step, site, rows'
+ * index, column, cols): keep it unchanged between a forward pass and its
+ * backward (or recomputed forward) pass, and advance it once per training
+ * step.  Being in device memory, it lets a captured graph draw new masks at
+ * every replay. */
+typedef struct {
+    uint64_t seed;
+    uint32_t step;
+    uint32_t reserved;          /* 0 */
+} zero_rng_t;
+
+/* Enqueue the initialisation of a generator: this seed, step 0.
+ * Errors: ZERO_EINVAL (NULL), ZERO_EALIGN, ZERO_EHIP. */
+int zero_rng_init(zero_rng_t* dev_rng, uint64_t seed, void* stream);
+
+/* Enqueue step += 1 (modulo 2^32).  Errors: as zero_rng_init. */
+int zero_rng_advance(zero_rng_t* dev_rng, void* stream);
+
+/* Dropout, with the bias before it and the residual sum after it:
+ *   out = residual + D(x + bias),   D(v) = kept ? v * s : 0
+ * (residual and bias NULL: left out).  The mask is never stored: it is the
+ * counter-based generator Philox4x32-10 (Salmon et al. 2011) with
+ *   key     = (seed low, seed high),
+ *   counter = (g low, g high, site, step), g = i * ceil(cols / 8) + j / 8,
+ * of whose 128 output bits element (i, j) takes the 16-bit word j % 8 (low
+ * half of an output first).  The element is dropped when that word is below
+ *   t = floor(65536 p + 1/2);   s = fp32(65536 / (65536 - t)),
+ * so the drop probability is p to the nearest 2^-16 and the expectation is
+ * kept exactly for it; t = 0 draws nothing (dev_rng may then be NULL), t =
+ * 65536 drops everything.  A dropped element is 0 whatever it held, inf and
+ * NaN too.  site tells apart the dropouts of one step (layer and place).
+ * dev_rng: device, 8-byte aligned, read when the kernel runs. */
+int zero_dropout_fwd(void* out, uint64_t ld_out, const void* x, uint64_t ld_x, const void* residual,
+                     uint64_t ld_residual, const void* bias, int bias_dtype, uint64_t rows, uint64_t cols, int dtype,
+                     double p, const zero_rng_t* dev_rng, uint32_t site, void* stream);
+
+/* Bytes of device workspace the backward passes below need for this shape
+ * (any of them, any type); 0 for an empty or refused shape. */
+size_t zero_layer_workspace_bytes(uint64_t rows, uint64_t cols);
+
+/* The backward pass of zero_dropout_fwd for the same generator state, site
+ * and p:  dx = D(dout);  dbias[j] = sum over the rows of D(dout) (binary32,
+ * of the unrounded values), stored, or with accumulate added to what dbias
+ * holds, then rounded once to grad_dtype.  dbias may be NULL (no sum; then
+ * no workspace is needed).  The residual's gradient is dout itself.
+ * workspace: device, 16-byte aligned, >= zero_layer_workspace_bytes(rows,
+ * cols); contents need no initialisation; calls that share it must be
+ * ordered. */
+int zero_dropout_bwd(void* dx, uint64_t ld_dx, void* dbias, int grad_dtype, int accumulate, const void* dout,
+                     uint64_t ld_dout, uint64_t rows, uint64_t cols, int dtype, double p, const zero_rng_t* dev_rng,
+                     uint32_t site, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Layer norm (Ba, Kiros and Hinton 2016) over each row:
+ *   mean = sum(x) / cols,  var = sum((x - mean)^2) / cols,
+ *   rstd = 1 / sqrt(var + eps),  y = (x - mean) * rstd * w + b
+ * (w NULL: 1; b NULL: 0).  mean and rstd (binary32, one per row, kept for the
+ * backward pass) may be NULL. */
+int zero_layernorm_fwd(void* y, uint64_t ld_y, float* mean, float* rstd, const void* x, uint64_t ld_x, const void* w,
+                       const void* b, int vec_dtype, uint64_t rows, uint64_t cols, int dtype, double eps,
+                       void* stream);
+
+/* The backward pass of zero_layernorm_fwd, from the mean and rstd it stored:
+ *   h = (x - mean) * rstd,  g = dy * w,
+ *   dx = rstd * (g - sum(g)/cols - h * sum(g*h)/cols) + dres
+ *   dw[j] = sum over the rows of dy * h,  db[j] = sum over the rows of dy
+ * dres (NULL: none) is the gradient that reaches x past the norm (the residual
+ * stream of a pre-norm block).  dw and db may be NULL; they are stored, or
+ * with accumulate added to what is there, then rounded once to grad_dtype: a
+ * binary16 gradient too large for it becomes inf, which the step's decision
+ * finds.  workspace: as for zero_dropout_bwd (always needed). */
+int zero_layernorm_bwd(void* dx, uint64_t ld_dx, void* dw, void* db, int grad_dtype, int accumulate, const void* dy,
+                       uint64_t ld_dy, const void* dres, uint64_t ld_dres, const void* x, uint64_t ld_x,
+                       const float* mean, const float* rstd, const void* w, int vec_dtype, uint64_t rows,
+                       uint64_t cols, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The two joined, as a transformer block has them between two sublayers:
+ *   r = residual + D(x + bias)  (rounded to dtype and stored),
+ *   y = layer norm of that r.
+ * Equal to zero_dropout_fwd followed by zero_layernorm_fwd on its output, in
+ * one pass.  residual and bias may be NULL. */
+int zero_dropout_layernorm_fwd(void* r, uint64_t ld_r, void* y, uint64_t ld_y, float* mean, float* rstd, const void* x,
+                               uint64_t ld_x, const void* residual, uint64_t ld_residual, const void* bias,
+                               const void* w, const void* b, int vec_dtype, uint64_t rows, uint64_t cols, int dtype,
+                               double eps, double p, const zero_rng_t* dev_rng, uint32_t site, void* stream);
+
+/* The backward pass of zero_dropout_layernorm_fwd, from the r, mean and rstd
+ * it stored.  dy is y's gradient, dres (NULL: none) the gradient that reaches
+ * r from where else it is used:
+ *   e  = rstd * (g - sum(g)/cols - h * sum(g*h)/cols) + dres  (as above, at r)
+ *   dr = e (the residual's gradient),  dx = D(e),
+ *   dw, db as in zero_layernorm_bwd,  dbias[j] = sum over the rows of D(e)
+ * with D of the unrounded e.  dw, db and dbias may be NULL.  workspace: as
+ * for zero_layernorm_bwd. */
+int zero_dropout_layernorm_bwd(void* dx, uint64_t ld_dx, void* dr, uint64_t ld_dr, void* dw, void* db, void* dbias,
+                               int grad_dtype, int accumulate, const void* dy, uint64_t ld_dy, const void* dres,
+                               uint64_t ld_dres, const void* r, uint64_t ld_r, const float* mean, const float* rstd,
+                               const void* w, int vec_dtype, uint64_t rows, uint64_t cols, int dtype, double p,
+                               const zero_rng_t* dev_rng, uint32_t site, void* workspace, size_t workspace_bytes,
+                               void* stream);
 
 /* ---- measurement reference ------------------------------------------ */
 

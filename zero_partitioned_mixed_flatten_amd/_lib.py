@@ -13,7 +13,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libzero_mi355x.so")
 
 ZERO_OK, ZERO_EINVAL, ZERO_EALIGN, ZERO_ERANGE, ZERO_EHIP, ZERO_ENOTSUP, ZERO_ENOMEM = 0, -1, -2, -3, -4, -5, -6
-ZERO_F16, ZERO_F32 = 1, 2
+ZERO_F16, ZERO_F32, ZERO_BF16 = 1, 2, 3
 
 # Every function the public header declares (checked against the header by a test).
 EXPORTS = ("zero_status_string", "zero_state_bytes", "zero_bucket_segments", "zero_step_state_init",
@@ -23,7 +23,9 @@ EXPORTS = ("zero_status_string", "zero_state_bytes", "zero_bucket_segments", "ze
            "zero_shard_norm_overflow_f32", "zero_shard_adam_step_f32", "zero_host_create", "zero_host_destroy",
            "zero_host_threads", "zero_host_state_init", "zero_host_norm_overflow", "zero_host_adam_step",
            "zero_offload_step", "zero_host_stream_copy", "zero_onebit_state_init", "zero_onebit_workspace_bytes",
-           "zero_onebit_step", "zero_shard_norm_overflow_noalloc", "zero_shard_decide_f32")
+           "zero_onebit_step", "zero_shard_norm_overflow_noalloc", "zero_shard_decide_f32", "zero_rng_init",
+           "zero_rng_advance", "zero_dropout_fwd", "zero_dropout_bwd", "zero_layer_workspace_bytes",
+           "zero_layernorm_fwd", "zero_layernorm_bwd", "zero_dropout_layernorm_fwd", "zero_dropout_layernorm_bwd")
 NORM_PARTIAL_BYTES = 16
 
 
@@ -70,6 +72,11 @@ class OneBitState(C.Structure):
         return (int(u[1]) << 64) | int(u[0])
 
 
+class RngState(C.Structure):
+    _fields_ = [("seed", C.c_uint64), ("step", C.c_uint32), ("reserved", C.c_uint32)]
+
+
+RNG_BYTES = C.sizeof(RngState)
 STATE_BYTES = C.sizeof(StepState)
 ONEBIT_STATE_BYTES = C.sizeof(OneBitState)
 assert STATE_BYTES == 128 and C.sizeof(Segment) == 32 and C.sizeof(HParams) == 80 and ONEBIT_STATE_BYTES == 72
@@ -129,9 +136,24 @@ def lib():
         L.zero_onebit_workspace_bytes.restype = C.c_size_t
         L.zero_onebit_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, u64, vp, vp, vp, vp, C.c_int64, vp, C.c_size_t,
                                        vp]
+        f64 = C.c_double
+        L.zero_rng_init.argtypes = [vp, u64, vp]
+        L.zero_rng_advance.argtypes = [vp, vp]
+        L.zero_dropout_fwd.argtypes = [vp, u64, vp, u64, vp, u64, vp, i32, u64, u64, i32, f64, vp, u32, vp]
+        L.zero_dropout_bwd.argtypes = [vp, u64, vp, i32, i32, vp, u64, u64, u64, i32, f64, vp, u32, vp, C.c_size_t, vp]
+        L.zero_layer_workspace_bytes.argtypes = [u64, u64]
+        L.zero_layer_workspace_bytes.restype = C.c_size_t
+        L.zero_layernorm_fwd.argtypes = [vp, u64, vp, vp, vp, u64, vp, vp, i32, u64, u64, i32, f64, vp]
+        L.zero_layernorm_bwd.argtypes = [vp, u64, vp, vp, i32, i32, vp, u64, vp, u64, vp, u64, vp, vp, vp, i32, u64, u64,
+                                         i32, vp, C.c_size_t, vp]
+        L.zero_dropout_layernorm_fwd.argtypes = [vp, u64, vp, u64, vp, vp, vp, u64, vp, u64, vp, vp, vp, i32, u64, u64,
+                                                 i32, f64, f64, vp, u32, vp]
+        L.zero_dropout_layernorm_bwd.argtypes = [vp, u64, vp, u64, vp, vp, vp, i32, i32, vp, u64, vp, u64, vp, u64, vp,
+                                                 vp, vp, i32, u64, u64, i32, f64, vp, u32, vp, C.c_size_t, vp]
         for name in EXPORTS:
             if name not in ("zero_status_string", "zero_norm_workspace_bytes", "zero_flatten_norm_partials",
-                            "zero_decide_workspace_bytes", "zero_host_destroy", "zero_onebit_workspace_bytes"):
+                            "zero_decide_workspace_bytes", "zero_host_destroy", "zero_onebit_workspace_bytes",
+                            "zero_layer_workspace_bytes"):
                 getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -513,3 +535,201 @@ def zero_onebit_step(p16, p32, m32, v32, err_w, err_s, grad16, n: int, bits_w, b
 def read_onebit_state(dev_onebit) -> OneBitState:
     raw = dev_onebit.detach().to("cpu").numpy().tobytes()
     return OneBitState.from_buffer_copy(raw)
+
+
+# ---- layer operators -----------------------------------------------------------------
+# Matrices are torch tensors of shape (..., cols): contiguous, or 2-D with
+# contiguous rows any distance apart (a slice of a padded buffer).  Rows and
+# columns come from the first one; vectors over the columns (w, b, bias and
+# their gradients) are contiguous, of the matrices' type or float32.  Every
+# tensor lives on the current device, which the stream belongs to.
+
+_dtype_codes = None
+
+
+def _layer_dtype(fn: str, t) -> int:
+    global _dtype_codes
+    if _dtype_codes is None:
+        import torch
+        _dtype_codes = {torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32}
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{fn}: {t.dtype} is not float16, bfloat16 or float32")
+    return code
+
+
+class _LayerCall:
+    """One call's shape (from its first matrix) and the checks of its tensors."""
+    __slots__ = ("fn", "rows", "cols", "dtype", "code", "device", "stream")
+
+    def __init__(self, fn: str, ref, stream):
+        if not ref.is_cuda:
+            raise ValueError(f"{fn}: expected a device tensor")
+        if ref.dim() < 1:
+            raise ValueError(f"{fn}: expected a matrix")
+        self.fn, self.dtype, self.code = fn, ref.dtype, _layer_dtype(fn, ref)
+        self.cols = ref.shape[-1]
+        self.rows = ref.numel() // self.cols if self.cols else 0
+        self.device = ref.get_device()
+        import torch
+        if self.device != torch.cuda.current_device():
+            raise ValueError(f"{fn}: the tensors are on device {self.device}, the current device is "
+                             f"{torch.cuda.current_device()}")
+        if stream is not None and stream.device_index != self.device:
+            raise ValueError(f"{fn}: the stream belongs to device {stream.device_index}, the tensors are on "
+                             f"{self.device}")
+        self.stream = _stream(stream)
+
+    def mat(self, t) -> Tuple[int, int]:
+        """(address, row stride in elements) of a rows x cols matrix; (0, 0) for None."""
+        if t is None:
+            return 0, 0
+        if t.get_device() != self.device or t.dtype != self.dtype:
+            raise TypeError(f"{self.fn}: expected {self.dtype} on device {self.device}, got {t.dtype} on {t.device}")
+        if t.dim() < 1 or t.shape[-1] != self.cols or t.numel() != self.rows * self.cols:
+            raise ValueError(f"{self.fn}: expected {self.rows} x {self.cols} elements, got {tuple(t.shape)}")
+        if t.is_contiguous():
+            return t.data_ptr(), self.cols
+        if t.dim() != 2 or (self.cols > 1 and t.stride(1) != 1):
+            raise ValueError(f"{self.fn}: expected a contiguous tensor, or a 2-D one with contiguous rows")
+        return t.data_ptr(), t.stride(0)
+
+    def vecs(self, *ts) -> Tuple[int, ...]:
+        """The addresses of vectors over the columns (0 for None), then their one type."""
+        code, out = self.code, []
+        seen = None
+        for t in ts:
+            if t is None:
+                out.append(0)
+                continue
+            if seen is not None and t.dtype != seen:
+                raise TypeError(f"{self.fn}: the vectors are {seen} and {t.dtype}: they share one type")
+            seen = t.dtype
+            code = _layer_dtype(self.fn, t)
+            if code not in (self.code, ZERO_F32):
+                raise TypeError(f"{self.fn}: vectors are {self.dtype} or torch.float32, got {t.dtype}")
+            if t.get_device() != self.device:
+                raise ValueError(f"{self.fn}: expected device {self.device}, got {t.device}")
+            if t.numel() != self.cols or not t.is_contiguous():
+                raise ValueError(f"{self.fn}: expected a contiguous vector of {self.cols} elements")
+            out.append(t.data_ptr())
+        return (*out, code)
+
+    def stat(self, t) -> int:
+        """The address of a float32 vector over the rows (0 for None)."""
+        if t is None:
+            return 0
+        import torch
+        if t.dtype != torch.float32 or t.get_device() != self.device:
+            raise TypeError(f"{self.fn}: expected torch.float32 on device {self.device}, got {t.dtype} on {t.device}")
+        if t.numel() != self.rows or not t.is_contiguous():
+            raise ValueError(f"{self.fn}: expected a contiguous vector of {self.rows} elements (one per row)")
+        return t.data_ptr()
+
+    def rng(self, dev_rng) -> int:
+        if dev_rng is None:
+            return 0
+        if isinstance(dev_rng, int):
+            return dev_rng
+        _need(self.fn, dev_rng, RNG_BYTES)
+        if dev_rng.get_device() != self.device:
+            raise ValueError(f"{self.fn}: expected device {self.device}, got {dev_rng.device}")
+        return _ptr(dev_rng)
+
+    def workspace(self, ws, stream):
+        """(tensor, address, bytes).  None: taken from torch's allocator on the
+        call's stream, so neither streams nor captured graphs share it."""
+        if ws is None:
+            import torch
+            need = max(16, lib().zero_layer_workspace_bytes(self.rows, self.cols))
+            if stream is None:
+                ws = torch.empty(need, dtype=torch.uint8, device=f"cuda:{self.device}")
+            else:
+                with torch.cuda.stream(stream):
+                    ws = torch.empty(need, dtype=torch.uint8, device=f"cuda:{self.device}")
+        elif ws.get_device() != self.device:
+            raise ValueError(f"{self.fn}: expected device {self.device}, got {ws.device}")
+        return ws, _ptr(ws), ws.numel() * ws.element_size()
+
+    def check(self, rc: int) -> None:
+        if rc != ZERO_OK:
+            _check(self.fn, rc)
+
+
+def zero_rng_init(dev_rng, seed: int, stream=None) -> None:
+    _need("zero_rng_init", dev_rng, RNG_BYTES)
+    _check("zero_rng_init", lib().zero_rng_init(_ptr(dev_rng), seed, _stream(stream)))
+
+
+def zero_rng_advance(dev_rng, stream=None) -> None:
+    _need("zero_rng_advance", dev_rng, RNG_BYTES)
+    _check("zero_rng_advance", lib().zero_rng_advance(_ptr(dev_rng), _stream(stream)))
+
+
+def read_rng(dev_rng) -> RngState:
+    """Copy a generator's state to the host (synchronises the current stream)."""
+    return RngState.from_buffer_copy(dev_rng.detach().to("cpu").numpy().tobytes())
+
+
+def zero_layer_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().zero_layer_workspace_bytes(rows, cols))
+
+
+def zero_dropout_fwd(out, x, p: float, dev_rng, site: int = 0, residual=None, bias=None, stream=None) -> None:
+    """out = residual + D(x + bias)."""
+    c = _LayerCall("zero_dropout_fwd", out, stream)
+    bias_, btype = c.vecs(bias)
+    c.check(lib().zero_dropout_fwd(*c.mat(out), *c.mat(x), *c.mat(residual), bias_, btype, c.rows, c.cols, c.code, p,
+                                   c.rng(dev_rng), site, c.stream))
+
+
+def zero_dropout_bwd(dx, dout, p: float, dev_rng, site: int = 0, dbias=None, accumulate: bool = False, workspace=None,
+                     stream=None) -> None:
+    """dx = D(dout); dbias = (dbias +) the sum of D(dout) over the rows."""
+    c = _LayerCall("zero_dropout_bwd", dx, stream)
+    dbias_, gtype = c.vecs(dbias)
+    ws, wptr, wbytes = c.workspace(workspace, stream) if dbias is not None else (None, 0, 0)
+    c.check(lib().zero_dropout_bwd(*c.mat(dx), dbias_, gtype, int(bool(accumulate)), *c.mat(dout), c.rows, c.cols,
+                                   c.code, p, c.rng(dev_rng), site, wptr, wbytes, c.stream))
+
+
+def zero_layernorm_fwd(y, mean, rstd, x, w, b, eps: float = 1e-5, stream=None) -> None:
+    """y = (x - mean) * rstd * w + b, and each row's mean and rstd (None: not kept)."""
+    c = _LayerCall("zero_layernorm_fwd", y, stream)
+    w_, b_, vtype = c.vecs(w, b)
+    c.check(lib().zero_layernorm_fwd(*c.mat(y), c.stat(mean), c.stat(rstd), *c.mat(x), w_, b_, vtype, c.rows, c.cols,
+                                     c.code, eps, c.stream))
+
+
+def zero_layernorm_bwd(dx, dw, db, dy, x, mean, rstd, w, dres=None, accumulate: bool = False, workspace=None,
+                       stream=None) -> None:
+    """dx = the layer norm's gradient at x, plus dres; dw and db: the sums over the rows (None: not wanted)."""
+    c = _LayerCall("zero_layernorm_bwd", dx, stream)
+    dw_, db_, gtype = c.vecs(dw, db)
+    w_, vtype = c.vecs(w)
+    ws, wptr, wbytes = c.workspace(workspace, stream)
+    c.check(lib().zero_layernorm_bwd(*c.mat(dx), dw_, db_, gtype, int(bool(accumulate)), *c.mat(dy), *c.mat(dres),
+                                     *c.mat(x), c.stat(mean), c.stat(rstd), w_, vtype, c.rows, c.cols, c.code, wptr,
+                                     wbytes, c.stream))
+
+
+def zero_dropout_layernorm_fwd(r, y, mean, rstd, x, residual, bias, w, b, eps: float, p: float, dev_rng,
+                               site: int = 0, stream=None) -> None:
+    """r = residual + D(x + bias); y = the layer norm of r, and each row's mean and rstd."""
+    c = _LayerCall("zero_dropout_layernorm_fwd", r, stream)
+    bias_, w_, b_, vtype = c.vecs(bias, w, b)
+    c.check(lib().zero_dropout_layernorm_fwd(*c.mat(r), *c.mat(y), c.stat(mean), c.stat(rstd), *c.mat(x),
+                                             *c.mat(residual), bias_, w_, b_, vtype, c.rows, c.cols, c.code, eps, p,
+                                             c.rng(dev_rng), site, c.stream))
+
+
+def zero_dropout_layernorm_bwd(dx, dr, dw, db, dbias, dy, dres, r, mean, rstd, w, p: float, dev_rng, site: int = 0,
+                               accumulate: bool = False, workspace=None, stream=None) -> None:
+    """dr = the layer norm's gradient at r, plus dres; dx = D(dr); dw, db and dbias: the sums over the rows."""
+    c = _LayerCall("zero_dropout_layernorm_bwd", dx, stream)
+    dw_, db_, dbias_, gtype = c.vecs(dw, db, dbias)
+    w_, vtype = c.vecs(w)
+    ws, wptr, wbytes = c.workspace(workspace, stream)
+    c.check(lib().zero_dropout_layernorm_bwd(*c.mat(dx), *c.mat(dr), dw_, db_, dbias_, gtype, int(bool(accumulate)),
+                                             *c.mat(dy), *c.mat(dres), *c.mat(r), c.stat(mean), c.stat(rstd), w_, vtype,
+                                             c.rows, c.cols, c.code, p, c.rng(dev_rng), site, wptr, wbytes, c.stream))

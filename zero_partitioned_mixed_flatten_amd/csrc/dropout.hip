@@ -59,7 +59,8 @@ __global__ __launch_bounds__(kDropBlock) void dropout_kernel(DropoutArgs<T> a)
         uint32_t c = uint32_t(base - row0 * a.groups) + threadIdx.x;
         const uint32_t wrap = c / uint32_t(a.groups);
         const uint64_t row = row0 + wrap;
-        const uint32_t col = (c - wrap * uint32_t(a.groups)) * 8, k = a.cols - col;
+        const uint32_t col = (c - wrap * uint32_t(a.groups)) * 8;
+        const int k = int(a.cols - col);
         f32x8 v = widen<T>(load8(a.x + row * a.ld_x + col, k));
         if (a.bias)
             v = v + load8_vector<T>(a.bias, a.bias_f32, col, k, 0.0f);

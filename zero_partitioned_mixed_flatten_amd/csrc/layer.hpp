@@ -37,8 +37,9 @@ struct Raw<float> {
     typedef f32x8 type;
 };
 
+// The first k elements of a group (k <= 0: none), the others 0.
 template <typename T>
-__device__ __forceinline__ typename Raw<T>::type load8(const T* p, uint32_t k)
+__device__ __forceinline__ typename Raw<T>::type load8(const T* p, int k)
 {
     typedef typename Raw<T>::type V;
     typedef V __attribute__((aligned(sizeof(T)))) VU;
@@ -46,24 +47,41 @@ __device__ __forceinline__ typename Raw<T>::type load8(const T* p, uint32_t k)
         return __builtin_nontemporal_load(reinterpret_cast<const VU*>(p));
     V v;
 #pragma unroll
-    for (uint32_t j = 0; j < 8; ++j)
-        v[j] = j < k ? p[j] : T(0.0f);
+    for (int j = 0; j < 8; ++j)
+        v[j] = T(0.0f);
+    if (k > 0)
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < k)
+                v[j] = p[j];
     return v;
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T* p, typename Raw<T>::type v, uint32_t k)
+__device__ __forceinline__ void store8(T* p, typename Raw<T>::type v, int k)
 {
     typedef typename Raw<T>::type V;
     typedef V __attribute__((aligned(sizeof(T)))) VU;
-    if (k >= 8) {
+    if (k >= 8)
         __builtin_nontemporal_store(v, reinterpret_cast<VU*>(p));
-        return;
-    }
+    else if (k > 0)
 #pragma unroll
-    for (uint32_t j = 0; j < 8; ++j)
-        if (j < k)
-            p[j] = v[j];
+        for (int j = 0; j < 7; ++j)
+            if (j < k)
+                p[j] = v[j];
+}
+
+// 8 sums into a partial's row, which the fold reads back soon: kept in the caches.
+__device__ __forceinline__ void store8_f32(float* p, f32x8 v, int k)
+{
+    typedef f32x8 __attribute__((aligned(4))) VU;
+    if (k >= 8)
+        *reinterpret_cast<VU*>(p) = v;
+    else if (k > 0)
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < k)
+                p[j] = v[j];
 }
 
 template <typename T>
@@ -81,23 +99,23 @@ __device__ __forceinline__ typename Raw<T>::type narrow(f32x8 v)   // round to n
 // The vectors over the columns (weights, biases) have a type of their own:
 // the matrices' or binary32.  An absent one (NULL) reads as `absent`.
 template <typename T>
-__device__ __forceinline__ f32x8 load8_vector(const void* p, bool f32, uint64_t col, uint32_t k, float absent)
+__device__ __forceinline__ f32x8 load8_vector(const void* p, bool f32, uint64_t col, int k, float absent)
 {
     f32x8 v;
-    if (!p) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = absent;
+    for (int j = 0; j < 8; ++j)
+        v[j] = absent;
+    if (!p || k <= 0)
         return v;
-    }
     if (f32) {
         typedef f32x8 __attribute__((aligned(4))) VU;
         const float* q = static_cast<const float*>(p) + col;
         if (k >= 8)
             return *reinterpret_cast<const VU*>(q);
 #pragma unroll
-        for (uint32_t j = 0; j < 8; ++j)
-            v[j] = j < k ? q[j] : 0.0f;
+        for (int j = 0; j < 7; ++j)
+            if (j < k)
+                v[j] = q[j];
         return v;
     }
     typedef typename Raw<T>::type V;
@@ -106,8 +124,9 @@ __device__ __forceinline__ f32x8 load8_vector(const void* p, bool f32, uint64_t 
     if (k >= 8)
         return widen<T>(*reinterpret_cast<const VU*>(q));
 #pragma unroll
-    for (uint32_t j = 0; j < 8; ++j)
-        v[j] = j < k ? float(q[j]) : 0.0f;
+    for (int j = 0; j < 7; ++j)
+        if (j < k)
+            v[j] = float(q[j]);
     return v;
 }
 
@@ -171,29 +190,62 @@ __device__ __forceinline__ f32x8 dropped(f32x8 v, const Drop& d, RngKey key, uin
     return v;
 }
 
-// ---- sums over a workgroup ----------------------------------------------------------
-__device__ __forceinline__ float wave_sum(float v)
+// ---- sums over the threads of a row ------------------------------------------------------
+// A row is shared by TPR threads.  Within a wave the sum goes through lane
+// permutes of the vector ALU (DPP), each step a pairwise addition that both
+// lanes do alike, so every thread of the row ends with the same bits.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v)
 {
-#pragma unroll
-    for (int m = 32; m; m >>= 1)
-        v += __shfl_xor(v, m);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v)
+{
+    v += dpp<0xB1>(v);                             // quad_perm 1,0,3,2: lane ^ 1
+    v += dpp<0x4E>(v);                             // quad_perm 2,3,0,1: lane ^ 2
+    v += dpp<0x141>(v);                            // row_half_mirror: the other quad of 8
+    if (LANES >= 16)
+        v += dpp<0x140>(v);                        // row_mirror: the other 8 of 16
+    if (LANES >= 32)
+        v += __shfl_xor(v, 16);
+    if (LANES >= 64)
+        v += __shfl_xor(v, 32);
     return v;
 }
 
-// The sum of v over the workgroup, in every thread, in a fixed order.
-// `scratch`: one float per wave; usable again after the next barrier.
-template <int BLOCK>
-__device__ __forceinline__ float block_sum(float v, float* scratch)
+// The sums of N values over the TPR threads of each row of the workgroup, in
+// every thread of the row.  Rows wider than a wave meet in LDS, one barrier
+// a call: `scratch` is [2][N][BLOCK / 64] floats, its halves used in turn
+// (`parity`), so a call's reads are over before the same half is written
+// again.  Every thread of the workgroup calls it.
+template <int BLOCK, int TPR, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float* scratch, uint32_t& parity)
 {
-    v = wave_sum(v);
-    if ((threadIdx.x & 63) == 0)
-        scratch[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < BLOCK / 64; ++i)
-        s += scratch[i];
-    return s;
+    for (int i = 0; i < N; ++i)
+        v[i] = lanes_sum<(TPR < 64 ? TPR : 64)>(v[i]);
+    if (TPR <= 64)
+        return;
+    constexpr int kWaves = BLOCK / 64, kPerRow = TPR / 64;
+    float* buf = scratch + parity * (N * kWaves);
+    parity ^= 1;
+    const uint32_t wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            buf[i * kWaves + wave] = v[i];
+    __syncthreads();
+    const uint32_t first = wave / kPerRow * kPerRow;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kPerRow; ++j)
+            s += buf[i * kWaves + first + j];
+        v[i] = s;
+    }
 }
 
 // ---- host side ------------------------------------------------------------------------

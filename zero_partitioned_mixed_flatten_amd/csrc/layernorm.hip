@@ -35,21 +35,110 @@ struct FwdArgs {
     Drop drop;
 };
 
+// Rows that fit the registers of TPR threads, VPT groups of 8 columns each:
+// one pass over memory, the row kept as it was loaded.
+template <typename T, bool JOIN, int BLOCK, int TPR, int VPT>
+__global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
+{
+    typedef typename Raw<T>::type V;
+    constexpr int kRows = BLOCK / TPR;
+    __shared__ alignas(16) float scratch[2 * BLOCK / 64];
+    uint32_t parity = 0;
+    const RngKey key = rng_key(a.drop);
+    const uint32_t groups = (a.cols + 7) / 8;
+    const float n = float(a.cols);
+    uint32_t slot = threadIdx.x / TPR;
+    if (TPR >= 64)
+        slot = __builtin_amdgcn_readfirstlane(slot);
+    const uint32_t t = threadIdx.x % TPR;
+    for (uint64_t first = uint64_t(blockIdx.x) * kRows; first < a.rows; first += uint64_t(gridDim.x) * kRows) {
+        const uint64_t row = first + slot;
+        const bool live = row < a.rows;
+        V raw[VPT];
+        f32x8 w[VPT], b[VPT];
+        float s[1] = {0.0f}, q[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const uint32_t g = i * TPR + t, col = g * 8;
+            const int k = live ? int(a.cols) - int(col) : 0;
+            raw[i] = load8(a.x + row * a.ld_x + col, k);
+            if (JOIN) {
+                V res;
+                if (a.residual)
+                    res = load8(a.residual + row * a.ld_res + col, k);
+                f32x8 v = widen<T>(raw[i]);
+                if (a.bias)
+                    v = v + load8_vector<T>(a.bias, a.vec_f32, col, k, 0.0f);
+                v = dropped(v, a.drop, key, row * groups + g);
+                if (a.residual)
+                    v = widen<T>(res) + v;
+                raw[i] = narrow<T>(v);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const uint32_t col = (i * TPR + t) * 8;
+            const int k = live ? int(a.cols) - int(col) : 0;
+            w[i] = load8_vector<T>(a.w, a.vec_f32, col, k, 1.0f);
+            b[i] = load8_vector<T>(a.b, a.vec_f32, col, k, 0.0f);
+            if (JOIN)
+                store8(a.r + row * a.ld_r + col, raw[i], k);
+            f32x8 v = widen<T>(raw[i]);
+            if (k < 8)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = j < k ? v[j] : 0.0f;
+            s[0] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        }
+        row_sum<BLOCK, TPR>(s, scratch, parity);
+        const float mean = s[0] / n;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int k = int(a.cols) - int((i * TPR + t) * 8);
+            f32x8 v = widen<T>(raw[i]) - mean;
+            if (k < 8)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = j < k ? v[j] : 0.0f;
+            v = v * v;
+            q[0] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        }
+        row_sum<BLOCK, TPR>(q, scratch, parity);
+        const float rstd = 1.0f / sqrtf(q[0] / n + a.eps);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const uint32_t col = (i * TPR + t) * 8;
+            const int k = live ? int(a.cols) - int(col) : 0;
+            f32x8 v = widen<T>(raw[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = __builtin_fmaf((v[j] - mean) * rstd, w[i][j], b[i][j]);
+            store8(a.y + row * a.ld_y + col, narrow<T>(v), k);
+        }
+        if (t == 0 && live) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+    }
+}
+
 // Any width: a workgroup takes a row and goes over it three times.
 constexpr int kWideBlock = 256;
 
 template <typename T, bool JOIN>
 __global__ __launch_bounds__(kWideBlock) void norm_fwd_wide_kernel(FwdArgs<T> a)
 {
-    __shared__ float scratch[2][kWideBlock / 64];
+    __shared__ alignas(16) float scratch[2 * kWideBlock / 64];
+    uint32_t parity = 0;
     const RngKey key = rng_key(a.drop);
     const uint32_t groups = (a.cols + 7) / 8;
     const float n = float(a.cols);
     for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T* src = a.x + row * a.ld_x;
-        float s = 0.0f;
+        float s[1] = {0.0f}, q[1] = {0.0f};
         for (uint32_t g = threadIdx.x; g < groups; g += kWideBlock) {
-            const uint32_t col = g * 8, k = a.cols - col;
+            const uint32_t col = g * 8;
+            const int k = int(a.cols) - int(col);
             typename Raw<T>::type raw = load8(src + col, k);
             if (JOIN) {
                 f32x8 v = widen<T>(raw);
@@ -63,25 +152,28 @@ __global__ __launch_bounds__(kWideBlock) void norm_fwd_wide_kernel(FwdArgs<T> a)
             }
             const f32x8 v = widen<T>(raw);
 #pragma unroll
-            for (uint32_t j = 0; j < 8; ++j)
-                s += j < k ? v[j] : 0.0f;
+            for (int j = 0; j < 8; ++j)
+                s[0] += j < k ? v[j] : 0.0f;
         }
-        const float mean = block_sum<kWideBlock>(s, scratch[0]) / n;
+        row_sum<kWideBlock, kWideBlock>(s, scratch, parity);
+        const float mean = s[0] / n;
         if (JOIN)
             src = a.r + row * a.ld_r;
-        float q = 0.0f;
         for (uint32_t g = threadIdx.x; g < groups; g += kWideBlock) {
-            const uint32_t col = g * 8, k = a.cols - col;
+            const uint32_t col = g * 8;
+            const int k = int(a.cols) - int(col);
             const f32x8 v = widen<T>(load8(src + col, k));
 #pragma unroll
-            for (uint32_t j = 0; j < 8; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const float d = j < k ? v[j] - mean : 0.0f;
-                q = __builtin_fmaf(d, d, q);
+                q[0] = __builtin_fmaf(d, d, q[0]);
             }
         }
-        const float rstd = 1.0f / sqrtf(block_sum<kWideBlock>(q, scratch[1]) / n + a.eps);
+        row_sum<kWideBlock, kWideBlock>(q, scratch, parity);
+        const float rstd = 1.0f / sqrtf(q[0] / n + a.eps);
         for (uint32_t g = threadIdx.x; g < groups; g += kWideBlock) {
-            const uint32_t col = g * 8, k = a.cols - col;
+            const uint32_t col = g * 8;
+            const int k = int(a.cols) - int(col);
             f32x8 v = widen<T>(load8(src + col, k));
             const f32x8 w = load8_vector<T>(a.w, a.vec_f32, col, k, 1.0f);
             const f32x8 b = load8_vector<T>(a.b, a.vec_f32, col, k, 0.0f);
@@ -94,13 +186,32 @@ __global__ __launch_bounds__(kWideBlock) void norm_fwd_wide_kernel(FwdArgs<T> a)
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
-        __syncthreads();                           // scratch is free for the next row
     }
+}
+
+template <typename T, bool JOIN, int TPR, int VPT>
+int launch_rows(const FwdArgs<T>& a, hipStream_t s)
+{
+    constexpr int kBlock = TPR < 256 ? 256 : TPR;
+    uint64_t grid = (a.rows + kBlock / TPR - 1) / (kBlock / TPR);
+    if (grid > (1u << 20))
+        grid = 1u << 20;
+    hipLaunchKernelGGL((norm_fwd_kernel<T, JOIN, kBlock, TPR, VPT>), dim3(uint32_t(grid)), dim3(kBlock), 0, s, a);
+    return launch_status();
 }
 
 template <typename T, bool JOIN>
 int launch_fwd(const FwdArgs<T>& a, hipStream_t s)
 {
+    if (a.cols <= 64) return launch_rows<T, JOIN, 8, 1>(a, s);
+    if (a.cols <= 128) return launch_rows<T, JOIN, 16, 1>(a, s);
+    if (a.cols <= 256) return launch_rows<T, JOIN, 32, 1>(a, s);
+    if (a.cols <= 512) return launch_rows<T, JOIN, 64, 1>(a, s);
+    if (a.cols <= 1024) return launch_rows<T, JOIN, 128, 1>(a, s);
+    if (a.cols <= 2048) return launch_rows<T, JOIN, 256, 1>(a, s);
+    if (a.cols <= 4096) return launch_rows<T, JOIN, 512, 1>(a, s);
+    if (a.cols <= 8192) return launch_rows<T, JOIN, 512, 2>(a, s);
+    if (a.cols <= 16384) return launch_rows<T, JOIN, 1024, 2>(a, s);
     const uint64_t grid = a.rows < (1u << 20) ? a.rows : (1u << 20);
     hipLaunchKernelGGL((norm_fwd_wide_kernel<T, JOIN>), dim3(uint32_t(grid)), dim3(kWideBlock), 0, s, a);
     return launch_status();

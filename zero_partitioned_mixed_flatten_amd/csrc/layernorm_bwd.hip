@@ -35,6 +35,158 @@ struct BwdArgs {
     bool want[3];                                  // dw, db, dbias
 };
 
+// Rows that fit the registers of TPR threads, VPT groups of 8 columns each,
+// in one pass: a persistent workgroup takes every gridDim.x-th block of
+// BLOCK / TPR rows, the next rows' loads in flight while it works on the
+// present ones, and keeps its columns' sums in registers to the end, where
+// it stores one partial.
+template <typename T, bool NORM, bool DROP, int BLOCK, int TPR, int VPT>
+__global__ __launch_bounds__(BLOCK) void rows_bwd_kernel(BwdArgs<T> a)
+{
+    typedef typename Raw<T>::type V;
+    constexpr int kRows = BLOCK / TPR;
+    constexpr int kSums = (NORM ? 2 : 0) + (DROP ? 1 : 0);
+    __shared__ alignas(16) float scratch[NORM ? 4 * BLOCK / 64 : 1];
+    uint32_t parity = 0;
+    const RngKey key = rng_key(a.drop);
+    const uint32_t groups = (a.cols + 7) / 8;
+    const float n = float(a.cols);
+    uint32_t slot = threadIdx.x / TPR;
+    if (TPR >= 64)
+        slot = __builtin_amdgcn_readfirstlane(slot);
+    const uint32_t t = threadIdx.x % TPR;
+
+    f32x8 w[VPT], sum[kSums][VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const uint32_t col = (i * TPR + t) * 8;
+        if (NORM)
+            w[i] = load8_vector<T>(a.w, a.vec_f32, col, int(a.cols) - int(col), 1.0f);
+#pragma unroll
+        for (int q = 0; q < kSums; ++q)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                sum[q][i][j] = 0.0f;
+    }
+
+    struct Row {
+        V dy[VPT], r[VPT], dres[VPT];
+        float mean, rstd;
+    };
+    auto fetch = [&](uint64_t row, Row& f) {
+        const bool live = row < a.rows;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const uint32_t col = (i * TPR + t) * 8;
+            const int k = live ? int(a.cols) - int(col) : 0;
+            f.dy[i] = load8(a.dy + row * a.ld_dy + col, k);
+            if (NORM) {
+                f.r[i] = load8(a.r + row * a.ld_r + col, k);
+                if (a.dres)
+                    f.dres[i] = load8(a.dres + row * a.ld_dres + col, k);
+            }
+        }
+        f.mean = NORM && live ? a.mean[row] : 0.0f;
+        f.rstd = NORM && live ? a.rstd[row] : 0.0f;
+    };
+
+    const uint64_t stride = uint64_t(gridDim.x) * kRows;
+    uint64_t first = uint64_t(blockIdx.x) * kRows;
+    Row cur;
+    fetch(first + slot, cur);
+    for (; first < a.rows; first += stride) {
+        const uint64_t row = first + slot;
+        const bool live = row < a.rows;
+        Row next;
+        fetch(row + stride, next);
+
+        float c[2] = {0.0f, 0.0f};
+        if (NORM) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const f32x8 dy = widen<T>(cur.dy[i]);
+                const f32x8 g = dy * w[i], h = (widen<T>(cur.r[i]) - cur.mean) * cur.rstd;
+                const f32x8 gh = g * h;            // dy is 0 past the row's end
+                c[0] += ((g[0] + g[1]) + (g[2] + g[3])) + ((g[4] + g[5]) + (g[6] + g[7]));
+                c[1] += ((gh[0] + gh[1]) + (gh[2] + gh[3])) + ((gh[4] + gh[5]) + (gh[6] + gh[7]));
+            }
+            row_sum<BLOCK, TPR>(c, scratch, parity);
+            c[0] = c[0] / n;
+            c[1] = c[1] / n;
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const uint32_t g8 = i * TPR + t, col = g8 * 8;
+            const int k = live ? int(a.cols) - int(col) : 0;
+            f32x8 e = widen<T>(cur.dy[i]);
+            if (NORM) {
+                const f32x8 dy = e, h = (widen<T>(cur.r[i]) - cur.mean) * cur.rstd;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    sum[0][i][j] = __builtin_fmaf(dy[j], h[j], sum[0][i][j]);
+                    sum[1][i][j] += dy[j];
+                    e[j] = cur.rstd * __builtin_fmaf(-h[j], c[1], dy[j] * w[i][j] - c[0]);
+                }
+                if (a.dres)
+                    e = e + widen<T>(cur.dres[i]);
+            }
+            if (DROP) {
+                if (NORM)
+                    store8(a.dr + row * a.ld_dr + col, narrow<T>(e), k);
+                e = dropped(e, a.drop, key, row * groups + g8);
+                if (k > 0)
+                    sum[kSums - 1][i] = sum[kSums - 1][i] + e;
+            }
+            store8(a.dx + row * a.ld_dx + col, narrow<T>(e), k);
+        }
+        cur = next;
+    }
+
+    // one partial of the workgroup: the upper half of its rows' threads hands
+    // its sums to the lower half, until one row's are left
+    if (kRows > 1) {
+        __shared__ f32x4 hand[kRows > 1 ? kSums * VPT * BLOCK : 1];
+#pragma unroll
+        for (int half = kRows / 2; half >= 1; half /= 2) {
+            const int lanes = half * TPR;
+            if (int(slot) >= half && int(slot) < 2 * half)
+#pragma unroll
+                for (int q = 0; q < kSums * VPT; ++q)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const f32x8 v = sum[q / VPT][q % VPT];
+                        hand[(2 * q + p) * lanes + (int(threadIdx.x) - lanes)] = f32x4{v[4 * p], v[4 * p + 1], v[4 * p + 2],
+                                                                                       v[4 * p + 3]};
+                    }
+            __syncthreads();
+            if (int(slot) < half)
+#pragma unroll
+                for (int q = 0; q < kSums * VPT; ++q)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const f32x4 o = hand[(2 * q + p) * lanes + int(threadIdx.x)];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            sum[q / VPT][q % VPT][4 * p + j] += o[j];
+                    }
+            __syncthreads();
+        }
+    }
+    if (slot != 0)
+        return;
+#pragma unroll
+    for (int q = 0; q < kSums; ++q) {
+        const int which = NORM ? q : 2;
+        if (!a.want[which])
+            continue;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const uint32_t col = (i * TPR + t) * 8;
+            store8_f32(a.partials + (uint64_t(blockIdx.x) * 3 + which) * a.cols + col, sum[q][i], int(a.cols) - int(col));
+        }
+    }
+}
+
 // The pass in two kernels, for any width: c1 and c2 of each row, then strips
 // of columns going down a chunk of rows.
 constexpr int kWideBlock = 256;
@@ -52,32 +204,32 @@ uint64_t wide_chunks(uint64_t rows, uint64_t cols)
 template <typename T>
 __global__ __launch_bounds__(kWideBlock) void row_sums_kernel(BwdArgs<T> a)
 {
-    __shared__ float scratch[2][kWideBlock / 64];
+    __shared__ alignas(16) float scratch[4 * kWideBlock / 64];
+    uint32_t parity = 0;
     const uint32_t groups = (a.cols + 7) / 8;
     for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const float mean = a.mean[row], rstd = a.rstd[row];
-        float s1 = 0.0f, s2 = 0.0f;
+        float s[2] = {0.0f, 0.0f};
         for (uint32_t g = threadIdx.x; g < groups; g += kWideBlock) {
-            const uint32_t col = g * 8, k = a.cols - col;
+            const uint32_t col = g * 8;
+            const int k = int(a.cols) - int(col);
             const f32x8 dy = widen<T>(load8(a.dy + row * a.ld_dy + col, k));
             const f32x8 r = widen<T>(load8(a.r + row * a.ld_r + col, k));
             const f32x8 w = load8_vector<T>(a.w, a.vec_f32, col, k, 1.0f);
 #pragma unroll
-            for (uint32_t j = 0; j < 8; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const float gj = dy[j] * w[j], h = (r[j] - mean) * rstd;
                 if (j < k) {
-                    s1 += gj;
-                    s2 = __builtin_fmaf(gj, h, s2);
+                    s[0] += gj;
+                    s[1] = __builtin_fmaf(gj, h, s[1]);
                 }
             }
         }
-        s1 = block_sum<kWideBlock>(s1, scratch[0]);
-        s2 = block_sum<kWideBlock>(s2, scratch[1]);
+        row_sum<kWideBlock, kWideBlock>(s, scratch, parity);
         if (threadIdx.x == 0) {
-            a.row_sums[2 * row] = s1 / float(a.cols);
-            a.row_sums[2 * row + 1] = s2 / float(a.cols);
+            a.row_sums[2 * row] = s[0] / float(a.cols);
+            a.row_sums[2 * row + 1] = s[1] / float(a.cols);
         }
-        __syncthreads();
     }
 }
 
@@ -89,7 +241,8 @@ __global__ __launch_bounds__(kWideBlock) void strips_kernel(BwdArgs<T> a)
     if (g >= groups)
         return;
     const RngKey key = rng_key(a.drop);
-    const uint32_t col = g * 8, k = a.cols - col;
+    const uint32_t col = g * 8;
+    const int k = int(a.cols) - int(col);
     f32x8 w, sum[3];
     if (NORM)
         w = load8_vector<T>(a.w, a.vec_f32, col, k, 1.0f);
@@ -128,29 +281,49 @@ __global__ __launch_bounds__(kWideBlock) void strips_kernel(BwdArgs<T> a)
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i)
-        if (a.want[i]) {
-            float* p = a.partials + (uint64_t(blockIdx.y) * 3 + i) * a.cols + col;
-            for (uint32_t j = 0; j < 8; ++j)
-                if (j < k)
-                    p[j] = sum[i][j];
-        }
+        if (a.want[i])
+            store8_f32(a.partials + (uint64_t(blockIdx.y) * 3 + i) * a.cols + col, sum[i], k);
 }
 
-// Adds the chunks' partials of each column in their order and stores the sum,
-// or adds it to what is there, rounded once to the gradient's type.
-constexpr int kFoldBlock = 256;
+// Adds the partials of each column in their order and stores the sum, or adds
+// it to what is there, rounded once to the gradient's type.  A workgroup
+// takes 64 columns; each of its 16 waves adds every 16th partial, its loads in
+// flight together, and the waves' sums are added in order.
+constexpr int kFoldBlock = 1024;
+constexpr uint32_t kFoldCols = 64;
 
 template <typename T>
-__global__ __launch_bounds__(kFoldBlock) void fold_kernel(SumOut out, const float* partials, uint32_t chunks,
+__global__ __launch_bounds__(kFoldBlock) void fold_kernel(SumOut out, const float* __restrict__ partials, uint32_t chunks,
                                                           uint32_t cols)
 {
-    const uint64_t col = uint64_t(blockIdx.x) * kFoldBlock + threadIdx.x;
+    __shared__ float part[kFoldBlock / 64][kFoldCols];
     const int i = blockIdx.y;
-    if (col >= cols || !out.dst[i])
+    if (!out.dst[i])
         return;
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t col = blockIdx.x * kFoldCols + lane;
     float s = 0.0f;
-    for (uint32_t c = 0; c < chunks; ++c)
-        s += partials[(uint64_t(c) * 3 + i) * cols + col];
+    if (col < cols) {
+        const float* p = partials + uint64_t(i) * cols + col;
+        const uint64_t step = uint64_t(3) * cols;
+        for (uint32_t c = wave; c < chunks; c += 8 * 16) {
+            float v[8];
+#pragma unroll
+            for (uint32_t u = 0; u < 8; ++u)
+                v[u] = c + 16 * u < chunks ? p[(c + 16 * u) * step] : 0.0f;
+#pragma unroll
+            for (uint32_t u = 0; u < 8; ++u)
+                s += v[u];
+        }
+    }
+    part[wave][lane] = s;
+    __syncthreads();
+    if (wave || col >= cols)
+        return;
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kFoldBlock / 64; ++k)
+        s += part[k][lane];
     if (out.f32) {
         float* d = static_cast<float*>(out.dst[i]) + col;
         *d = out.accumulate ? *d + s : s;
@@ -176,11 +349,39 @@ struct BwdCall {
     size_t workspace_bytes;
 };
 
-uint64_t row_sums_bytes(uint64_t rows) { return (rows * 8 + 15) / 16 * 16; }
+// Widest row of the one-pass kernel, and the workgroups it runs: one per CU,
+// fewer where there are fewer rows.
+constexpr uint64_t kRowsMaxCols = 8192;
+constexpr uint64_t kRowsGrid = 256;
+constexpr int kRowsBlock = 1024;
+
+uint64_t rows_tpr(uint64_t cols)
+{
+    uint64_t tpr = 8;
+    while (tpr * 8 < cols)
+        tpr *= 2;
+    return tpr;
+}
+
+uint64_t rows_chunks(uint64_t rows, uint64_t cols)
+{
+    const uint64_t per = kRowsBlock / rows_tpr(cols), blocks = (rows + per - 1) / per;
+    return blocks < kRowsGrid ? blocks : kRowsGrid;
+}
+
+uint64_t row_sums_bytes(uint64_t rows, uint64_t cols) { return cols <= kRowsMaxCols ? 0 : (rows * 8 + 15) / 16 * 16; }
 
 uint64_t workspace_need(uint64_t rows, uint64_t cols)
 {
-    return row_sums_bytes(rows) + wide_chunks(rows, cols) * 3 * cols * 4;
+    const uint64_t chunks = cols <= kRowsMaxCols ? rows_chunks(rows, cols) : wide_chunks(rows, cols);
+    return row_sums_bytes(rows, cols) + chunks * 3 * cols * 4;
+}
+
+template <typename T, bool NORM, bool DROP, int TPR>
+void launch_rows(const BwdArgs<T>& a, uint64_t chunks, hipStream_t s)
+{
+    hipLaunchKernelGGL((rows_bwd_kernel<T, NORM, DROP, kRowsBlock, TPR, 1>), dim3(uint32_t(chunks)), dim3(kRowsBlock), 0, s,
+                       a);
 }
 
 template <typename T, bool NORM, bool DROP>
@@ -205,12 +406,24 @@ int run_bwd(const BwdCall& c, hipStream_t s)
     a.vec_f32 = c.vec_dtype == ZERO_F32;
     a.drop = c.drop;
     a.row_sums = static_cast<float*>(c.workspace);
-    a.partials = reinterpret_cast<float*>(static_cast<char*>(c.workspace) + row_sums_bytes(c.rows));
+    a.partials = reinterpret_cast<float*>(static_cast<char*>(c.workspace) + row_sums_bytes(c.rows, c.cols));
     a.want[0] = c.dw;
     a.want[1] = c.db;
     a.want[2] = c.dbias;
     uint64_t chunks = 0;
-    if (c.rows) {
+    if (c.rows && c.cols <= kRowsMaxCols) {
+        chunks = rows_chunks(c.rows, c.cols);
+        switch (rows_tpr(c.cols)) {
+        case 8: launch_rows<T, NORM, DROP, 8>(a, chunks, s); break;
+        case 16: launch_rows<T, NORM, DROP, 16>(a, chunks, s); break;
+        case 32: launch_rows<T, NORM, DROP, 32>(a, chunks, s); break;
+        case 64: launch_rows<T, NORM, DROP, 64>(a, chunks, s); break;
+        case 128: launch_rows<T, NORM, DROP, 128>(a, chunks, s); break;
+        case 256: launch_rows<T, NORM, DROP, 256>(a, chunks, s); break;
+        case 512: launch_rows<T, NORM, DROP, 512>(a, chunks, s); break;
+        default: launch_rows<T, NORM, DROP, 1024>(a, chunks, s); break;
+        }
+    } else if (c.rows) {
         chunks = wide_chunks(c.rows, c.cols);
         a.rows_per_chunk = (c.rows + chunks - 1) / chunks;
         chunks = (c.rows + a.rows_per_chunk - 1) / a.rows_per_chunk;
@@ -221,6 +434,8 @@ int run_bwd(const BwdCall& c, hipStream_t s)
         const uint64_t strips = (c.cols + kStrip - 1) / kStrip;
         hipLaunchKernelGGL((strips_kernel<T, NORM, DROP>), dim3(uint32_t(strips), uint32_t(chunks)), dim3(kWideBlock),
                            0, s, a);
+    }
+    if (c.rows) {
         const int rc = launch_status();
         if (rc)
             return rc;
@@ -228,7 +443,7 @@ int run_bwd(const BwdCall& c, hipStream_t s)
     if (!c.dw && !c.db && !c.dbias)
         return ZERO_OK;
     const SumOut out{{c.dw, c.db, c.dbias}, c.grad_dtype == ZERO_F32, c.accumulate};
-    hipLaunchKernelGGL(fold_kernel<T>, dim3(uint32_t((c.cols + kFoldBlock - 1) / kFoldBlock), 3), dim3(kFoldBlock), 0, s,
+    hipLaunchKernelGGL(fold_kernel<T>, dim3(uint32_t((c.cols + kFoldCols - 1) / kFoldCols), 3), dim3(kFoldBlock), 0, s,
                        out, a.partials, uint32_t(chunks), uint32_t(c.cols));
     return launch_status();
 }

@@ -16,6 +16,7 @@ import os
 import subprocess
 import sys
 import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -54,22 +55,27 @@ def host_cxx() -> str:
 
 
 def build(verbose: bool = False, extra_flags=()) -> str:
-    """Compile every source into the in-tree shared library (always rebuilds)."""
+    """Compile every source into the in-tree shared library (always rebuilds),
+    the sources side by side."""
     tmp = LIB + ".tmp"
-    with tempfile.TemporaryDirectory() as objdir:
-        objs = []
-        for src in HOST_SOURCES:
-            obj = os.path.join(objdir, os.path.splitext(src)[0] + ".o")
-            cmd = [host_cxx(), *HOST_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-c", os.path.join(CSRC, src), "-o", obj]
-            if verbose:
-                print(" ".join(cmd), flush=True)
-            subprocess.run(cmd, check=True)
-            objs.append(obj)
-        cmd = [hipcc(), *HIPCC_FLAGS, *extra_flags, f"-I{INCLUDE}", f"-I{CSRC}", "-o", tmp,
-               *[os.path.join(CSRC, s) for s in SOURCES], "-x", "none", *objs, "-lpthread"]
+    common = [f"-I{INCLUDE}", f"-I{CSRC}"]
+
+    def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
+
+    with tempfile.TemporaryDirectory() as objdir:
+        obj = lambda src: os.path.join(objdir, os.path.splitext(src)[0] + ".o")
+        compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+        cmds = [[hipcc(), *compile_flags, *extra_flags, *common, "-c", os.path.join(CSRC, src), "-o", obj(src)]
+                for src in SOURCES]
+        cmds += [[host_cxx(), *HOST_FLAGS, *common, "-c", os.path.join(CSRC, src), "-o", obj(src)]
+                 for src in HOST_SOURCES]
+        with ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as pool:
+            list(pool.map(run, cmds))
+        run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp,
+             *[obj(src) for src in SOURCES + HOST_SOURCES], "-lpthread"])
     os.replace(tmp, LIB)
     return LIB
 

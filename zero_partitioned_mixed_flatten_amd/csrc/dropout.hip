@@ -43,11 +43,17 @@ struct DropoutArgs {
 constexpr int kDropBlock = 256;
 
 // out = residual + D(x + bias), one group of 8 elements per thread: every
-// element is read once and written once, and the pass is bound by HBM.
-template <typename T>
+// element is read once and written once, and the pass is bound by HBM.  The
+// loads come first, without a branch, so that they are in flight together.
+// NARROW: rows of fewer than 8 columns, loaded by elements.
+template <typename T, int HINT, bool NARROW>
 __global__ __launch_bounds__(kDropBlock) void dropout_kernel(DropoutArgs<T> a)
 {
+    typedef typename Raw<T>::type V;
     const RngKey key = rng_key(a.drop);
+    const bool ragged = a.cols % 8 != 0;
+    const float one = opaque_one();
+    const uint32_t groups = uint32_t(a.groups);
     const uint64_t total = a.rows * a.groups, stride = uint64_t(gridDim.x) * kDropBlock;
     for (uint64_t base = uint64_t(blockIdx.x) * kDropBlock; base < total; base += stride) {
         const uint64_t g = base + threadIdx.x;
@@ -55,19 +61,40 @@ __global__ __launch_bounds__(kDropBlock) void dropout_kernel(DropoutArgs<T> a)
             return;
         // the workgroup's first row and column by one scalar division, the
         // thread's from there in 32 bits
-        const uint64_t row0 = base / a.groups;
-        uint32_t c = uint32_t(base - row0 * a.groups) + threadIdx.x;
-        const uint32_t wrap = c / uint32_t(a.groups);
-        const uint64_t row = row0 + wrap;
-        const uint32_t col = (c - wrap * uint32_t(a.groups)) * 8;
-        const int k = int(a.cols - col);
-        f32x8 v = widen<T>(load8(a.x + row * a.ld_x + col, k));
+        uint64_t row = base / a.groups;
+        uint32_t c = uint32_t(base - row * a.groups) + threadIdx.x;
+        if (groups >= kDropBlock) {                // at most one row's end among the workgroup's threads
+            const bool wrap = c >= groups;
+            row += wrap;
+            c -= wrap ? groups : 0;
+        } else {
+            const uint32_t wrap = c / groups;
+            row += wrap;
+            c -= wrap * groups;
+        }
+        const Group at = NARROW ? Group{0, 0, int(a.cols)} : group_at(c * 8, a.cols);
+        V x, res;
+        if (NARROW) {
+            x = load8(a.x + row * a.ld_x, at.k);
+            if (a.residual)
+                res = load8(a.residual + row * a.ld_res, at.k);
+        } else {
+            x = load8_full<HINT>(a.x + row * a.ld_x + at.at);
+            if (a.residual)
+                res = load8_full<HINT>(a.residual + row * a.ld_res + at.at);
+        }
+        f32x8 v = splat(-0.0f);                    // x + -0 is x, -0 too
         if (a.bias)
-            v = v + load8_vector<T>(a.bias, a.bias_f32, col, k, 0.0f);
-        v = dropped(v, a.drop, key, g);
+            v = load8_vector<T>(a.bias, a.bias_f32, c * 8, at.k, -0.0f);
+        if (!NARROW && ragged) {
+            x = settle<T>(x, at.shift, true);
+            if (a.residual)
+                res = settle<T>(res, at.shift, true);
+        }
+        v = dropped(raw_plus<T>(x, v, one), a.drop, key, g);
         if (a.residual)
-            v = widen<T>(load8(a.residual + row * a.ld_res + col, k)) + v;
-        store8(a.out + row * a.ld_out + col, narrow<T>(v), k);
+            v = raw_plus<T>(res, v, one);
+        store8<HINT>(a.out + row * a.ld_out + c * 8, narrow<T>(v), at.k);
     }
 }
 
@@ -80,7 +107,13 @@ int launch(void* out, uint64_t ld_out, const void* x, uint64_t ld_x, const void*
     uint64_t grid = (a.rows * a.groups + kDropBlock - 1) / kDropBlock;
     if (grid > (1u << 22))
         grid = 1u << 22;
-    hipLaunchKernelGGL(dropout_kernel<T>, dim3(uint32_t(grid)), dim3(kDropBlock), 0, s, a);
+    const uint64_t bytes = rows * cols * sizeof(T) * (residual ? 3 : 2);
+    if (cols < 8)
+        hipLaunchKernelGGL((dropout_kernel<T, kCached, true>), dim3(uint32_t(grid)), dim3(kDropBlock), 0, s, a);
+    else if (bytes <= kStreamBytes)
+        hipLaunchKernelGGL((dropout_kernel<T, kCached, false>), dim3(uint32_t(grid)), dim3(kDropBlock), 0, s, a);
+    else
+        hipLaunchKernelGGL((dropout_kernel<T, kStreamed, false>), dim3(uint32_t(grid)), dim3(kDropBlock), 0, s, a);
     return launch_status();
 }
 

@@ -20,7 +20,17 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 // group is loaded and stored with 16-byte instructions whatever its address:
 // the declared alignment is the element's, which the target's unaligned
 // global access serves in one instruction (rows of an odd width start
-// anywhere).  Only a row's last group, when it is short, goes by elements.
+// anywhere).
+
+// Cache hints of a pass: bit 0, loads nontemporal; bit 1, stores.  Stores
+// always are; loads only in a call that moves more than kStreamBytes: what a
+// smaller one reads, the operator before it has mostly left in the 256 MB
+// cache, while a larger one runs a little better past it.  Measured, plain
+// against nontemporal loads: layer norm forward 1600 x 8192 fp16 (52 MB) 11.0
+// and 13.3 us, backward 800 x 8192 (39 MB) 17.4 and 22.6 us, joined forward
+// 1600 x 8192 (105 MB) 23.7 and 22.7 us, 16384 x 8192 (1.07 GB) 203 and 183 us.
+constexpr int kCached = 2, kStreamed = 3;
+constexpr uint64_t kStreamBytes = 96000000;
 
 template <typename T>
 struct Raw;                                        // 8 elements as loaded
@@ -37,15 +47,23 @@ struct Raw<float> {
     typedef f32x8 type;
 };
 
+template <int HINT = kStreamed, typename T>
+__device__ __forceinline__ typename Raw<T>::type load8_full(const T* p)
+{
+    typedef typename Raw<T>::type V;
+    typedef V __attribute__((aligned(sizeof(T)))) VU;
+    if (HINT & 1)
+        return __builtin_nontemporal_load(reinterpret_cast<const VU*>(p));
+    return *reinterpret_cast<const VU*>(p);
+}
+
 // The first k elements of a group (k <= 0: none), the others 0.
 template <typename T>
 __device__ __forceinline__ typename Raw<T>::type load8(const T* p, int k)
 {
-    typedef typename Raw<T>::type V;
-    typedef V __attribute__((aligned(sizeof(T)))) VU;
     if (k >= 8)
-        return __builtin_nontemporal_load(reinterpret_cast<const VU*>(p));
-    V v;
+        return load8_full<kStreamed>(p);
+    typename Raw<T>::type v;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         v[j] = T(0.0f);
@@ -57,18 +75,74 @@ __device__ __forceinline__ typename Raw<T>::type load8(const T* p, int k)
     return v;
 }
 
-template <typename T>
+template <int HINT = kStreamed, typename T>
 __device__ __forceinline__ void store8(T* p, typename Raw<T>::type v, int k)
 {
     typedef typename Raw<T>::type V;
     typedef V __attribute__((aligned(sizeof(T)))) VU;
-    if (k >= 8)
+    if (k >= 8 && (HINT & 2))
         __builtin_nontemporal_store(v, reinterpret_cast<VU*>(p));
+    else if (k >= 8)
+        *reinterpret_cast<VU*>(p) = v;
     else if (k > 0)
 #pragma unroll
         for (int j = 0; j < 7; ++j)
             if (j < k)
                 p[j] = v[j];
+}
+
+// A thread's group of a row of at least 8 columns, loaded without a branch:
+// a branch around a load makes the next load wait for it.  A group past the
+// row's last 8 columns reads those 8 instead (memory of the row), and
+// settle() moves the elements to their places and puts 0 in the others.
+struct Group {
+    uint32_t at;                                   // first column loaded
+    uint32_t shift;                                // the group's column - at; 8 and more: no columns in the row
+    int k;                                         // columns in the row: 8, less in the last group, <= 0 past it
+};
+
+__device__ __forceinline__ Group group_at(uint32_t col, uint32_t cols)
+{
+    const uint32_t at = col < cols - 8 ? col : cols - 8;
+    return Group{at, col - at, int(cols) - int(col)};
+}
+
+template <int WORDS, int BITS>
+__device__ __forceinline__ void shift_down(uint32_t (&d)[WORDS], uint32_t shift)
+{
+#pragma unroll
+    for (int bit = 2; bit >= 0; --bit) {
+        const bool on = (shift >> bit) & 1;
+        const int words = (1 << bit) * BITS / 32;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            uint32_t moved;
+            if (words)
+                moved = i + words < WORDS ? d[i + words < WORDS ? i + words : 0] : 0;
+            else
+                moved = (d[i] >> 16) | (i + 1 < WORDS ? d[i + 1 < WORDS ? i + 1 : 0] << 16 : 0);
+            d[i] = on ? moved : d[i];
+        }
+    }
+}
+
+// `ragged`: cols is not a multiple of 8 (the same for every thread).  ZERO
+// false: groups with no columns in the row may keep what was loaded.
+template <typename T, bool ZERO = true>
+__device__ __forceinline__ typename Raw<T>::type settle(typename Raw<T>::type v, uint32_t shift, bool ragged)
+{
+    constexpr int kWords = 2 * int(sizeof(T));
+    struct Words {
+        uint32_t d[kWords];
+    };
+    Words x = __builtin_bit_cast(Words, v);
+    if (ragged)
+        shift_down<kWords, 8 * int(sizeof(T))>(x.d, shift);
+    if (ZERO)
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            x.d[i] = shift < 8 ? x.d[i] : 0;
+    return __builtin_bit_cast(typename Raw<T>::type, x);
 }
 
 // 8 sums into a partial's row, which the fold reads back soon: kept in the caches.
@@ -89,6 +163,38 @@ __device__ __forceinline__ f32x8 widen(typename Raw<T>::type v)
 {
     return __builtin_convertvector(v, f32x8);
 }
+
+// raw * a + b and raw + b, elementwise, rounded once.  binary16 elements are
+// widened inside the instruction (v_fma_mix_f32), which the compiler forms
+// only for a product: `one` is a 1 that it cannot see.
+__device__ __forceinline__ float opaque_one()
+{
+    float one = 1.0f;
+    asm("" : "+s"(one));
+    return one;
+}
+
+template <typename T>
+__device__ __forceinline__ f32x8 raw_plus(typename Raw<T>::type raw, f32x8 b, float one)
+{
+    f32x8 v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = __is_same(T, _Float16) ? __builtin_fmaf(float(raw[j]), one, b[j]) : float(raw[j]) + b[j];
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ f32x8 raw_times(typename Raw<T>::type raw, float a)
+{
+    f32x8 v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = __is_same(T, _Float16) ? __builtin_fmaf(float(raw[j]), a, -0.0f) : float(raw[j]) * a;
+    return v;
+}
+
+__device__ __forceinline__ f32x8 splat(float x) { return f32x8{x, x, x, x, x, x, x, x}; }
 
 template <typename T>
 __device__ __forceinline__ typename Raw<T>::type narrow(f32x8 v)   // round to nearest even
@@ -142,7 +248,7 @@ __device__ __forceinline__ f32x8 load8_vector(const void* p, bool f32, uint64_t 
 struct Drop {
     const zero_rng_t* rng;
     uint32_t site;
-    uint32_t threshold;                            // dropped when the 16-bit word is below it; 0: nothing is
+    uint32_t threshold;                            // dropped when the 16-bit word is below it; 0: nothing is, 65536: all
     float scale;                                   // 65536 / (65536 - threshold), rounded once; 0 when all is dropped
 };
 
@@ -165,8 +271,8 @@ __device__ __forceinline__ u32x4 philox(RngKey key, uint32_t site, uint64_t grou
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t a = uint64_t(0xD2511F53u) * c0, b = uint64_t(0xCD9E8D57u) * c2;
-        c0 = uint32_t(b >> 32) ^ c1 ^ k0;
-        c2 = uint32_t(a >> 32) ^ c3 ^ k1;
+        c0 = __builtin_amdgcn_bitop3_b32(uint32_t(b >> 32), c1, k0, 0x96);   // the exclusive or of the three
+        c2 = __builtin_amdgcn_bitop3_b32(uint32_t(a >> 32), c3, k1, 0x96);
         c1 = uint32_t(b);
         c3 = uint32_t(a);
         k0 += 0x9E3779B9u;
@@ -176,28 +282,35 @@ __device__ __forceinline__ u32x4 philox(RngKey key, uint32_t site, uint64_t grou
 }
 
 // D(v): a dropped element is 0 whatever it holds (a select, not a product, so
-// an inf or NaN there does not come through).
+// an inf or NaN there does not come through).  The 16-bit words are compared
+// in the upper half of a register: the odd ones as they are, what is below
+// them does not change the order.
 __device__ __forceinline__ f32x8 dropped(f32x8 v, const Drop& d, RngKey key, uint64_t group)
 {
     if (!d.threshold)
         return v;
+    if (d.threshold > 0xffffu)
+        return splat(0.0f);
     const u32x4 bits = philox(key, d.site, group);
+    const uint32_t limit = d.threshold << 16;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const uint32_t word = (bits[j >> 1] >> (16 * (j & 1))) & 0xffffu;
-        v[j] = word >= d.threshold ? v[j] * d.scale : 0.0f;
+        const uint32_t word = j & 1 ? bits[j >> 1] : bits[j >> 1] << 16;
+        v[j] = word >= limit ? v[j] * d.scale : 0.0f;
     }
     return v;
 }
 
 // ---- sums over the threads of a row ------------------------------------------------------
 // A row is shared by TPR threads.  Within a wave the sum goes through lane
-// permutes of the vector ALU (DPP), each step a pairwise addition that both
-// lanes do alike, so every thread of the row ends with the same bits.
-template <int CTRL>
+// permutes of the vector ALU (DPP): up to 16 lanes by pairwise additions that
+// both lanes do alike, then by adding up the rows of 16; every thread of the
+// row ends with the same bits.
+// ROWS: the rows of 16 lanes that take part, the others get 0.
+template <int CTRL, int ROWS = 0xf>
 __device__ __forceinline__ float dpp(float v)
 {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, ROWS == 0xf));
 }
 
 template <int LANES>
@@ -208,11 +321,23 @@ __device__ __forceinline__ float lanes_sum(float v)
     v += dpp<0x141>(v);                            // row_half_mirror: the other quad of 8
     if (LANES >= 16)
         v += dpp<0x140>(v);                        // row_mirror: the other 8 of 16
-    if (LANES >= 32)
+    if (LANES == 32)
         v += __shfl_xor(v, 16);
-    if (LANES >= 64)
-        v += __shfl_xor(v, 32);
+    if (LANES >= 64) {                             // rows of 16 lanes: 1 += 0 and 3 += 2, then 3 += 1; lane 63 has it all
+        v += dpp<0x142, 0xa>(v);                   // row_bcast 15
+        v += dpp<0x143, 0xc>(v);                   // row_bcast 31
+        v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+    }
     return v;
+}
+
+// s / n for a whole number n and inv = fp32(1 / n): the product corrected by
+// its remainder, which gives the rounded quotient at 5 instructions (an inf or
+// NaN stays what the product makes of it).
+__device__ __forceinline__ float over(float s, float n, float inv)
+{
+    const float q = s * inv, rest = __builtin_fmaf(-q, n, s);
+    return rest == rest ? __builtin_fmaf(rest, inv, q) : q;
 }
 
 // The sums of N values over the TPR threads of each row of the workgroup, in
@@ -237,14 +362,13 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* scratch, uint32_t&
         for (int i = 0; i < N; ++i)
             buf[i * kWaves + wave] = v[i];
     __syncthreads();
-    const uint32_t first = wave / kPerRow * kPerRow;
+    // each wave adds up its row's waves in its first 8 or 16 lanes' order
+    constexpr int kLanes = kPerRow <= 8 ? 8 : 16;
+    const uint32_t j = threadIdx.x % kLanes, first = wave / kPerRow * kPerRow;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kPerRow; ++j)
-            s += buf[i * kWaves + first + j];
-        v[i] = s;
+        const float part = buf[i * kWaves + first + (j < kPerRow ? j : 0)];
+        v[i] = lanes_sum<kLanes>(j < kPerRow ? part : 0.0f);
     }
 }
 

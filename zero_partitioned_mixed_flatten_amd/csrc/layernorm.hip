@@ -36,8 +36,10 @@ struct FwdArgs {
 };
 
 // Rows that fit the registers of TPR threads, VPT groups of 8 columns each:
-// one pass over memory, the row kept as it was loaded.
-template <typename T, bool JOIN, int BLOCK, int TPR, int VPT>
+// one pass over memory, the row kept as it was loaded.  A persistent workgroup
+// takes every gridDim.x-th block of BLOCK / TPR rows, the next rows' loads in
+// flight while it works on the present ones, w, b and bias in registers.
+template <typename T, bool JOIN, int BLOCK, int TPR, int VPT, int HINT>
 __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
 {
     typedef typename Raw<T>::type V;
@@ -46,83 +48,101 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
     uint32_t parity = 0;
     const RngKey key = rng_key(a.drop);
     const uint32_t groups = (a.cols + 7) / 8;
-    const float n = float(a.cols);
+    const bool ragged = a.cols % 8 != 0;
+    const float n = float(a.cols), inv = 1.0f / n, one = opaque_one();
     uint32_t slot = threadIdx.x / TPR;
     if (TPR >= 64)
         slot = __builtin_amdgcn_readfirstlane(slot);
     const uint32_t t = threadIdx.x % TPR;
-    for (uint64_t first = uint64_t(blockIdx.x) * kRows; first < a.rows; first += uint64_t(gridDim.x) * kRows) {
+
+    Group at[VPT];
+    f32x8 w[VPT], b[VPT], bias[VPT];
+    struct Row {
+        V x[VPT], res[VPT];
+    };
+    auto fetch = [&](uint64_t row, Row& f) {
+        row = row < a.rows ? row : a.rows - 1;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            f.x[i] = load8_full<HINT>(a.x + row * a.ld_x + at[i].at);
+            if (JOIN && a.residual)
+                f.res[i] = load8_full<HINT>(a.residual + row * a.ld_res + at[i].at);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        at[i] = group_at((i * TPR + t) * 8, a.cols);
+    const uint64_t stride = uint64_t(gridDim.x) * kRows;
+    uint64_t first = uint64_t(blockIdx.x) * kRows;
+    Row cur, next;
+    fetch(first + slot, cur);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const uint32_t col = (i * TPR + t) * 8;
+        w[i] = load8_vector<T>(a.w, a.vec_f32, col, at[i].k, 1.0f);
+        b[i] = load8_vector<T>(a.b, a.vec_f32, col, at[i].k, 0.0f);
+        if (JOIN)
+            bias[i] = load8_vector<T>(a.bias, a.vec_f32, col, at[i].k, -0.0f);   // x + -0 is x, -0 too
+    }
+    for (; first < a.rows; first += stride) {
         const uint64_t row = first + slot;
+        if (first + stride < a.rows)
+            fetch(row + stride, next);
         const bool live = row < a.rows;
-        V raw[VPT];
-        f32x8 w[VPT], b[VPT];
+        V raw[VPT];                                // 0 past the row's end, the sum needs no test
+        f32x8 x[VPT];
         float s[1] = {0.0f}, q[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint32_t g = i * TPR + t, col = g * 8;
-            const int k = live ? int(a.cols) - int(col) : 0;
-            raw[i] = load8(a.x + row * a.ld_x + col, k);
+            raw[i] = settle<T>(cur.x[i], at[i].shift, ragged);
             if (JOIN) {
-                V res;
+                f32x8 v = raw_plus<T>(raw[i], bias[i], one);
+                v = dropped(v, a.drop, key, row * groups + (i * TPR + t));
                 if (a.residual)
-                    res = load8(a.residual + row * a.ld_res + col, k);
-                f32x8 v = widen<T>(raw[i]);
-                if (a.bias)
-                    v = v + load8_vector<T>(a.bias, a.vec_f32, col, k, 0.0f);
-                v = dropped(v, a.drop, key, row * groups + g);
-                if (a.residual)
-                    v = widen<T>(res) + v;
+                    v = raw_plus<T>(settle<T>(cur.res[i], at[i].shift, ragged), v, one);
                 raw[i] = narrow<T>(v);
+                store8<HINT>(a.r + row * a.ld_r + (i * TPR + t) * 8, raw[i], live ? at[i].k : 0);
             }
-        }
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const uint32_t col = (i * TPR + t) * 8;
-            const int k = live ? int(a.cols) - int(col) : 0;
-            w[i] = load8_vector<T>(a.w, a.vec_f32, col, k, 1.0f);
-            b[i] = load8_vector<T>(a.b, a.vec_f32, col, k, 0.0f);
-            if (JOIN)
-                store8(a.r + row * a.ld_r + col, raw[i], k);
-            f32x8 v = widen<T>(raw[i]);
-            if (k < 8)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] = j < k ? v[j] : 0.0f;
+            const f32x8 v = widen<T>(raw[i]);
             s[0] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
         }
         row_sum<BLOCK, TPR>(s, scratch, parity);
-        const float mean = s[0] / n;
+        const float mean = over(s[0], n, inv);
+        float qb = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int k = int(a.cols) - int((i * TPR + t) * 8);
-            f32x8 v = widen<T>(raw[i]) - mean;
-            if (k < 8)
+            x[i] = raw_plus<T>(raw[i], splat(-mean), one);
+            if (at[i].k < 8)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    v[j] = j < k ? v[j] : 0.0f;
-            v = v * v;
-            q[0] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+                    x[i][j] = j < at[i].k ? x[i][j] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                q[0] = __builtin_fmaf(x[i][j], x[i][j], q[0]);
+                qb = __builtin_fmaf(x[i][j + 1], x[i][j + 1], qb);
+            }
         }
+        q[0] += qb;
         row_sum<BLOCK, TPR>(q, scratch, parity);
-        const float rstd = 1.0f / sqrtf(q[0] / n + a.eps);
+        const float rstd = 1.0f / sqrtf(over(q[0], n, inv) + a.eps);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint32_t col = (i * TPR + t) * 8;
-            const int k = live ? int(a.cols) - int(col) : 0;
-            f32x8 v = widen<T>(raw[i]);
+            f32x8 v;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[j] = __builtin_fmaf((v[j] - mean) * rstd, w[i][j], b[i][j]);
-            store8(a.y + row * a.ld_y + col, narrow<T>(v), k);
+                v[j] = __builtin_fmaf(x[i][j] * rstd, w[i][j], b[i][j]);
+            store8<HINT>(a.y + row * a.ld_y + (i * TPR + t) * 8, narrow<T>(v), live ? at[i].k : 0);
         }
         if (t == 0 && live) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
+        cur = next;
     }
 }
 
-// Any width: a workgroup takes a row and goes over it three times.
+// Any width (and fewer than 8 columns): a workgroup takes a row and goes over
+// it three times.
 constexpr int kWideBlock = 256;
 
 template <typename T, bool JOIN>
@@ -189,32 +209,63 @@ __global__ __launch_bounds__(kWideBlock) void norm_fwd_wide_kernel(FwdArgs<T> a)
     }
 }
 
+// The threads of a row: as few powers of two as hold its groups one each up to
+// a wave; wider rows take two groups a thread and whole waves, at least two.
+// The workgroup is one row, or as many as make 256 threads.  Grid: 1024
+// resident threads a CU with two groups each, 1536 with one, and no more
+// workgroups than blocks of rows.  Measured at 13.1 M fp16 elements (layer
+// norm / joined, us; two copies of the same bytes take 10.6 / 21.1): 512
+// columns 12.8 / 22.7, 64 threads x 1, against 13.1 / 23.6 with 32 x 2; 1600
+// columns 13.7 / 24.2, 128 x 2, against 14.6 / 25.6 with 256 x 1 and 14.9 /
+// 29.2 with 64 x 4; 8192 columns 13.1 / 23.8, 512 x 2, against 14.5 / 27.0
+// with 1024 x 1 and 15.1 / 26.8 with 256 x 4.  Grid, 512 columns: 13.2 / 23.0
+// with 1024 threads a CU, 12.6 / 24.8 with 2048; 1600 columns: 15.4 / 26.4 with
+// 1536, 16.6 / 28.9 with 512.
+constexpr uint64_t kCus = 256;
+
 template <typename T, bool JOIN, int TPR, int VPT>
 int launch_rows(const FwdArgs<T>& a, hipStream_t s)
 {
-    constexpr int kBlock = TPR < 256 ? 256 : TPR;
+    constexpr int kBlock = TPR < 192 ? 256 : TPR;
+    constexpr uint64_t kMost = kCus * (VPT == 1 ? 1536 : 1024) / kBlock;
     uint64_t grid = (a.rows + kBlock / TPR - 1) / (kBlock / TPR);
-    if (grid > (1u << 20))
-        grid = 1u << 20;
-    hipLaunchKernelGGL((norm_fwd_kernel<T, JOIN, kBlock, TPR, VPT>), dim3(uint32_t(grid)), dim3(kBlock), 0, s, a);
+    if (grid > kMost)
+        grid = kMost;
+    const uint64_t bytes = a.rows * a.cols * sizeof(T) * (JOIN ? (a.residual ? 4 : 3) : 2);
+    if (bytes <= kStreamBytes)
+        hipLaunchKernelGGL((norm_fwd_kernel<T, JOIN, kBlock, TPR, VPT, kCached>), dim3(uint32_t(grid)), dim3(kBlock), 0, s,
+                           a);
+    else
+        hipLaunchKernelGGL((norm_fwd_kernel<T, JOIN, kBlock, TPR, VPT, kStreamed>), dim3(uint32_t(grid)), dim3(kBlock), 0,
+                           s, a);
     return launch_status();
 }
 
 template <typename T, bool JOIN>
 int launch_fwd(const FwdArgs<T>& a, hipStream_t s)
 {
+    if (a.cols < 8 || a.cols > 16384) {
+        const uint64_t grid = a.rows < (1u << 20) ? a.rows : (1u << 20);
+        hipLaunchKernelGGL((norm_fwd_wide_kernel<T, JOIN>), dim3(uint32_t(grid)), dim3(kWideBlock), 0, s, a);
+        return launch_status();
+    }
     if (a.cols <= 64) return launch_rows<T, JOIN, 8, 1>(a, s);
     if (a.cols <= 128) return launch_rows<T, JOIN, 16, 1>(a, s);
     if (a.cols <= 256) return launch_rows<T, JOIN, 32, 1>(a, s);
     if (a.cols <= 512) return launch_rows<T, JOIN, 64, 1>(a, s);
-    if (a.cols <= 1024) return launch_rows<T, JOIN, 128, 1>(a, s);
-    if (a.cols <= 2048) return launch_rows<T, JOIN, 256, 1>(a, s);
-    if (a.cols <= 4096) return launch_rows<T, JOIN, 512, 1>(a, s);
-    if (a.cols <= 8192) return launch_rows<T, JOIN, 512, 2>(a, s);
-    if (a.cols <= 16384) return launch_rows<T, JOIN, 1024, 2>(a, s);
-    const uint64_t grid = a.rows < (1u << 20) ? a.rows : (1u << 20);
-    hipLaunchKernelGGL((norm_fwd_wide_kernel<T, JOIN>), dim3(uint32_t(grid)), dim3(kWideBlock), 0, s, a);
-    return launch_status();
+    if (a.cols <= 1024) return launch_rows<T, JOIN, 64, 2>(a, s);
+    switch ((a.cols + 1023) / 1024) {              // whole waves of 1024 columns
+    case 2: return launch_rows<T, JOIN, 128, 2>(a, s);
+    case 3: return launch_rows<T, JOIN, 192, 2>(a, s);
+    case 4: return launch_rows<T, JOIN, 256, 2>(a, s);
+    case 5: return launch_rows<T, JOIN, 320, 2>(a, s);
+    case 6: return launch_rows<T, JOIN, 384, 2>(a, s);
+    case 7: return launch_rows<T, JOIN, 448, 2>(a, s);
+    case 8: return launch_rows<T, JOIN, 512, 2>(a, s);
+    case 9: case 10: return launch_rows<T, JOIN, 640, 2>(a, s);
+    case 11: case 12: return launch_rows<T, JOIN, 768, 2>(a, s);
+    default: return launch_rows<T, JOIN, 1024, 2>(a, s);
+    }
 }
 
 struct FwdCall {

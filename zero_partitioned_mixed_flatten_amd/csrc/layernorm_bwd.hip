@@ -40,7 +40,7 @@ struct BwdArgs {
 // BLOCK / TPR rows, the next rows' loads in flight while it works on the
 // present ones, and keeps its columns' sums in registers to the end, where
 // it stores one partial.
-template <typename T, bool NORM, bool DROP, int BLOCK, int TPR, int VPT>
+template <typename T, bool NORM, bool DROP, int BLOCK, int TPR, int VPT, int NBUF, int HINT>
 __global__ __launch_bounds__(BLOCK) void rows_bwd_kernel(BwdArgs<T> a)
 {
     typedef typename Raw<T>::type V;
@@ -50,96 +50,121 @@ __global__ __launch_bounds__(BLOCK) void rows_bwd_kernel(BwdArgs<T> a)
     uint32_t parity = 0;
     const RngKey key = rng_key(a.drop);
     const uint32_t groups = (a.cols + 7) / 8;
-    const float n = float(a.cols);
+    const bool ragged = a.cols % 8 != 0;
+    const float n = float(a.cols), inv = 1.0f / n, one = opaque_one();
     uint32_t slot = threadIdx.x / TPR;
     if (TPR >= 64)
         slot = __builtin_amdgcn_readfirstlane(slot);
     const uint32_t t = threadIdx.x % TPR;
 
+    Group at[VPT];
     f32x8 w[VPT], sum[kSums][VPT];
+    struct Row {
+        V dy[VPT], r[VPT], dres[VPT];
+        float mean, rstd;
+    };
+    auto fetch = [&](uint64_t row, Row& f) {
+        row = row < a.rows ? row : a.rows - 1;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            f.dy[i] = load8_full<HINT>(a.dy + row * a.ld_dy + at[i].at);
+            if (NORM) {
+                f.r[i] = load8_full<HINT>(a.r + row * a.ld_r + at[i].at);
+                if (a.dres)
+                    f.dres[i] = load8_full<HINT>(a.dres + row * a.ld_dres + at[i].at);
+            }
+        }
+        if (NORM) {
+            f.mean = a.mean[row];
+            f.rstd = a.rstd[row];
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        at[i] = group_at((i * TPR + t) * 8, a.cols);
+    const uint64_t stride = uint64_t(gridDim.x) * kRows;
+    uint64_t first = uint64_t(blockIdx.x) * kRows;
+    Row buf[NBUF];
+#pragma unroll
+    for (int i = 0; i < NBUF - 1; ++i)
+        fetch(first + i * stride + slot, buf[i]);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const uint32_t col = (i * TPR + t) * 8;
         if (NORM)
-            w[i] = load8_vector<T>(a.w, a.vec_f32, col, int(a.cols) - int(col), 1.0f);
+            w[i] = load8_vector<T>(a.w, a.vec_f32, (i * TPR + t) * 8, at[i].k, 1.0f);
 #pragma unroll
         for (int q = 0; q < kSums; ++q)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 sum[q][i][j] = 0.0f;
     }
-
-    struct Row {
-        V dy[VPT], r[VPT], dres[VPT];
-        float mean, rstd;
-    };
-    auto fetch = [&](uint64_t row, Row& f) {
+    auto work = [&](uint64_t row, Row& cur) {
         const bool live = row < a.rows;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const uint32_t col = (i * TPR + t) * 8;
-            const int k = live ? int(a.cols) - int(col) : 0;
-            f.dy[i] = load8(a.dy + row * a.ld_dy + col, k);
-            if (NORM) {
-                f.r[i] = load8(a.r + row * a.ld_r + col, k);
-                if (a.dres)
-                    f.dres[i] = load8(a.dres + row * a.ld_dres + col, k);
-            }
-        }
-        f.mean = NORM && live ? a.mean[row] : 0.0f;
-        f.rstd = NORM && live ? a.rstd[row] : 0.0f;
-    };
-
-    const uint64_t stride = uint64_t(gridDim.x) * kRows;
-    uint64_t first = uint64_t(blockIdx.x) * kRows;
-    Row cur;
-    fetch(first + slot, cur);
-    for (; first < a.rows; first += stride) {
-        const uint64_t row = first + slot;
-        const bool live = row < a.rows;
-        Row next;
-        fetch(row + stride, next);
-
+        // with d = dy * rstd and x = r - mean: g rstd = d w, h rstd = x rstd^2
+        f32x8 x[VPT], g[VPT];
         float c[2] = {0.0f, 0.0f};
         if (NORM) {
+            float c0b = 0.0f, c1b = 0.0f;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const f32x8 dy = widen<T>(cur.dy[i]);
-                const f32x8 g = dy * w[i], h = (widen<T>(cur.r[i]) - cur.mean) * cur.rstd;
-                const f32x8 gh = g * h;            // dy is 0 past the row's end
-                c[0] += ((g[0] + g[1]) + (g[2] + g[3])) + ((g[4] + g[5]) + (g[6] + g[7]));
-                c[1] += ((gh[0] + gh[1]) + (gh[2] + gh[3])) + ((gh[4] + gh[5]) + (gh[6] + gh[7]));
+                cur.dy[i] = settle<T>(cur.dy[i], at[i].shift, ragged);   // 0 past the row's end
+                const f32x8 d = raw_times<T>(cur.dy[i], cur.rstd);
+                x[i] = raw_plus<T>(settle<T, false>(cur.r[i], at[i].shift, ragged), splat(-cur.mean), one);
+                g[i] = d * w[i];
+                if (live) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        sum[0][i][j] = __builtin_fmaf(d[j], x[i][j], sum[0][i][j]);
+                    sum[1][i] = raw_plus<T>(cur.dy[i], sum[1][i], one);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    c[0] += g[i][j];
+                    c0b += g[i][j + 1];
+                    c[1] = __builtin_fmaf(g[i][j], x[i][j], c[1]);
+                    c1b = __builtin_fmaf(g[i][j + 1], x[i][j + 1], c1b);
+                }
             }
+            c[0] += c0b;
+            c[1] += c1b;
             row_sum<BLOCK, TPR>(c, scratch, parity);
-            c[0] = c[0] / n;
-            c[1] = c[1] / n;
+            c[0] = -over(c[0], n, inv);
+            c[1] = -(over(c[1], n, inv) * cur.rstd * cur.rstd);
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const uint32_t g8 = i * TPR + t, col = g8 * 8;
-            const int k = live ? int(a.cols) - int(col) : 0;
-            f32x8 e = widen<T>(cur.dy[i]);
+            const int k = live ? at[i].k : 0;
+            f32x8 e;
             if (NORM) {
-                const f32x8 dy = e, h = (widen<T>(cur.r[i]) - cur.mean) * cur.rstd;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    sum[0][i][j] = __builtin_fmaf(dy[j], h[j], sum[0][i][j]);
-                    sum[1][i][j] += dy[j];
-                    e[j] = cur.rstd * __builtin_fmaf(-h[j], c[1], dy[j] * w[i][j] - c[0]);
-                }
+                for (int j = 0; j < 8; ++j)
+                    e[j] = __builtin_fmaf(x[i][j], c[1], g[i][j] + c[0]);
                 if (a.dres)
-                    e = e + widen<T>(cur.dres[i]);
+                    e = raw_plus<T>(settle<T, false>(cur.dres[i], at[i].shift, ragged), e, one);
+            } else {
+                e = widen<T>(settle<T>(cur.dy[i], at[i].shift, ragged));
             }
             if (DROP) {
                 if (NORM)
-                    store8(a.dr + row * a.ld_dr + col, narrow<T>(e), k);
+                    store8<HINT>(a.dr + row * a.ld_dr + col, narrow<T>(e), k);
                 e = dropped(e, a.drop, key, row * groups + g8);
-                if (k > 0)
+                if (live)
                     sum[kSums - 1][i] = sum[kSums - 1][i] + e;
             }
-            store8(a.dx + row * a.ld_dx + col, narrow<T>(e), k);
+            store8<HINT>(a.dx + row * a.ld_dx + col, narrow<T>(e), k);
         }
-        cur = next;
+    };
+    for (bool more = true; more;) {
+#pragma unroll
+        for (int i = 0; i < NBUF; ++i) {           // the buffers in turn: a copy would wait for its loads
+            if (more) {
+                fetch(first + (NBUF - 1) * stride + slot, buf[(i + NBUF - 1) % NBUF]);
+                work(first + slot, buf[i]);
+                first += stride;
+                more = first < a.rows;
+            }
+        }
     }
 
     // one partial of the workgroup: the upper half of its rows' threads hands
@@ -349,10 +374,17 @@ struct BwdCall {
     size_t workspace_bytes;
 };
 
-// Widest row of the one-pass kernel, and the workgroups it runs: one per CU,
-// fewer where there are fewer rows.
+// The one-pass kernel: rows up to 8192 columns, one workgroup of 1024 threads
+// a CU, one group of 8 columns a thread.  Every workgroup costs a partial
+// (written and read again: as much as 2.4 joined rows of fp16), so there are no
+// more than 256, and only 128 where 256 would get no more than 1.5 blocks of
+// rows each.  Measured (kernel and fold, us, fp16): joined 8192 x 1600, 256 x
+// 4 rows of 256 threads 33.4, 512 workgroups of 512 threads 34.7, 128 threads
+// with two groups each 44.0; joined 16384 x 8192, 1024 threads x 1 group 237,
+// 512 x 2 254.  Layer norm, 128 against 256 workgroups at most: 200 x 8192
+// 12.7 and 15.1, 400 x 8192 15.0 and 17.6, 1000 x 1600 9.2 and 9.7, 800 x 8192
+// 18.4 and 17.4, 2000 x 1600 11.7 and 11.0.
 constexpr uint64_t kRowsMaxCols = 8192;
-constexpr uint64_t kRowsGrid = 256;
 constexpr int kRowsBlock = 1024;
 
 uint64_t rows_tpr(uint64_t cols)
@@ -363,25 +395,37 @@ uint64_t rows_tpr(uint64_t cols)
     return tpr;
 }
 
+bool one_pass(uint64_t cols) { return cols >= 8 && cols <= kRowsMaxCols; }
+
 uint64_t rows_chunks(uint64_t rows, uint64_t cols)
 {
     const uint64_t per = kRowsBlock / rows_tpr(cols), blocks = (rows + per - 1) / per;
-    return blocks < kRowsGrid ? blocks : kRowsGrid;
+    const uint64_t most = blocks <= 400 ? 128 : 256;
+    return blocks < most ? blocks : most;
 }
 
-uint64_t row_sums_bytes(uint64_t rows, uint64_t cols) { return cols <= kRowsMaxCols ? 0 : (rows * 8 + 15) / 16 * 16; }
+uint64_t row_sums_bytes(uint64_t rows, uint64_t cols) { return one_pass(cols) ? 0 : (rows * 8 + 15) / 16 * 16; }
 
 uint64_t workspace_need(uint64_t rows, uint64_t cols)
 {
-    const uint64_t chunks = cols <= kRowsMaxCols ? rows_chunks(rows, cols) : wide_chunks(rows, cols);
+    const uint64_t chunks = one_pass(cols) ? rows_chunks(rows, cols) : wide_chunks(rows, cols);
     return row_sums_bytes(rows, cols) + chunks * 3 * cols * 4;
 }
 
+// Two rows in flight ahead of the present one where the registers hold them
+// (layer norm alone, 16-bit elements: 8192 x 1600 21.8 us against 22.1 with one,
+// 1600 x 8192 28.5 against 29.3), else one.
 template <typename T, bool NORM, bool DROP, int TPR>
 void launch_rows(const BwdArgs<T>& a, uint64_t chunks, hipStream_t s)
 {
-    hipLaunchKernelGGL((rows_bwd_kernel<T, NORM, DROP, kRowsBlock, TPR, 1>), dim3(uint32_t(chunks)), dim3(kRowsBlock), 0, s,
-                       a);
+    constexpr int kBuffers = DROP || sizeof(T) == 4 ? 2 : 3;
+    const uint64_t arrays = (NORM ? 3 + (a.dres != nullptr) : 2) + (NORM && DROP);
+    if (a.rows * a.cols * sizeof(T) * arrays <= kStreamBytes)
+        hipLaunchKernelGGL((rows_bwd_kernel<T, NORM, DROP, kRowsBlock, TPR, 1, kBuffers, kCached>), dim3(uint32_t(chunks)),
+                           dim3(kRowsBlock), 0, s, a);
+    else
+        hipLaunchKernelGGL((rows_bwd_kernel<T, NORM, DROP, kRowsBlock, TPR, 1, kBuffers, kStreamed>),
+                           dim3(uint32_t(chunks)), dim3(kRowsBlock), 0, s, a);
 }
 
 template <typename T, bool NORM, bool DROP>
@@ -411,7 +455,7 @@ int run_bwd(const BwdCall& c, hipStream_t s)
     a.want[1] = c.db;
     a.want[2] = c.dbias;
     uint64_t chunks = 0;
-    if (c.rows && c.cols <= kRowsMaxCols) {
+    if (c.rows && one_pass(c.cols)) {
         chunks = rows_chunks(c.rows, c.cols);
         switch (rows_tpr(c.cols)) {
         case 8: launch_rows<T, NORM, DROP, 8>(a, chunks, s); break;

@@ -42,59 +42,131 @@ struct DropoutArgs {
 
 constexpr int kDropBlock = 256;
 
+// A short last group of 16-bit elements, loaded from the row's last 8 columns.
+template <typename T>
+__device__ __forceinline__ typename Raw<T>::type settle16(typename Raw<T>::type v, uint32_t shift)
+{
+    struct Words {
+        uint32_t d[sizeof(v) / 4];
+    };
+    Words x = __builtin_bit_cast(Words, v);
+    shift_down<int(sizeof(v) / 4), 8 * int(sizeof(T))>(x.d, shift);
+    return __builtin_bit_cast(typename Raw<T>::type, x);
+}
+
 // out = residual + D(x + bias), one group of 8 elements per thread: every
 // element is read once and written once, and the pass is bound by HBM.  The
 // loads come first, without a branch, so that they are in flight together.
-// NARROW: rows of fewer than 8 columns, loaded by elements.
+// NARROW: rows of fewer than 8 columns, loaded by elements.  Binary32 goes by
+// the traded pieces of layer.hpp, over the 64 consecutive groups of a wave
+// whatever rows they are in.
 template <typename T, int HINT, bool NARROW>
 __global__ __launch_bounds__(kDropBlock) void dropout_kernel(DropoutArgs<T> a)
 {
     typedef typename Raw<T>::type V;
+    constexpr bool PIECES = sizeof(T) == 4 && !NARROW;
     const RngKey key = rng_key(a.drop);
     const bool ragged = a.cols % 8 != 0;
     const float one = opaque_one();
-    const uint32_t groups = uint32_t(a.groups);
+    const uint32_t groups = uint32_t(a.groups), lane = threadIdx.x & 63;
     const uint64_t total = a.rows * a.groups, stride = uint64_t(gridDim.x) * kDropBlock;
     for (uint64_t base = uint64_t(blockIdx.x) * kDropBlock; base < total; base += stride) {
-        const uint64_t g = base + threadIdx.x;
-        if (g >= total)
-            return;
         // the workgroup's first row and column by one scalar division, the
         // thread's from there in 32 bits
-        uint64_t row = base / a.groups;
-        uint32_t c = uint32_t(base - row * a.groups) + threadIdx.x;
-        if (groups >= kDropBlock) {                // at most one row's end among the workgroup's threads
-            const bool wrap = c >= groups;
-            row += wrap;
-            c -= wrap ? groups : 0;
-        } else {
-            const uint32_t wrap = c / groups;
-            row += wrap;
-            c -= wrap * groups;
-        }
-        const Group at = NARROW ? Group{0, 0, int(a.cols)} : group_at(c * 8, a.cols);
+        const uint64_t row0 = base / a.groups;
+        const uint32_t c0 = uint32_t(base - row0 * a.groups);
+        auto locate = [&](uint32_t offset, uint64_t& row, uint32_t& c) {   // the group `offset` after the first
+            row = row0;
+            c = c0 + offset;
+            if (groups >= kDropBlock) {            // at most one row's end among the workgroup's threads
+                const bool wrap = c >= groups;
+                row += wrap;
+                c -= wrap ? groups : 0;
+            } else {
+                const uint32_t wrap = c / groups;
+                row += wrap;
+                c -= wrap * groups;
+            }
+        };
+        uint32_t mine = threadIdx.x;               // the thread's group, counted from the workgroup's first
+        if (PIECES)
+            mine = mine - lane + lane / 2 + (lane & 1) * 32;
+        uint64_t row;
+        uint32_t c;
         V x, res;
-        if (NARROW) {
-            x = load8(a.x + row * a.ld_x, at.k);
+        if constexpr (PIECES) {
+            uint64_t rows[2];
+            uint32_t col[2], at[2];
+            f32x4 xp[2], rp[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const uint32_t group = threadIdx.x - lane + lane / 2 + p * 32;
+                const bool in = base + group < total;
+                locate(in ? group : 0, rows[p], col[p]);
+                col[p] = col[p] * 8 + (lane & 1) * 4;
+                at[p] = col[p] < a.cols - 4 ? col[p] : a.cols - 4;
+                xp[p] = load4_full<HINT>(a.x + rows[p] * a.ld_x + at[p]);
+                if (a.residual)
+                    rp[p] = load4_full<HINT>(a.residual + rows[p] * a.ld_res + at[p]);
+            }
+            locate(base + mine < total ? mine : 0, row, c);
+            struct Words {
+                uint32_t d[2][4];
+            };
+            auto settle = [&](const f32x4 (&v)[2]) {
+                Words w;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    uint32_t (&d)[4] = w.d[p];
+                    __builtin_memcpy(d, &v[p], 16);
+                    if (ragged)
+                        shift_down<4, 32>(d, col[p] - at[p]);
+                }
+                Part<float, 64>::trade(w.d[0], w.d[1]);
+                return __builtin_bit_cast(f32x8, w);
+            };
+            f32x8 v = splat(-0.0f);                // x + -0 is x, -0 too
+            if (a.bias)
+                v = load8_vector<T>(a.bias, a.bias_f32, c * 8, int(a.cols) - int(c * 8), -0.0f);
+            v = dropped(settle(xp) + v, a.drop, key, base + mine);
             if (a.residual)
-                res = load8(a.residual + row * a.ld_res, at.k);
+                v = settle(rp) + v;
+            Words w = __builtin_bit_cast(Words, v);
+            Part<float, 64>::trade(w.d[0], w.d[1]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const uint32_t group = threadIdx.x - lane + lane / 2 + p * 32;
+                f32x4 o;
+                __builtin_memcpy(&o, w.d[p], 16);
+                store4<HINT>(a.out + rows[p] * a.ld_out + col[p], o, base + group < total ? int(a.cols) - int(col[p]) : 0);
+            }
         } else {
-            x = load8_full<HINT>(a.x + row * a.ld_x + at.at);
+            if (base + mine >= total)
+                return;
+            locate(mine, row, c);
+            const Group at = NARROW ? Group{0, 0, int(a.cols)} : group_at(c * 8, a.cols);
+            if (NARROW) {
+                x = load8(a.x + row * a.ld_x, at.k);
+                if (a.residual)
+                    res = load8(a.residual + row * a.ld_res, at.k);
+            } else {
+                x = load8_full<HINT>(a.x + row * a.ld_x + at.at);
+                if (a.residual)
+                    res = load8_full<HINT>(a.residual + row * a.ld_res + at.at);
+            }
+            f32x8 v = splat(-0.0f);
+            if (a.bias)
+                v = load8_vector<T>(a.bias, a.bias_f32, c * 8, at.k, -0.0f);
+            if (!NARROW && ragged) {
+                x = settle16<T>(x, at.shift);
+                if (a.residual)
+                    res = settle16<T>(res, at.shift);
+            }
+            v = dropped(raw_plus<T>(x, v, one), a.drop, key, base + mine);
             if (a.residual)
-                res = load8_full<HINT>(a.residual + row * a.ld_res + at.at);
+                v = raw_plus<T>(res, v, one);
+            store8<HINT>(a.out + row * a.ld_out + c * 8, narrow<T>(v), at.k);
         }
-        f32x8 v = splat(-0.0f);                    // x + -0 is x, -0 too
-        if (a.bias)
-            v = load8_vector<T>(a.bias, a.bias_f32, c * 8, at.k, -0.0f);
-        if (!NARROW && ragged) {
-            x = settle<T>(x, at.shift, true);
-            if (a.residual)
-                res = settle<T>(res, at.shift, true);
-        }
-        v = dropped(raw_plus<T>(x, v, one), a.drop, key, g);
-        if (a.residual)
-            v = raw_plus<T>(res, v, one);
-        store8<HINT>(a.out + row * a.ld_out + c * 8, narrow<T>(v), at.k);
     }
 }
 

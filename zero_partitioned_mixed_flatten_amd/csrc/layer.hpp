@@ -57,6 +57,30 @@ __device__ __forceinline__ typename Raw<T>::type load8_full(const T* p)
     return *reinterpret_cast<const VU*>(p);
 }
 
+template <int HINT>
+__device__ __forceinline__ f32x4 load4_full(const float* p)
+{
+    typedef f32x4 __attribute__((aligned(4))) VU;
+    if (HINT & 1)
+        return __builtin_nontemporal_load(reinterpret_cast<const VU*>(p));
+    return *reinterpret_cast<const VU*>(p);
+}
+
+template <int HINT>
+__device__ __forceinline__ void store4(float* p, f32x4 v, int k)
+{
+    typedef f32x4 __attribute__((aligned(4))) VU;
+    if (k >= 4 && (HINT & 2))
+        __builtin_nontemporal_store(v, reinterpret_cast<VU*>(p));
+    else if (k >= 4)
+        *reinterpret_cast<VU*>(p) = v;
+    else if (k > 0)
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            if (j < k)
+                p[j] = v[j];
+}
+
 // The first k elements of a group (k <= 0: none), the others 0.
 template <typename T>
 __device__ __forceinline__ typename Raw<T>::type load8(const T* p, int k)
@@ -91,10 +115,10 @@ __device__ __forceinline__ void store8(T* p, typename Raw<T>::type v, int k)
                 p[j] = v[j];
 }
 
-// A thread's group of a row of at least 8 columns, loaded without a branch:
-// a branch around a load makes the next load wait for it.  A group past the
-// row's last 8 columns reads those 8 instead (memory of the row), and
-// settle() moves the elements to their places and puts 0 in the others.
+// Where a group of 8 columns is loaded without a branch (a branch around a load
+// makes the next load wait for it), in a row of at least 8 columns: a group
+// past the row's last 8 columns reads those 8 instead (memory of the row), and
+// settling moves the elements to their places and puts 0 in the others.
 struct Group {
     uint32_t at;                                   // first column loaded
     uint32_t shift;                                // the group's column - at; 8 and more: no columns in the row
@@ -107,11 +131,12 @@ __device__ __forceinline__ Group group_at(uint32_t col, uint32_t cols)
     return Group{at, col - at, int(cols) - int(col)};
 }
 
+// Moves WORDS words down by `shift` elements of BITS bits, 0 from above.
 template <int WORDS, int BITS>
 __device__ __forceinline__ void shift_down(uint32_t (&d)[WORDS], uint32_t shift)
 {
 #pragma unroll
-    for (int bit = 2; bit >= 0; --bit) {
+    for (int bit = BITS == 16 ? 2 : 1; bit >= 0; --bit) {
         const bool on = (shift >> bit) & 1;
         const int words = (1 << bit) * BITS / 32;
 #pragma unroll
@@ -126,24 +151,122 @@ __device__ __forceinline__ void shift_down(uint32_t (&d)[WORDS], uint32_t shift)
     }
 }
 
-// `ragged`: cols is not a multiple of 8 (the same for every thread).  ZERO
-// false: groups with no columns in the row may keep what was loaded.
-template <typename T, bool ZERO = true>
-__device__ __forceinline__ typename Raw<T>::type settle(typename Raw<T>::type v, uint32_t shift, bool ragged)
-{
-    constexpr int kWords = 2 * int(sizeof(T));
-    struct Words {
-        uint32_t d[kWords];
-    };
-    Words x = __builtin_bit_cast(Words, v);
-    if (ragged)
-        shift_down<kWords, 8 * int(sizeof(T))>(x.d, shift);
-    if (ZERO)
+// The part of a row that one of its TPR threads holds in pass i, and how it is
+// loaded and stored.  16-bit elements: the thread's group, one 16-byte access.
+// Binary32: a group is two 16-byte pieces, and threads that each accessed
+// their own 32 bytes would leave every access of a wave with half of each line
+// (a plain copy done so runs at 3.9 TB/s against 6.2).  So the threads of a
+// wave access the pieces of 2 * 64 consecutive pieces in order, 64 at a time,
+// and neighbours trade: an even thread ends with the group whose two pieces
+// the pair has in the first access, an odd one with the second's.  TPR = 1:
+// a row of fewer than 8 columns, by elements.
+template <typename T, int TPR>
+struct Part {
+    static constexpr int kPieces = sizeof(T) == 4 ? 2 : 1;
+    static constexpr uint32_t kPer = 8 / kPieces;  // elements of a piece
+    uint32_t group;
+    int k;                                         // the group's columns in the row
+    uint32_t at[kPieces], shift[kPieces];          // the pieces as loaded
+    int have[kPieces];                             // the pieces' columns in the row
+
+    __device__ __forceinline__ Part(uint32_t i, uint32_t t, uint32_t cols)
+    {
+        if (TPR == 1) {
+            group = 0;
+            k = have[0] = int(cols);
+            return;
+        }
+        if (kPieces == 1) {
+            group = i * TPR + t;
+            at[0] = group * 8;
+        } else {
+            constexpr uint32_t kSpan = TPR < 64 ? TPR : 64;
+            const uint32_t lane = t % kSpan, base = i * TPR + (t - lane);
+            group = base + lane / 2 + (lane & 1) * (kSpan / 2);
+            at[0] = base * 8 + lane * 4;
+            at[kPieces - 1] = at[0] + kSpan * 4;
+        }
+        k = int(cols) - int(group * 8);
 #pragma unroll
-        for (int i = 0; i < kWords; ++i)
-            x.d[i] = shift < 8 ? x.d[i] : 0;
-    return __builtin_bit_cast(typename Raw<T>::type, x);
-}
+        for (int p = 0; p < kPieces; ++p) {
+            const uint32_t col = at[p];
+            have[p] = int(cols) - int(col);
+            at[p] = col < cols - kPer ? col : cols - kPer;
+            shift[p] = col - at[p];
+        }
+    }
+
+    template <int HINT>
+    __device__ __forceinline__ typename Raw<T>::type load(const T* row) const
+    {
+        if constexpr (TPR == 1) {
+            return load8(row, k);
+        } else if constexpr (kPieces == 1) {
+            return load8_full<HINT>(row + at[0]);
+        } else {
+            const f32x4 a = load4_full<HINT>(row + at[0]), b = load4_full<HINT>(row + at[1]);
+            return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    }
+
+    // What load() gave, as the thread's group.  `ragged`: cols is not a multiple
+    // of 8 (the same for every thread).  ZERO false: groups with no columns in
+    // the row may hold anything.
+    template <bool ZERO = true>
+    __device__ __forceinline__ typename Raw<T>::type settle(typename Raw<T>::type v, bool ragged) const
+    {
+        if constexpr (TPR == 1) {
+            return v;
+        } else {
+            constexpr int kWords = 2 * int(sizeof(T)) / kPieces;
+            struct Words {
+                uint32_t d[kPieces][kWords];
+            };
+            Words x = __builtin_bit_cast(Words, v);
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                if (ragged)
+                    shift_down<kWords, 8 * int(sizeof(T))>(x.d[p], shift[p]);
+                if (ZERO)
+#pragma unroll
+                    for (int i = 0; i < kWords; ++i)
+                        x.d[p][i] = shift[p] < kPer ? x.d[p][i] : 0;
+            }
+            if constexpr (kPieces == 2)
+                trade(x.d[0], x.d[1]);
+            return __builtin_bit_cast(typename Raw<T>::type, x);
+        }
+    }
+
+    template <int HINT>
+    __device__ __forceinline__ void store(T* row, typename Raw<T>::type v, bool live) const
+    {
+        if constexpr (kPieces == 1 || TPR == 1) {
+            store8<HINT>(row + group * 8, v, live ? k : 0);
+        } else {
+            struct Words {
+                uint32_t d[2][4];
+            };
+            Words x = __builtin_bit_cast(Words, v);
+            trade(x.d[0], x.d[1]);
+            store4<HINT>(row + at[0] + shift[0], __builtin_bit_cast(f32x4, x.d[0]), live ? have[0] : 0);
+            store4<HINT>(row + at[1] + shift[1], __builtin_bit_cast(f32x4, x.d[1]), live ? have[1] : 0);
+        }
+    }
+
+    // The even thread gives its second piece and takes the odd one's first: its own inverse.
+    static __device__ __forceinline__ void trade(uint32_t (&lo)[4], uint32_t (&hi)[4])
+    {
+        const bool odd = threadIdx.x & 1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t give = odd ? lo[i] : hi[i];
+            const uint32_t take = __builtin_amdgcn_update_dpp(0, give, 0xB1, 0xf, 0xf, true);   // lane ^ 1
+            lo[i] = odd ? take : lo[i];
+            hi[i] = odd ? hi[i] : take;
+        }
+    }
+};
 
 // 8 sums into a partial's row, which the fold reads back soon: kept in the caches.
 __device__ __forceinline__ void store8_f32(float* p, f32x8 v, int k)
@@ -236,6 +359,39 @@ __device__ __forceinline__ f32x8 load8_vector(const void* p, bool f32, uint64_t 
     return v;
 }
 
+// The same without a branch on the thread (see Group), for loads inside a
+// loop; groups with no columns in the row may hold anything.
+template <typename T>
+__device__ __forceinline__ f32x8 load8_vector_at(const void* p, bool f32, const Group& at, bool ragged, float absent)
+{
+    if (!p)
+        return splat(absent);
+    f32x8 v;
+    if (f32) {
+        typedef f32x8 __attribute__((aligned(4))) VU;
+        v = *reinterpret_cast<const VU*>(static_cast<const float*>(p) + at.at);
+    } else {
+        typedef typename Raw<T>::type V;
+        typedef V __attribute__((aligned(sizeof(T)))) VU;
+        v = widen<T>(*reinterpret_cast<const VU*>(static_cast<const T*>(p) + at.at));
+    }
+    if (ragged) {
+        struct Words {
+            uint32_t d[8];
+        };
+        Words x = __builtin_bit_cast(Words, v);
+#pragma unroll
+        for (int bit = 2; bit >= 0; --bit)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int from = i + (1 << bit);
+                x.d[i] = (at.shift >> bit) & 1 ? (from < 8 ? x.d[from < 8 ? from : 0] : 0) : x.d[i];
+            }
+        v = __builtin_bit_cast(f32x8, x);
+    }
+    return v;
+}
+
 // ---- the generator ---------------------------------------------------------------
 // Philox4x32-10 (Salmon, Moraes, Dror and Shaw 2011): ten rounds of two
 // 32 x 32 -> 64-bit products over a 128-bit counter under a 64-bit key.
@@ -316,9 +472,12 @@ __device__ __forceinline__ float dpp(float v)
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v)
 {
-    v += dpp<0xB1>(v);                             // quad_perm 1,0,3,2: lane ^ 1
-    v += dpp<0x4E>(v);                             // quad_perm 2,3,0,1: lane ^ 2
-    v += dpp<0x141>(v);                            // row_half_mirror: the other quad of 8
+    static_assert(LANES == 1 || LANES == 8 || LANES == 16 || LANES == 32 || LANES == 64, "lanes of a row");
+    if (LANES >= 8) {
+        v += dpp<0xB1>(v);                         // quad_perm 1,0,3,2: lane ^ 1
+        v += dpp<0x4E>(v);                         // quad_perm 2,3,0,1: lane ^ 2
+        v += dpp<0x141>(v);                        // row_half_mirror: the other quad of 8
+    }
     if (LANES >= 16)
         v += dpp<0x140>(v);                        // row_mirror: the other 8 of 16
     if (LANES == 32)

@@ -43,6 +43,7 @@ template <typename T, bool JOIN, int BLOCK, int TPR, int VPT, int HINT>
 __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
 {
     typedef typename Raw<T>::type V;
+    typedef Part<T, TPR> P;
     constexpr int kRows = BLOCK / TPR;
     __shared__ alignas(16) float scratch[2 * BLOCK / 64];
     uint32_t parity = 0;
@@ -54,9 +55,8 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
     if (TPR >= 64)
         slot = __builtin_amdgcn_readfirstlane(slot);
     const uint32_t t = threadIdx.x % TPR;
+    auto part = [&](int i) { return P(i, t, a.cols); };
 
-    Group at[VPT];
-    f32x8 w[VPT], b[VPT], bias[VPT];
     struct Row {
         V x[VPT], res[VPT];
     };
@@ -64,25 +64,23 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
         row = row < a.rows ? row : a.rows - 1;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            f.x[i] = load8_full<HINT>(a.x + row * a.ld_x + at[i].at);
+            f.x[i] = part(i).template load<HINT>(a.x + row * a.ld_x);
             if (JOIN && a.residual)
-                f.res[i] = load8_full<HINT>(a.residual + row * a.ld_res + at[i].at);
+                f.res[i] = part(i).template load<HINT>(a.residual + row * a.ld_res);
         }
     };
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-        at[i] = group_at((i * TPR + t) * 8, a.cols);
     const uint64_t stride = uint64_t(gridDim.x) * kRows;
     uint64_t first = uint64_t(blockIdx.x) * kRows;
     Row cur, next;
     fetch(first + slot, cur);
+    f32x8 w[VPT], b[VPT], bias[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const uint32_t col = (i * TPR + t) * 8;
-        w[i] = load8_vector<T>(a.w, a.vec_f32, col, at[i].k, 1.0f);
-        b[i] = load8_vector<T>(a.b, a.vec_f32, col, at[i].k, 0.0f);
+        const P at = part(i);
+        w[i] = load8_vector<T>(a.w, a.vec_f32, at.group * 8, at.k, 1.0f);
+        b[i] = load8_vector<T>(a.b, a.vec_f32, at.group * 8, at.k, 0.0f);
         if (JOIN)
-            bias[i] = load8_vector<T>(a.bias, a.vec_f32, col, at[i].k, -0.0f);   // x + -0 is x, -0 too
+            bias[i] = load8_vector<T>(a.bias, a.vec_f32, at.group * 8, at.k, -0.0f);   // x + -0 is x, -0 too
     }
     for (; first < a.rows; first += stride) {
         const uint64_t row = first + slot;
@@ -94,14 +92,15 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
         float s[1] = {0.0f}, q[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            raw[i] = settle<T>(cur.x[i], at[i].shift, ragged);
+            const P at = part(i);
+            raw[i] = at.settle(cur.x[i], ragged);
             if (JOIN) {
                 f32x8 v = raw_plus<T>(raw[i], bias[i], one);
-                v = dropped(v, a.drop, key, row * groups + (i * TPR + t));
+                v = dropped(v, a.drop, key, row * groups + at.group);
                 if (a.residual)
-                    v = raw_plus<T>(settle<T>(cur.res[i], at[i].shift, ragged), v, one);
+                    v = raw_plus<T>(at.settle(cur.res[i], ragged), v, one);
                 raw[i] = narrow<T>(v);
-                store8<HINT>(a.r + row * a.ld_r + (i * TPR + t) * 8, raw[i], live ? at[i].k : 0);
+                at.template store<HINT>(a.r + row * a.ld_r, raw[i], live);
             }
             const f32x8 v = widen<T>(raw[i]);
             s[0] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
@@ -111,11 +110,12 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
         float qb = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
+            const int k = part(i).k;
             x[i] = raw_plus<T>(raw[i], splat(-mean), one);
-            if (at[i].k < 8)
+            if (k < 8)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    x[i][j] = j < at[i].k ? x[i][j] : 0.0f;
+                    x[i][j] = j < k ? x[i][j] : 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
                 q[0] = __builtin_fmaf(x[i][j], x[i][j], q[0]);
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[j] = __builtin_fmaf(x[i][j] * rstd, w[i][j], b[i][j]);
-            store8<HINT>(a.y + row * a.ld_y + (i * TPR + t) * 8, narrow<T>(v), live ? at[i].k : 0);
+            part(i).template store<HINT>(a.y + row * a.ld_y, narrow<T>(v), live);
         }
         if (t == 0 && live) {
             if (a.mean) a.mean[row] = mean;
@@ -141,66 +141,67 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
     }
 }
 
-// Any width (and fewer than 8 columns): a workgroup takes a row and goes over
-// it three times.
-constexpr int kWideBlock = 256;
+// Wider rows: a workgroup takes a row and goes over it three times, the second
+// and third time from the caches.
+constexpr int kWideBlock = 1024;
 
 template <typename T, bool JOIN>
 __global__ __launch_bounds__(kWideBlock) void norm_fwd_wide_kernel(FwdArgs<T> a)
 {
+    typedef typename Raw<T>::type V;
+    typedef Part<T, kWideBlock> P;
     __shared__ alignas(16) float scratch[2 * kWideBlock / 64];
     uint32_t parity = 0;
     const RngKey key = rng_key(a.drop);
-    const uint32_t groups = (a.cols + 7) / 8;
-    const float n = float(a.cols);
+    const uint32_t groups = (a.cols + 7) / 8, rounds = (groups + kWideBlock - 1) / kWideBlock;
+    const bool ragged = a.cols % 8 != 0;
+    const float n = float(a.cols), inv = 1.0f / n, one = opaque_one();
     for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T* src = a.x + row * a.ld_x;
         float s[1] = {0.0f}, q[1] = {0.0f};
-        for (uint32_t g = threadIdx.x; g < groups; g += kWideBlock) {
-            const uint32_t col = g * 8;
-            const int k = int(a.cols) - int(col);
-            typename Raw<T>::type raw = load8(src + col, k);
+        for (uint32_t i = 0; i < rounds; ++i) {
+            const P at(i, threadIdx.x, a.cols);
+            V raw = at.template load<kCached>(src), res;
+            if (JOIN && a.residual)
+                res = at.template load<kCached>(a.residual + row * a.ld_res);
+            raw = at.settle(raw, ragged);
             if (JOIN) {
-                f32x8 v = widen<T>(raw);
-                if (a.bias)
-                    v = v + load8_vector<T>(a.bias, a.vec_f32, col, k, 0.0f);
-                v = dropped(v, a.drop, key, row * groups + g);
+                const Group g = group_at(at.group * 8, a.cols);
+                f32x8 v = raw_plus<T>(raw, load8_vector_at<T>(a.bias, a.vec_f32, g, ragged, -0.0f), one);
+                v = dropped(v, a.drop, key, row * groups + at.group);
                 if (a.residual)
-                    v = widen<T>(load8(a.residual + row * a.ld_res + col, k)) + v;
+                    v = raw_plus<T>(at.settle(res, ragged), v, one);
+                if (at.k <= 0)
+                    v = splat(0.0f);               // past the row: not the bias either
                 raw = narrow<T>(v);
-                store8(a.r + row * a.ld_r + col, raw, k);
+                at.template store<0>(a.r + row * a.ld_r, raw, true);
             }
             const f32x8 v = widen<T>(raw);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                s[0] += j < k ? v[j] : 0.0f;
+            s[0] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
         }
         row_sum<kWideBlock, kWideBlock>(s, scratch, parity);
-        const float mean = s[0] / n;
+        const float mean = over(s[0], n, inv);
         if (JOIN)
-            src = a.r + row * a.ld_r;
-        for (uint32_t g = threadIdx.x; g < groups; g += kWideBlock) {
-            const uint32_t col = g * 8;
-            const int k = int(a.cols) - int(col);
-            const f32x8 v = widen<T>(load8(src + col, k));
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float d = j < k ? v[j] - mean : 0.0f;
-                q[0] = __builtin_fmaf(d, d, q[0]);
-            }
-        }
-        row_sum<kWideBlock, kWideBlock>(q, scratch, parity);
-        const float rstd = 1.0f / sqrtf(q[0] / n + a.eps);
-        for (uint32_t g = threadIdx.x; g < groups; g += kWideBlock) {
-            const uint32_t col = g * 8;
-            const int k = int(a.cols) - int(col);
-            f32x8 v = widen<T>(load8(src + col, k));
-            const f32x8 w = load8_vector<T>(a.w, a.vec_f32, col, k, 1.0f);
-            const f32x8 b = load8_vector<T>(a.b, a.vec_f32, col, k, 0.0f);
+            src = a.r + row * a.ld_r;              // each thread uses what it stored there itself
+        for (uint32_t i = 0; i < rounds; ++i) {
+            const P at(i, threadIdx.x, a.cols);
+            const f32x8 d = raw_plus<T>(at.settle(at.template load<kCached>(src), ragged), splat(-mean), one);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[j] = __builtin_fmaf((v[j] - mean) * rstd, w[j], b[j]);
-            store8(a.y + row * a.ld_y + col, narrow<T>(v), k);
+                q[0] = j < at.k ? __builtin_fmaf(d[j], d[j], q[0]) : q[0];
+        }
+        row_sum<kWideBlock, kWideBlock>(q, scratch, parity);
+        const float rstd = 1.0f / sqrtf(over(q[0], n, inv) + a.eps);
+        for (uint32_t i = 0; i < rounds; ++i) {
+            const P at(i, threadIdx.x, a.cols);
+            const Group g = group_at(at.group * 8, a.cols);
+            f32x8 v = raw_plus<T>(at.settle(at.template load<kCached>(src), ragged), splat(-mean), one);
+            const f32x8 w = load8_vector_at<T>(a.w, a.vec_f32, g, ragged, 1.0f);
+            const f32x8 b = load8_vector_at<T>(a.b, a.vec_f32, g, ragged, 0.0f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = __builtin_fmaf(v[j] * rstd, w[j], b[j]);
+            at.template store<kStreamed>(a.y + row * a.ld_y, narrow<T>(v), true);
         }
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[row] = mean;
@@ -209,25 +210,26 @@ __global__ __launch_bounds__(kWideBlock) void norm_fwd_wide_kernel(FwdArgs<T> a)
     }
 }
 
-// The threads of a row: as few powers of two as hold its groups one each up to
-// a wave; wider rows take two groups a thread and whole waves, at least two.
-// The workgroup is one row, or as many as make 256 threads.  Grid: 1024
-// resident threads a CU with two groups each, 1536 with one, and no more
-// workgroups than blocks of rows.  Measured at 13.1 M fp16 elements (layer
-// norm / joined, us; two copies of the same bytes take 10.6 / 21.1): 512
-// columns 12.8 / 22.7, 64 threads x 1, against 13.1 / 23.6 with 32 x 2; 1600
-// columns 13.7 / 24.2, 128 x 2, against 14.6 / 25.6 with 256 x 1 and 14.9 /
-// 29.2 with 64 x 4; 8192 columns 13.1 / 23.8, 512 x 2, against 14.5 / 27.0
-// with 1024 x 1 and 15.1 / 26.8 with 256 x 4.  Grid, 512 columns: 13.2 / 23.0
-// with 1024 threads a CU, 12.6 / 24.8 with 2048; 1600 columns: 15.4 / 26.4 with
-// 1536, 16.6 / 28.9 with 512.
+// The threads of a row: one below 8 columns; as few powers of two as hold its
+// groups one each up to a wave; wider rows take two groups a thread and whole
+// waves, at least two.  The workgroup is one row, or as
+// many as make 256 threads.  Grid: the workgroups that 1024 threads a CU make
+// with two groups each, 1536 with one, all resident at once, and no more than
+// there are blocks of rows.  Measured at 13.1 M fp16 elements (layer norm /
+// joined, us; two copies of the same bytes take 10.6 / 21.1): 512 columns 12.8
+// / 22.7, 64 threads x 1, against 13.1 / 23.6 with 32 x 2; 1600 columns 13.7 /
+// 24.2, 128 x 2, against 14.6 / 25.6 with 256 x 1 and 14.9 / 29.2 with 64 x 4;
+// 8192 columns 13.1 / 23.8, 512 x 2, against 14.5 / 27.0 with 1024 x 1 and 15.1
+// / 26.8 with 256 x 4.  Grid, 512 columns: 13.2 / 23.0 with 1024 threads a CU,
+// 12.6 / 24.8 with 2048; 1600 columns: 15.4 / 26.4 with 1536, 16.6 / 28.9 with
+// 512.
 constexpr uint64_t kCus = 256;
 
 template <typename T, bool JOIN, int TPR, int VPT>
 int launch_rows(const FwdArgs<T>& a, hipStream_t s)
 {
     constexpr int kBlock = TPR < 192 ? 256 : TPR;
-    constexpr uint64_t kMost = kCus * (VPT == 1 ? 1536 : 1024) / kBlock;
+    constexpr uint64_t kMost = kCus * ((VPT == 1 ? 1536 : 1024) / kBlock);
     uint64_t grid = (a.rows + kBlock / TPR - 1) / (kBlock / TPR);
     if (grid > kMost)
         grid = kMost;
@@ -244,11 +246,7 @@ int launch_rows(const FwdArgs<T>& a, hipStream_t s)
 template <typename T, bool JOIN>
 int launch_fwd(const FwdArgs<T>& a, hipStream_t s)
 {
-    if (a.cols < 8 || a.cols > 16384) {
-        const uint64_t grid = a.rows < (1u << 20) ? a.rows : (1u << 20);
-        hipLaunchKernelGGL((norm_fwd_wide_kernel<T, JOIN>), dim3(uint32_t(grid)), dim3(kWideBlock), 0, s, a);
-        return launch_status();
-    }
+    if (a.cols < 8) return launch_rows<T, JOIN, 1, 1>(a, s);
     if (a.cols <= 64) return launch_rows<T, JOIN, 8, 1>(a, s);
     if (a.cols <= 128) return launch_rows<T, JOIN, 16, 1>(a, s);
     if (a.cols <= 256) return launch_rows<T, JOIN, 32, 1>(a, s);
@@ -264,8 +262,11 @@ int launch_fwd(const FwdArgs<T>& a, hipStream_t s)
     case 8: return launch_rows<T, JOIN, 512, 2>(a, s);
     case 9: case 10: return launch_rows<T, JOIN, 640, 2>(a, s);
     case 11: case 12: return launch_rows<T, JOIN, 768, 2>(a, s);
-    default: return launch_rows<T, JOIN, 1024, 2>(a, s);
+    case 13: case 14: case 15: case 16: return launch_rows<T, JOIN, 1024, 2>(a, s);
     }
+    const uint64_t grid = a.rows < (1u << 20) ? a.rows : (1u << 20);
+    hipLaunchKernelGGL((norm_fwd_wide_kernel<T, JOIN>), dim3(uint32_t(grid)), dim3(kWideBlock), 0, s, a);
+    return launch_status();
 }
 
 struct FwdCall {

@@ -35,12 +35,12 @@ struct BwdArgs {
     bool want[3];                                  // dw, db, dbias
 };
 
-// Rows that fit the registers of TPR threads, VPT groups of 8 columns each,
-// in one pass: a persistent workgroup takes every gridDim.x-th block of
-// BLOCK / TPR rows, the next rows' loads in flight while it works on the
-// present ones, and keeps its columns' sums in registers to the end, where
+// Rows that fit the registers of TPR threads, a group of 8 columns each, in
+// one pass: a persistent workgroup takes every gridDim.x-th block of
+// BLOCK / TPR rows, the loads of the next NBUF - 1 in flight while it works on
+// the present one, and keeps its columns' sums in registers to the end, where
 // it stores one partial.
-template <typename T, bool NORM, bool DROP, int BLOCK, int TPR, int VPT, int NBUF, int HINT>
+template <typename T, bool NORM, bool DROP, int BLOCK, int TPR, int NBUF, int HINT>
 __global__ __launch_bounds__(BLOCK) void rows_bwd_kernel(BwdArgs<T> a)
 {
     typedef typename Raw<T>::type V;
@@ -55,105 +55,78 @@ __global__ __launch_bounds__(BLOCK) void rows_bwd_kernel(BwdArgs<T> a)
     uint32_t slot = threadIdx.x / TPR;
     if (TPR >= 64)
         slot = __builtin_amdgcn_readfirstlane(slot);
-    const uint32_t t = threadIdx.x % TPR;
+    const Part<T, TPR> at(0, threadIdx.x % TPR, a.cols);
 
-    Group at[VPT];
-    f32x8 w[VPT], sum[kSums][VPT];
     struct Row {
-        V dy[VPT], r[VPT], dres[VPT];
+        V dy, r, dres;
         float mean, rstd;
     };
     auto fetch = [&](uint64_t row, Row& f) {
         row = row < a.rows ? row : a.rows - 1;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            f.dy[i] = load8_full<HINT>(a.dy + row * a.ld_dy + at[i].at);
-            if (NORM) {
-                f.r[i] = load8_full<HINT>(a.r + row * a.ld_r + at[i].at);
-                if (a.dres)
-                    f.dres[i] = load8_full<HINT>(a.dres + row * a.ld_dres + at[i].at);
-            }
-        }
+        f.dy = at.template load<HINT>(a.dy + row * a.ld_dy);
         if (NORM) {
+            f.r = at.template load<HINT>(a.r + row * a.ld_r);
+            if (a.dres)
+                f.dres = at.template load<HINT>(a.dres + row * a.ld_dres);
             f.mean = a.mean[row];
             f.rstd = a.rstd[row];
         }
     };
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-        at[i] = group_at((i * TPR + t) * 8, a.cols);
     const uint64_t stride = uint64_t(gridDim.x) * kRows;
     uint64_t first = uint64_t(blockIdx.x) * kRows;
     Row buf[NBUF];
 #pragma unroll
     for (int i = 0; i < NBUF - 1; ++i)
         fetch(first + i * stride + slot, buf[i]);
+    f32x8 w, sum[kSums];
+    if (NORM)
+        w = load8_vector<T>(a.w, a.vec_f32, at.group * 8, at.k, 1.0f);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        if (NORM)
-            w[i] = load8_vector<T>(a.w, a.vec_f32, (i * TPR + t) * 8, at[i].k, 1.0f);
-#pragma unroll
-        for (int q = 0; q < kSums; ++q)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                sum[q][i][j] = 0.0f;
-    }
+    for (int q = 0; q < kSums; ++q)
+        sum[q] = splat(0.0f);
     auto work = [&](uint64_t row, Row& cur) {
         const bool live = row < a.rows;
-        // with d = dy * rstd and x = r - mean: g rstd = d w, h rstd = x rstd^2
-        f32x8 x[VPT], g[VPT];
-        float c[2] = {0.0f, 0.0f};
+        const V dy = at.settle(cur.dy, ragged);    // 0 past the row's end
+        f32x8 e;
         if (NORM) {
-            float c0b = 0.0f, c1b = 0.0f;
+            // with d = dy * rstd and x = r - mean: g rstd = d w, h rstd = x rstd^2
+            const f32x8 d = raw_times<T>(dy, cur.rstd);
+            const f32x8 x = raw_plus<T>(at.template settle<false>(cur.r, ragged), splat(-cur.mean), one), g = d * w;
+            if (live) {
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                cur.dy[i] = settle<T>(cur.dy[i], at[i].shift, ragged);   // 0 past the row's end
-                const f32x8 d = raw_times<T>(cur.dy[i], cur.rstd);
-                x[i] = raw_plus<T>(settle<T, false>(cur.r[i], at[i].shift, ragged), splat(-cur.mean), one);
-                g[i] = d * w[i];
-                if (live) {
+                for (int j = 0; j < 8; ++j)
+                    sum[0][j] = __builtin_fmaf(d[j], x[j], sum[0][j]);
+                sum[1] = raw_plus<T>(dy, sum[1], one);
+            }
+            float c[2] = {0.0f, 0.0f}, c0b = 0.0f, c1b = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        sum[0][i][j] = __builtin_fmaf(d[j], x[i][j], sum[0][i][j]);
-                    sum[1][i] = raw_plus<T>(cur.dy[i], sum[1][i], one);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    c[0] += g[i][j];
-                    c0b += g[i][j + 1];
-                    c[1] = __builtin_fmaf(g[i][j], x[i][j], c[1]);
-                    c1b = __builtin_fmaf(g[i][j + 1], x[i][j + 1], c1b);
-                }
+            for (int j = 0; j < 8; j += 2) {
+                c[0] += g[j];
+                c0b += g[j + 1];
+                c[1] = __builtin_fmaf(g[j], x[j], c[1]);
+                c1b = __builtin_fmaf(g[j + 1], x[j + 1], c1b);
             }
             c[0] += c0b;
             c[1] += c1b;
             row_sum<BLOCK, TPR>(c, scratch, parity);
             c[0] = -over(c[0], n, inv);
             c[1] = -(over(c[1], n, inv) * cur.rstd * cur.rstd);
-        }
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const uint32_t g8 = i * TPR + t, col = g8 * 8;
-            const int k = live ? at[i].k : 0;
-            f32x8 e;
-            if (NORM) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    e[j] = __builtin_fmaf(x[i][j], c[1], g[i][j] + c[0]);
-                if (a.dres)
-                    e = raw_plus<T>(settle<T, false>(cur.dres[i], at[i].shift, ragged), e, one);
-            } else {
-                e = widen<T>(settle<T>(cur.dy[i], at[i].shift, ragged));
-            }
-            if (DROP) {
-                if (NORM)
-                    store8<HINT>(a.dr + row * a.ld_dr + col, narrow<T>(e), k);
-                e = dropped(e, a.drop, key, row * groups + g8);
-                if (live)
-                    sum[kSums - 1][i] = sum[kSums - 1][i] + e;
-            }
-            store8<HINT>(a.dx + row * a.ld_dx + col, narrow<T>(e), k);
+            for (int j = 0; j < 8; ++j)
+                e[j] = __builtin_fmaf(x[j], c[1], g[j] + c[0]);
+            if (a.dres)
+                e = raw_plus<T>(at.template settle<false>(cur.dres, ragged), e, one);
+        } else {
+            e = widen<T>(dy);
         }
+        if (DROP) {
+            if (NORM)
+                at.template store<HINT>(a.dr + row * a.ld_dr, narrow<T>(e), live);
+            e = dropped(e, a.drop, key, row * groups + at.group);
+            if (live)
+                sum[kSums - 1] = sum[kSums - 1] + e;
+        }
+        at.template store<HINT>(a.dx + row * a.ld_dx, narrow<T>(e), live);
     };
     for (bool more = true; more;) {
 #pragma unroll
@@ -170,29 +143,26 @@ __global__ __launch_bounds__(BLOCK) void rows_bwd_kernel(BwdArgs<T> a)
     // one partial of the workgroup: the upper half of its rows' threads hands
     // its sums to the lower half, until one row's are left
     if (kRows > 1) {
-        __shared__ f32x4 hand[kRows > 1 ? kSums * VPT * BLOCK : 1];
-#pragma unroll
+        __shared__ f32x4 hand[kRows > 1 ? kSums * BLOCK : 1];
         for (int half = kRows / 2; half >= 1; half /= 2) {
             const int lanes = half * TPR;
             if (int(slot) >= half && int(slot) < 2 * half)
 #pragma unroll
-                for (int q = 0; q < kSums * VPT; ++q)
+                for (int q = 0; q < kSums; ++q)
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const f32x8 v = sum[q / VPT][q % VPT];
-                        hand[(2 * q + p) * lanes + (int(threadIdx.x) - lanes)] = f32x4{v[4 * p], v[4 * p + 1], v[4 * p + 2],
-                                                                                       v[4 * p + 3]};
-                    }
+                    for (int p = 0; p < 2; ++p)
+                        hand[(2 * q + p) * lanes + (int(threadIdx.x) - lanes)] =
+                            f32x4{sum[q][4 * p], sum[q][4 * p + 1], sum[q][4 * p + 2], sum[q][4 * p + 3]};
             __syncthreads();
             if (int(slot) < half)
 #pragma unroll
-                for (int q = 0; q < kSums * VPT; ++q)
+                for (int q = 0; q < kSums; ++q)
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
                         const f32x4 o = hand[(2 * q + p) * lanes + int(threadIdx.x)];
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            sum[q / VPT][q % VPT][4 * p + j] += o[j];
+                            sum[q][4 * p + j] += o[j];
                     }
             __syncthreads();
         }
@@ -202,18 +172,14 @@ __global__ __launch_bounds__(BLOCK) void rows_bwd_kernel(BwdArgs<T> a)
 #pragma unroll
     for (int q = 0; q < kSums; ++q) {
         const int which = NORM ? q : 2;
-        if (!a.want[which])
-            continue;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const uint32_t col = (i * TPR + t) * 8;
-            store8_f32(a.partials + (uint64_t(blockIdx.x) * 3 + which) * a.cols + col, sum[q][i], int(a.cols) - int(col));
-        }
+        if (a.want[which])
+            store8_f32(a.partials + (uint64_t(blockIdx.x) * 3 + which) * a.cols + at.group * 8, sum[q], at.k);
     }
 }
 
-// The pass in two kernels, for any width: c1 and c2 of each row, then strips
-// of columns going down a chunk of rows.
+// Wider rows, in two kernels: c1 and c2 of each row, then strips of columns
+// going down a chunk of rows, reading dy and r again (as far as they are still
+// there from the 256 MB cache).
 constexpr int kWideBlock = 256;
 constexpr uint64_t kStrip = kWideBlock * 8;
 constexpr uint64_t kWideTarget = 1024;             // workgroups the strips are cut into rows for
@@ -229,31 +195,33 @@ uint64_t wide_chunks(uint64_t rows, uint64_t cols)
 template <typename T>
 __global__ __launch_bounds__(kWideBlock) void row_sums_kernel(BwdArgs<T> a)
 {
+    typedef Part<T, kWideBlock> P;
     __shared__ alignas(16) float scratch[4 * kWideBlock / 64];
     uint32_t parity = 0;
-    const uint32_t groups = (a.cols + 7) / 8;
+    const uint32_t groups = (a.cols + 7) / 8, rounds = (groups + kWideBlock - 1) / kWideBlock;
+    const bool ragged = a.cols % 8 != 0;
+    const float n = float(a.cols), inv = 1.0f / n, one = opaque_one();
     for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const float mean = a.mean[row], rstd = a.rstd[row];
-        float s[2] = {0.0f, 0.0f};
-        for (uint32_t g = threadIdx.x; g < groups; g += kWideBlock) {
-            const uint32_t col = g * 8;
-            const int k = int(a.cols) - int(col);
-            const f32x8 dy = widen<T>(load8(a.dy + row * a.ld_dy + col, k));
-            const f32x8 r = widen<T>(load8(a.r + row * a.ld_r + col, k));
-            const f32x8 w = load8_vector<T>(a.w, a.vec_f32, col, k, 1.0f);
+        float c[2] = {0.0f, 0.0f};
+#pragma unroll 2
+        for (uint32_t i = 0; i < rounds; ++i) {
+            const P at(i, threadIdx.x, a.cols);
+            const typename Raw<T>::type dy = at.template load<kCached>(a.dy + row * a.ld_dy);
+            const typename Raw<T>::type r = at.template load<kCached>(a.r + row * a.ld_r);
+            const f32x8 w = load8_vector_at<T>(a.w, a.vec_f32, group_at(at.group * 8, a.cols), ragged, 1.0f);
+            const f32x8 g = raw_times<T>(at.settle(dy, ragged), rstd) * w;       // 0 past the row's end
+            const f32x8 x = raw_plus<T>(at.settle(r, ragged), splat(-mean), one);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float gj = dy[j] * w[j], h = (r[j] - mean) * rstd;
-                if (j < k) {
-                    s[0] += gj;
-                    s[1] = __builtin_fmaf(gj, h, s[1]);
-                }
+                c[0] += g[j];
+                c[1] = __builtin_fmaf(g[j], x[j], c[1]);
             }
         }
-        row_sum<kWideBlock, kWideBlock>(s, scratch, parity);
+        row_sum<kWideBlock, kWideBlock>(c, scratch, parity);
         if (threadIdx.x == 0) {
-            a.row_sums[2 * row] = s[0] / float(a.cols);
-            a.row_sums[2 * row + 1] = s[1] / float(a.cols);
+            a.row_sums[2 * row] = -over(c[0], n, inv);
+            a.row_sums[2 * row + 1] = -(over(c[1], n, inv) * rstd * rstd);
         }
     }
 }
@@ -261,53 +229,77 @@ __global__ __launch_bounds__(kWideBlock) void row_sums_kernel(BwdArgs<T> a)
 template <typename T, bool NORM, bool DROP>
 __global__ __launch_bounds__(kWideBlock) void strips_kernel(BwdArgs<T> a)
 {
-    const uint32_t groups = (a.cols + 7) / 8;
-    const uint32_t g = blockIdx.x * kWideBlock + threadIdx.x;
-    if (g >= groups)
-        return;
+    typedef typename Raw<T>::type V;
+    constexpr int kSums = (NORM ? 2 : 0) + (DROP ? 1 : 0);
     const RngKey key = rng_key(a.drop);
-    const uint32_t col = g * 8;
-    const int k = int(a.cols) - int(col);
-    f32x8 w, sum[3];
-    if (NORM)
-        w = load8_vector<T>(a.w, a.vec_f32, col, k, 1.0f);
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            sum[i][j] = 0.0f;
+    const uint32_t groups = (a.cols + 7) / 8;
+    const bool ragged = a.cols % 8 != 0;
+    const float one = opaque_one();
+    const Part<T, kWideBlock> at(blockIdx.x, threadIdx.x, a.cols);
+    struct Row {
+        V dy, r, dres;
+    };
+    auto fetch = [&](uint64_t row, Row& f) {
+        row = row < a.rows ? row : a.rows - 1;
+        f.dy = at.template load<kStreamed>(a.dy + row * a.ld_dy);
+        if (NORM) {
+            f.r = at.template load<kStreamed>(a.r + row * a.ld_r);
+            if (a.dres)
+                f.dres = at.template load<kStreamed>(a.dres + row * a.ld_dres);
+        }
+    };
     const uint64_t first = uint64_t(blockIdx.y) * a.rows_per_chunk;
     const uint64_t last = first + a.rows_per_chunk < a.rows ? first + a.rows_per_chunk : a.rows;
-    for (uint64_t row = first; row < last; ++row) {
-        f32x8 e = widen<T>(load8(a.dy + row * a.ld_dy + col, k));
+    Row buf[2];
+    fetch(first, buf[0]);
+    f32x8 w, sum[kSums];
+    if (NORM)
+        w = load8_vector<T>(a.w, a.vec_f32, at.group * 8, at.k, 1.0f);
+#pragma unroll
+    for (int q = 0; q < kSums; ++q)
+        sum[q] = splat(0.0f);
+    auto work = [&](uint64_t row, Row& cur) {
+        const V dy = at.settle(cur.dy, ragged);
+        f32x8 e;
         if (NORM) {
             const float mean = a.mean[row], rstd = a.rstd[row];
-            const float c1 = a.row_sums[2 * row], c2 = a.row_sums[2 * row + 1];
-            f32x8 r = widen<T>(load8(a.r + row * a.ld_r + col, k));
-            f32x8 t;
+            const float c0 = a.row_sums[2 * row], c1 = a.row_sums[2 * row + 1];
+            const f32x8 d = raw_times<T>(dy, rstd);
+            const f32x8 x = raw_plus<T>(at.template settle<false>(cur.r, ragged), splat(-mean), one), g = d * w;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float h = (r[j] - mean) * rstd;
-                sum[0][j] = __builtin_fmaf(e[j], h, sum[0][j]);
-                sum[1][j] += e[j];
-                t[j] = rstd * __builtin_fmaf(-h, c2, e[j] * w[j] - c1);
+                sum[0][j] = __builtin_fmaf(d[j], x[j], sum[0][j]);
+                e[j] = __builtin_fmaf(x[j], c1, g[j] + c0);
             }
-            e = t;
+            sum[1] = raw_plus<T>(dy, sum[1], one);
             if (a.dres)
-                e = e + widen<T>(load8(a.dres + row * a.ld_dres + col, k));
+                e = raw_plus<T>(at.template settle<false>(cur.dres, ragged), e, one);
+        } else {
+            e = widen<T>(dy);
         }
         if (DROP) {
             if (NORM)
-                store8(a.dr + row * a.ld_dr + col, narrow<T>(e), k);
-            e = dropped(e, a.drop, key, row * groups + g);
-            sum[2] = sum[2] + e;
+                at.template store<kStreamed>(a.dr + row * a.ld_dr, narrow<T>(e), true);
+            e = dropped(e, a.drop, key, row * groups + at.group);
+            sum[kSums - 1] = sum[kSums - 1] + e;
         }
-        store8(a.dx + row * a.ld_dx + col, narrow<T>(e), k);
+        at.template store<kStreamed>(a.dx + row * a.ld_dx, narrow<T>(e), true);
+    };
+    for (uint64_t row = first; row < last;) {
+        fetch(row + 1, buf[1]);
+        work(row, buf[0]);
+        if (++row >= last)
+            break;
+        fetch(row + 1, buf[0]);
+        work(row, buf[1]);
+        ++row;
     }
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-        if (a.want[i])
-            store8_f32(a.partials + (uint64_t(blockIdx.y) * 3 + i) * a.cols + col, sum[i], k);
+    for (int q = 0; q < kSums; ++q) {
+        const int which = NORM ? q : 2;
+        if (a.want[which])
+            store8_f32(a.partials + (uint64_t(blockIdx.y) * 3 + which) * a.cols + at.group * 8, sum[q], at.k);
+    }
 }
 
 // Adds the partials of each column in their order and stores the sum, or adds
@@ -375,27 +367,30 @@ struct BwdCall {
 };
 
 // The one-pass kernel: rows up to 8192 columns, one workgroup of 1024 threads
-// a CU, one group of 8 columns a thread.  Every workgroup costs a partial
-// (written and read again: as much as 2.4 joined rows of fp16), so there are no
-// more than 256, and only 128 where 256 would get no more than 1.5 blocks of
-// rows each.  Measured (kernel and fold, us, fp16): joined 8192 x 1600, 256 x
-// 4 rows of 256 threads 33.4, 512 workgroups of 512 threads 34.7, 128 threads
-// with two groups each 44.0; joined 16384 x 8192, 1024 threads x 1 group 237,
-// 512 x 2 254.  Layer norm, 128 against 256 workgroups at most: 200 x 8192
-// 12.7 and 15.1, 400 x 8192 15.0 and 17.6, 1000 x 1600 9.2 and 9.7, 800 x 8192
-// 18.4 and 17.4, 2000 x 1600 11.7 and 11.0.
+// a CU, one group of 8 columns a thread (with two a thread, rows up to 16384
+// columns spill the sums: layer norm 2048 x 12288 72 us and joined 175, against
+// 58 and 82 in two kernels).  Every workgroup costs a partial (written and read again: as much as 2.4 joined rows
+// of fp16), so there are no more than 256, and only 128 where 256 would get no
+// more than 1.5 blocks of rows each.  Measured (kernel and fold, us, fp16):
+// joined 8192 x 1600, 256 x 4 rows of 256 threads 33.4, 512 workgroups of 512
+// threads 34.7, 128 threads with two groups each 44.0; joined 16384 x 8192, 1024
+// threads x 1 group 237, 512 x 2 254.  Layer norm, 128 against 256 workgroups
+// at most: 200 x 8192 12.7 and 15.1, 400 x 8192 15.0 and 17.6, 1000 x 1600 9.2
+// and 9.7, 800 x 8192 18.4 and 17.4, 2000 x 1600 11.7 and 11.0.
 constexpr uint64_t kRowsMaxCols = 8192;
 constexpr int kRowsBlock = 1024;
 
 uint64_t rows_tpr(uint64_t cols)
 {
+    if (cols < 8)
+        return 1;
     uint64_t tpr = 8;
     while (tpr * 8 < cols)
         tpr *= 2;
     return tpr;
 }
 
-bool one_pass(uint64_t cols) { return cols >= 8 && cols <= kRowsMaxCols; }
+bool one_pass(uint64_t cols) { return cols <= kRowsMaxCols; }
 
 uint64_t rows_chunks(uint64_t rows, uint64_t cols)
 {
@@ -412,19 +407,19 @@ uint64_t workspace_need(uint64_t rows, uint64_t cols)
     return row_sums_bytes(rows, cols) + chunks * 3 * cols * 4;
 }
 
-// Two rows in flight ahead of the present one where the registers hold them
-// (layer norm alone, 16-bit elements: 8192 x 1600 21.8 us against 22.1 with one,
-// 1600 x 8192 28.5 against 29.3), else one.
+// Rows in flight ahead of the present one: as many as the registers hold
+// (layer norm alone, 16-bit elements, two: 8192 x 1600 21.8 us against 22.1 with
+// one, 1600 x 8192 28.5 against 29.3).
 template <typename T, bool NORM, bool DROP, int TPR>
 void launch_rows(const BwdArgs<T>& a, uint64_t chunks, hipStream_t s)
 {
-    constexpr int kBuffers = DROP || sizeof(T) == 4 ? 2 : 3;
+    constexpr int kBuffers = !NORM ? 4 : DROP || sizeof(T) == 4 ? 2 : 3;
     const uint64_t arrays = (NORM ? 3 + (a.dres != nullptr) : 2) + (NORM && DROP);
     if (a.rows * a.cols * sizeof(T) * arrays <= kStreamBytes)
-        hipLaunchKernelGGL((rows_bwd_kernel<T, NORM, DROP, kRowsBlock, TPR, 1, kBuffers, kCached>), dim3(uint32_t(chunks)),
-                           dim3(kRowsBlock), 0, s, a);
+        hipLaunchKernelGGL((rows_bwd_kernel<T, NORM, DROP, kRowsBlock, TPR, kBuffers, kCached>),
+                           dim3(uint32_t(chunks)), dim3(kRowsBlock), 0, s, a);
     else
-        hipLaunchKernelGGL((rows_bwd_kernel<T, NORM, DROP, kRowsBlock, TPR, 1, kBuffers, kStreamed>),
+        hipLaunchKernelGGL((rows_bwd_kernel<T, NORM, DROP, kRowsBlock, TPR, kBuffers, kStreamed>),
                            dim3(uint32_t(chunks)), dim3(kRowsBlock), 0, s, a);
 }
 
@@ -458,6 +453,7 @@ int run_bwd(const BwdCall& c, hipStream_t s)
     if (c.rows && one_pass(c.cols)) {
         chunks = rows_chunks(c.rows, c.cols);
         switch (rows_tpr(c.cols)) {
+        case 1: launch_rows<T, NORM, DROP, 1>(a, chunks, s); break;
         case 8: launch_rows<T, NORM, DROP, 8>(a, chunks, s); break;
         case 16: launch_rows<T, NORM, DROP, 16>(a, chunks, s); break;
         case 32: launch_rows<T, NORM, DROP, 32>(a, chunks, s); break;

@@ -545,48 +545,51 @@ def read_onebit_state(dev_onebit) -> OneBitState:
 # tensor lives on the current device, which the stream belongs to.
 
 _dtype_codes = None
+_torch = None
 
 
-def _layer_dtype(fn: str, t) -> int:
-    global _dtype_codes
-    if _dtype_codes is None:
-        import torch
-        _dtype_codes = {torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32}
-    code = _dtype_codes.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{fn}: {t.dtype} is not float16, bfloat16 or float32")
-    return code
+def _layer_setup():
+    global _dtype_codes, _torch
+    import torch
+    _torch = torch
+    _dtype_codes = {torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32}
 
 
 class _LayerCall:
-    """One call's shape (from its first matrix) and the checks of its tensors."""
-    __slots__ = ("fn", "rows", "cols", "dtype", "code", "device", "stream")
+    """One call's shape (from its first matrix) and the checks of its tensors.
+    A call's checks are most of its time on a small shape, so each reads as
+    few properties of a tensor as it can."""
+    __slots__ = ("fn", "shape", "rows", "cols", "dtype", "code", "device", "stream")
 
     def __init__(self, fn: str, ref, stream):
+        if _torch is None:
+            _layer_setup()
         if not ref.is_cuda:
             raise ValueError(f"{fn}: expected a device tensor")
-        if ref.dim() < 1:
+        self.fn, self.dtype, self.shape = fn, ref.dtype, ref.shape
+        code = _dtype_codes.get(self.dtype)
+        if code is None:
+            raise TypeError(f"{fn}: {self.dtype} is not float16, bfloat16 or float32")
+        self.code = code
+        if not self.shape:
             raise ValueError(f"{fn}: expected a matrix")
-        self.fn, self.dtype, self.code = fn, ref.dtype, _layer_dtype(fn, ref)
-        self.cols = ref.shape[-1]
-        self.rows = ref.numel() // self.cols if self.cols else 0
-        self.device = ref.get_device()
-        import torch
-        if self.device != torch.cuda.current_device():
-            raise ValueError(f"{fn}: the tensors are on device {self.device}, the current device is "
-                             f"{torch.cuda.current_device()}")
-        if stream is not None and stream.device_index != self.device:
-            raise ValueError(f"{fn}: the stream belongs to device {stream.device_index}, the tensors are on "
-                             f"{self.device}")
+        self.cols = cols = self.shape[-1]
+        self.rows = ref.numel() // cols if cols else 0
+        self.device = device = ref.get_device()
+        if device != _torch.cuda.current_device():
+            raise ValueError(f"{fn}: the tensors are on device {device}, the current device is "
+                             f"{_torch.cuda.current_device()}")
+        if stream is not None and stream.device_index != device:
+            raise ValueError(f"{fn}: the stream belongs to device {stream.device_index}, the tensors are on {device}")
         self.stream = _stream(stream)
 
     def mat(self, t) -> Tuple[int, int]:
         """(address, row stride in elements) of a rows x cols matrix; (0, 0) for None."""
         if t is None:
             return 0, 0
-        if t.get_device() != self.device or t.dtype != self.dtype:
+        if t.dtype is not self.dtype or t.get_device() != self.device:
             raise TypeError(f"{self.fn}: expected {self.dtype} on device {self.device}, got {t.dtype} on {t.device}")
-        if t.dim() < 1 or t.shape[-1] != self.cols or t.numel() != self.rows * self.cols:
+        if t.shape != self.shape and (t.dim() < 1 or t.shape[-1] != self.cols or t.numel() != self.rows * self.cols):
             raise ValueError(f"{self.fn}: expected {self.rows} x {self.cols} elements, got {tuple(t.shape)}")
         if t.is_contiguous():
             return t.data_ptr(), self.cols
@@ -594,33 +597,32 @@ class _LayerCall:
             raise ValueError(f"{self.fn}: expected a contiguous tensor, or a 2-D one with contiguous rows")
         return t.data_ptr(), t.stride(0)
 
-    def vecs(self, *ts) -> Tuple[int, ...]:
+    def vecs(self, *ts) -> List[int]:
         """The addresses of vectors over the columns (0 for None), then their one type."""
-        code, out = self.code, []
-        seen = None
+        out, seen = [], None
         for t in ts:
             if t is None:
                 out.append(0)
                 continue
-            if seen is not None and t.dtype != seen:
-                raise TypeError(f"{self.fn}: the vectors are {seen} and {t.dtype}: they share one type")
-            seen = t.dtype
-            code = _layer_dtype(self.fn, t)
-            if code not in (self.code, ZERO_F32):
-                raise TypeError(f"{self.fn}: vectors are {self.dtype} or torch.float32, got {t.dtype}")
+            if t.dtype is not seen:
+                if seen is not None:
+                    raise TypeError(f"{self.fn}: the vectors are {seen} and {t.dtype}: they share one type")
+                seen = t.dtype
+                if seen is not self.dtype and seen is not _torch.float32:
+                    raise TypeError(f"{self.fn}: vectors are {self.dtype} or torch.float32, got {seen}")
             if t.get_device() != self.device:
                 raise ValueError(f"{self.fn}: expected device {self.device}, got {t.device}")
             if t.numel() != self.cols or not t.is_contiguous():
                 raise ValueError(f"{self.fn}: expected a contiguous vector of {self.cols} elements")
             out.append(t.data_ptr())
-        return (*out, code)
+        out.append(self.code if seen is None or seen is self.dtype else ZERO_F32)
+        return out
 
     def stat(self, t) -> int:
         """The address of a float32 vector over the rows (0 for None)."""
         if t is None:
             return 0
-        import torch
-        if t.dtype != torch.float32 or t.get_device() != self.device:
+        if t.dtype is not _torch.float32 or t.get_device() != self.device:
             raise TypeError(f"{self.fn}: expected torch.float32 on device {self.device}, got {t.dtype} on {t.device}")
         if t.numel() != self.rows or not t.is_contiguous():
             raise ValueError(f"{self.fn}: expected a contiguous vector of {self.rows} elements (one per row)")
@@ -629,27 +631,28 @@ class _LayerCall:
     def rng(self, dev_rng) -> int:
         if dev_rng is None:
             return 0
-        if isinstance(dev_rng, int):
-            return dev_rng
-        _need(self.fn, dev_rng, RNG_BYTES)
         if dev_rng.get_device() != self.device:
             raise ValueError(f"{self.fn}: expected device {self.device}, got {dev_rng.device}")
-        return _ptr(dev_rng)
+        if dev_rng.numel() * dev_rng.element_size() < RNG_BYTES or not dev_rng.is_contiguous():
+            raise ValueError(f"{self.fn}: expected a contiguous generator state of {RNG_BYTES} bytes")
+        return dev_rng.data_ptr()
 
     def workspace(self, ws, stream):
         """(tensor, address, bytes).  None: taken from torch's allocator on the
         call's stream, so neither streams nor captured graphs share it."""
         if ws is None:
-            import torch
             need = max(16, lib().zero_layer_workspace_bytes(self.rows, self.cols))
             if stream is None:
-                ws = torch.empty(need, dtype=torch.uint8, device=f"cuda:{self.device}")
+                ws = _torch.empty(need, dtype=_torch.uint8, device=f"cuda:{self.device}")
             else:
-                with torch.cuda.stream(stream):
-                    ws = torch.empty(need, dtype=torch.uint8, device=f"cuda:{self.device}")
-        elif ws.get_device() != self.device:
+                with _torch.cuda.stream(stream):
+                    ws = _torch.empty(need, dtype=_torch.uint8, device=f"cuda:{self.device}")
+            return ws, ws.data_ptr(), need
+        if ws.get_device() != self.device:
             raise ValueError(f"{self.fn}: expected device {self.device}, got {ws.device}")
-        return ws, _ptr(ws), ws.numel() * ws.element_size()
+        if not ws.is_contiguous():
+            raise ValueError(f"{self.fn}: expected a contiguous workspace")
+        return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
     def check(self, rc: int) -> None:
         if rc != ZERO_OK:

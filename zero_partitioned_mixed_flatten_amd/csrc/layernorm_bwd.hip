@@ -204,7 +204,6 @@ __global__ __launch_bounds__(kWideBlock) void row_sums_kernel(BwdArgs<T> a)
     for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const float mean = a.mean[row], rstd = a.rstd[row];
         float c[2] = {0.0f, 0.0f};
-#pragma unroll 2
         for (uint32_t i = 0; i < rounds; ++i) {
             const P at(i, threadIdx.x, a.cols);
             const typename Raw<T>::type dy = at.template load<kCached>(a.dy + row * a.ld_dy);

@@ -27,6 +27,26 @@ __global__ void rng_init_kernel(zero_rng_t* r, uint64_t seed) { *r = zero_rng_t{
 
 __global__ void rng_advance_kernel(zero_rng_t* r) { r->step += 1; }
 
+// Division of 32-bit numbers by a number that is fixed for the launch, exact
+// for every dividend (Granlund and Montgomery 1994).
+struct Quotient {
+    uint32_t multiplier, shift1, shift2;
+    __device__ uint32_t operator()(uint32_t n) const
+    {
+        const uint32_t t = __umulhi(multiplier, n);
+        return (t + ((n - t) >> shift1)) >> shift2;
+    }
+};
+
+Quotient quotient_by(uint32_t d)
+{
+    uint32_t l = 0;
+    while ((uint64_t(1) << l) < d)
+        ++l;
+    const uint64_t m = ((uint64_t(1) << l) - d) * (uint64_t(1) << 32) / d + 1;
+    return Quotient{uint32_t(m), l < 1 ? l : 1, l > 0 ? l - 1 : 0};
+}
+
 template <typename T>
 struct DropoutArgs {
     T* out;
@@ -35,6 +55,7 @@ struct DropoutArgs {
     const void* bias;
     uint64_t ld_out, ld_x, ld_res;
     uint64_t rows, groups;                         // groups of 8 columns in a row
+    Quotient by_groups;
     uint32_t cols;
     bool bias_f32;
     Drop drop;
@@ -55,25 +76,30 @@ __device__ __forceinline__ typename Raw<T>::type settle16(typename Raw<T>::type 
 }
 
 // out = residual + D(x + bias), one group of 8 elements per thread: every
-// element is read once and written once, and the pass is bound by HBM.  The
-// loads come first, without a branch, so that they are in flight together.
-// NARROW: rows of fewer than 8 columns, loaded by elements.  Binary32 goes by
-// the traded pieces of layer.hpp, over the 64 consecutive groups of a wave
-// whatever rows they are in.
-template <typename T, int HINT, bool NARROW>
+// element is read once and written once, and the pass is bound by HBM.  A
+// workgroup lives for one load and one store, so what comes before its loads
+// counts: they come first, without a branch, after one multiplication in place
+// of a division and before the generator's state is waited for (16384 x 8192
+// fp16, no residual: 84.5 us = 6.35 TB/s; with a 64-bit division and the state
+// first 97.0 us; a copy 81.2 us).  NARROW: rows of fewer than 8 columns, loaded
+// by elements.  FAR: 2^32 groups or more, or more workgroups than a launch
+// takes (the grid then goes around).  Binary32 goes by the traded pieces of
+// layer.hpp, over the 64 consecutive groups of a wave whatever rows they are
+// in.
+template <typename T, int HINT, bool NARROW, bool FAR>
 __global__ __launch_bounds__(kDropBlock) void dropout_kernel(DropoutArgs<T> a)
 {
     typedef typename Raw<T>::type V;
     constexpr bool PIECES = sizeof(T) == 4 && !NARROW;
-    const RngKey key = rng_key(a.drop);
     const bool ragged = a.cols % 8 != 0;
     const float one = opaque_one();
     const uint32_t groups = uint32_t(a.groups), lane = threadIdx.x & 63;
-    const uint64_t total = a.rows * a.groups, stride = uint64_t(gridDim.x) * kDropBlock;
-    for (uint64_t base = uint64_t(blockIdx.x) * kDropBlock; base < total; base += stride) {
-        // the workgroup's first row and column by one scalar division, the
-        // thread's from there in 32 bits
-        const uint64_t row0 = base / a.groups;
+    const uint64_t total = FAR ? a.rows * a.groups : uint32_t(a.rows) * uint32_t(a.groups);
+    const uint64_t stride = uint64_t(gridDim.x) * kDropBlock;
+    uint64_t base = uint64_t(blockIdx.x) * kDropBlock;
+    do {
+        // the workgroup's first row and column, the thread's from there
+        const uint64_t row0 = FAR ? base / a.groups : a.by_groups(uint32_t(base));
         const uint32_t c0 = uint32_t(base - row0 * a.groups);
         auto locate = [&](uint32_t offset, uint64_t& row, uint32_t& c) {   // the group `offset` after the first
             row = row0;
@@ -83,7 +109,7 @@ __global__ __launch_bounds__(kDropBlock) void dropout_kernel(DropoutArgs<T> a)
                 row += wrap;
                 c -= wrap ? groups : 0;
             } else {
-                const uint32_t wrap = c / groups;
+                const uint32_t wrap = a.by_groups(c);
                 row += wrap;
                 c -= wrap * groups;
             }
@@ -128,7 +154,7 @@ __global__ __launch_bounds__(kDropBlock) void dropout_kernel(DropoutArgs<T> a)
             f32x8 v = splat(-0.0f);                // x + -0 is x, -0 too
             if (a.bias)
                 v = load8_vector<T>(a.bias, a.bias_f32, c * 8, int(a.cols) - int(c * 8), -0.0f);
-            v = dropped(settle(xp) + v, a.drop, key, base + mine);
+            v = dropped(settle(xp) + v, a.drop, rng_key(a.drop), base + mine);
             if (a.residual)
                 v = settle(rp) + v;
             Words w = __builtin_bit_cast(Words, v);
@@ -142,7 +168,7 @@ __global__ __launch_bounds__(kDropBlock) void dropout_kernel(DropoutArgs<T> a)
             }
         } else {
             if (base + mine >= total)
-                return;
+                continue;
             locate(mine, row, c);
             const Group at = NARROW ? Group{0, 0, int(a.cols)} : group_at(c * 8, a.cols);
             if (NARROW) {
@@ -162,12 +188,12 @@ __global__ __launch_bounds__(kDropBlock) void dropout_kernel(DropoutArgs<T> a)
                 if (a.residual)
                     res = settle16<T>(res, at.shift);
             }
-            v = dropped(raw_plus<T>(x, v, one), a.drop, key, base + mine);
+            v = dropped(raw_plus<T>(x, v, one), a.drop, rng_key(a.drop), base + mine);
             if (a.residual)
                 v = raw_plus<T>(res, v, one);
             store8<HINT>(a.out + row * a.ld_out + c * 8, narrow<T>(v), at.k);
         }
-    }
+    } while (FAR && (base += stride) < total);
 }
 
 template <typename T>
@@ -175,17 +201,23 @@ int launch(void* out, uint64_t ld_out, const void* x, uint64_t ld_x, const void*
            const void* bias, int bias_dtype, uint64_t rows, uint64_t cols, const Drop& d, hipStream_t s)
 {
     DropoutArgs<T> a{static_cast<T*>(out), static_cast<const T*>(x), static_cast<const T*>(residual), bias,
-                     ld_out, ld_x, ld_res, rows, (cols + 7) / 8, uint32_t(cols), bias_dtype == ZERO_F32, d};
-    uint64_t grid = (a.rows * a.groups + kDropBlock - 1) / kDropBlock;
-    if (grid > (1u << 22))
-        grid = 1u << 22;
+                     ld_out, ld_x, ld_res, rows, (cols + 7) / 8, quotient_by(uint32_t((cols + 7) / 8)), uint32_t(cols),
+                     bias_dtype == ZERO_F32, d};
+    const uint64_t grid = (rows * a.groups + kDropBlock - 1) / kDropBlock;
     const uint64_t bytes = rows * cols * sizeof(T) * (residual ? 3 : 2);
-    if (cols < 8)
-        hipLaunchKernelGGL((dropout_kernel<T, kCached, true>), dim3(uint32_t(grid)), dim3(kDropBlock), 0, s, a);
+    constexpr uint64_t kMost = 1u << 22;
+    const dim3 block(kDropBlock);
+    if (grid > kMost) {
+        if (cols < 8)
+            hipLaunchKernelGGL((dropout_kernel<T, kStreamed, true, true>), dim3(kMost), block, 0, s, a);
+        else
+            hipLaunchKernelGGL((dropout_kernel<T, kStreamed, false, true>), dim3(kMost), block, 0, s, a);
+    } else if (cols < 8)
+        hipLaunchKernelGGL((dropout_kernel<T, kCached, true, false>), dim3(uint32_t(grid)), block, 0, s, a);
     else if (bytes <= kStreamBytes)
-        hipLaunchKernelGGL((dropout_kernel<T, kCached, false>), dim3(uint32_t(grid)), dim3(kDropBlock), 0, s, a);
+        hipLaunchKernelGGL((dropout_kernel<T, kCached, false, false>), dim3(uint32_t(grid)), block, 0, s, a);
     else
-        hipLaunchKernelGGL((dropout_kernel<T, kStreamed, false>), dim3(uint32_t(grid)), dim3(kDropBlock), 0, s, a);
+        hipLaunchKernelGGL((dropout_kernel<T, kStreamed, false, false>), dim3(uint32_t(grid)), block, 0, s, a);
     return launch_status();
 }
 

@@ -212,34 +212,42 @@ __global__ __launch_bounds__(kWideBlock) void norm_fwd_wide_kernel(FwdArgs<T> a)
 
 // The threads of a row: one below 8 columns; as few powers of two as hold its
 // groups one each up to a wave; wider rows take two groups a thread and whole
-// waves, at least two.  The workgroup is one row, or as
-// many as make 256 threads.  Grid: the workgroups that 1024 threads a CU make
-// with two groups each, 1536 with one, all resident at once, and no more than
-// there are blocks of rows.  Measured at 13.1 M fp16 elements (layer norm /
-// joined, us; two copies of the same bytes take 10.6 / 21.1): 512 columns 12.8
-// / 22.7, 64 threads x 1, against 13.1 / 23.6 with 32 x 2; 1600 columns 13.7 /
-// 24.2, 128 x 2, against 14.6 / 25.6 with 256 x 1 and 14.9 / 29.2 with 64 x 4;
-// 8192 columns 13.1 / 23.8, 512 x 2, against 14.5 / 27.0 with 1024 x 1 and 15.1
-// / 26.8 with 256 x 4.  Grid, 512 columns: 13.2 / 23.0 with 1024 threads a CU,
-// 12.6 / 24.8 with 2048; 1600 columns: 15.4 / 26.4 with 1536, 16.6 / 28.9 with
-// 512.
+// waves, at least two.  The workgroup is one row, or as many as make 256
+// threads.  Measured at 13.1 M fp16 elements (layer norm / joined, us; a copy
+// and two copies of the same bytes take 10.6 / 21.1): 512 columns 12.8 / 22.7,
+// 64 threads x 1, against 13.1 / 23.6 with 32 x 2; 1600 columns 13.7 / 24.2,
+// 128 x 2, against 14.6 / 25.6 with 256 x 1 and 14.9 / 29.2 with 64 x 4; 8192
+// columns 13.1 / 23.8, 512 x 2, against 14.5 / 27.0 with 1024 x 1 and 15.1 / 26.8
+// with 256 x 4.
+//
+// The grid: what is resident at once with the registers each form takes, and
+// no more than there are blocks of rows; workgroups that wait for a place
+// leave the last ones running alone.  Threads a CU, layer norm, plain loads:
+// 512 columns 2048 10.5 us, 1536 11.1, 1024 11.4; 1600 columns 1536 10.8, 1024
+// 11.7, 768 12.0; joined, 1600 columns: 1024 24.2, 768 24.7, 2048 26.5.  Past
+// the cache two groups a thread do better with 1024 (16384 x 8192: 92 us, 1536
+// 101).
 constexpr uint64_t kCus = 256;
+
+template <typename T, bool JOIN, int TPR, int VPT, int HINT>
+void launch_hinted(const FwdArgs<T>& a, hipStream_t s)
+{
+    constexpr int kBlock = TPR < 192 ? 256 : TPR;
+    constexpr int kThreads = VPT == 1 ? (JOIN ? 1536 : 2048) : JOIN || sizeof(T) == 4 || HINT == kStreamed ? 1024 : 1536;
+    constexpr uint64_t kMost = kCus * (kThreads / kBlock);
+    const uint64_t blocks = (a.rows + kBlock / TPR - 1) / (kBlock / TPR);
+    hipLaunchKernelGGL((norm_fwd_kernel<T, JOIN, kBlock, TPR, VPT, HINT>), dim3(uint32_t(blocks < kMost ? blocks : kMost)),
+                       dim3(kBlock), 0, s, a);
+}
 
 template <typename T, bool JOIN, int TPR, int VPT>
 int launch_rows(const FwdArgs<T>& a, hipStream_t s)
 {
-    constexpr int kBlock = TPR < 192 ? 256 : TPR;
-    constexpr uint64_t kMost = kCus * ((VPT == 1 ? 1536 : 1024) / kBlock);
-    uint64_t grid = (a.rows + kBlock / TPR - 1) / (kBlock / TPR);
-    if (grid > kMost)
-        grid = kMost;
     const uint64_t bytes = a.rows * a.cols * sizeof(T) * (JOIN ? (a.residual ? 4 : 3) : 2);
     if (bytes <= kStreamBytes)
-        hipLaunchKernelGGL((norm_fwd_kernel<T, JOIN, kBlock, TPR, VPT, kCached>), dim3(uint32_t(grid)), dim3(kBlock), 0, s,
-                           a);
+        launch_hinted<T, JOIN, TPR, VPT, kCached>(a, s);
     else
-        hipLaunchKernelGGL((norm_fwd_kernel<T, JOIN, kBlock, TPR, VPT, kStreamed>), dim3(uint32_t(grid)), dim3(kBlock), 0,
-                           s, a);
+        launch_hinted<T, JOIN, TPR, VPT, kStreamed>(a, s);
     return launch_status();
 }
 

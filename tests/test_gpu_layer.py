@@ -673,3 +673,122 @@ def test_many_rows(rows, cols):
     close(dx, want[0], O.stored(bound[0], want[0], "f32"), "dx")
     close(dw, want[1], O.stored(bound[1], want[1], "f32"), "dw")
     close(db, want[2], O.stored(bound[2], want[2], "f32"), "db")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("cols", [9, 100, 255, 300, 511, 700, 1024, 1100, 2048, 2500, 3500, 5120, 6000, 7000, 8191, 8193, 10000,
+                                  12000, 15000, 16384, 16385])
+def test_every_width_class(cols, kind):
+    """Each number of threads a row can have, in the forward and backward
+    passes, with more rows than one workgroup holds."""
+    rows = 5 if cols > 1000 else 150
+    log("width", cols, kind)
+    g = gen("width", cols, kind)
+    x, res = matrix(g, rows, cols, kind, 1.0, 0.2), matrix(g, rows, cols, kind, 2.0, pad=1)
+    bias, w, b = vector(g, cols, "f32", 0.0, 0.3), vector(g, cols, "f32", 1.0, 0.3), vector(g, cols, "f32", 0.0, 0.3)
+    rng = rng_state(SEED, 1)
+    r, y = empty(rows, cols, kind), empty(rows, cols, kind, pad=2)
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    Z.zero_dropout_layernorm_fwd(r, y, mean, rstd, x, res, bias, w, b, EPS, 0.25, rng, 2)
+    kept, s = O.keep(rows, cols, 0.25, SEED, 1, 2), O.scale(0.25)
+    same_bits(r, expect_r(x, res, bias, kept, s), "r")
+    _check_fwd(r, y, mean, rstd, w, b, kind)
+    y2, m2, s2 = empty(rows, cols, kind), torch.empty_like(mean), torch.empty_like(rstd)
+    Z.zero_layernorm_fwd(y2, m2, s2, r, w, b, EPS)
+    _check_fwd(r, y2, m2, s2, w, b, kind)
+    dy, dres = matrix(g, rows, cols, kind, 0.5), matrix(g, rows, cols, kind, 0.5)
+    dx, dr = empty(rows, cols, kind, pad=1), empty(rows, cols, kind)
+    sums = [torch.empty(cols, device="cuda") for _ in range(3)]
+    Z.zero_dropout_layernorm_bwd(dx, dr, *sums, dy, dres, r, mean, rstd, w, 0.25, rng, 2,
+                                 workspace=dirty_workspace(rows, cols))
+    want, bound = O.norm_bwd(f64(dy), f64(r), f64(mean), f64(rstd), f64(w)[None], f64(dres))
+    e, e_e = want[0], 1.01 * bound[0]
+    close(dr, e, O.stored(e_e, e, kind), "dr")
+    d = O.dropped(e, kept, s)
+    e_d = O.dropped(e_e, kept, s) + O.U * np.abs(d)
+    close(dx, d, O.stored(e_d, d, kind), "dx")
+    close(sums[0], want[1], O.stored(bound[1], want[1], "f32"), "dw")
+    close(sums[1], want[2], O.stored(bound[2], want[2], "f32"), "db")
+    t, e_t = O.column_sum(d, e_d)
+    close(sums[2], t, O.stored(e_t, t, "f32"), "dbias")
+    dx2, dw2 = empty(rows, cols, kind), torch.empty(cols, device="cuda")
+    Z.zero_layernorm_bwd(dx2, dw2, None, dy, r, mean, rstd, w, dres=dres, workspace=dirty_workspace(rows, cols))
+    close(dx2, e, O.stored(e_e, e, kind), "dx of the layer norm alone")
+    close(dw2, want[1], O.stored(bound[1], want[1], "f32"), "dw of the layer norm alone")
+
+
+@pytest.mark.parametrize("rows,cols,kind", [(36000, 1601, "f16"), (36000, 1600, "bf16"), (300_001, 70, "f32"),
+                                            (7000, 8192, "f16"), (9_000_001, 3, "f32"), (2100, 12001, "f32")])
+def test_past_the_cache(rows, cols, kind):
+    """Calls that move more than the cache holds (their loads take the other
+    hint, and a workgroup many blocks of rows): the first, middle and last
+    rows against the 64-bit forms, the sums over all rows against sums in 64
+    bits on the device."""
+    log("past the cache", rows, cols, kind)
+    gg = torch.Generator("cuda")
+    gg.manual_seed(rows + cols)
+    make = lambda s: (torch.randn(rows, cols, device="cuda", generator=gg) * s).to(KINDS[kind])
+    x, res, dy, dres = make(1.0), make(2.0), make(0.5), make(0.5)
+    g = gen("past", rows, cols)
+    bias, w, b = vector(g, cols, "f32", 0.0, 0.3), vector(g, cols, "f32", 1.0, 0.3), vector(g, cols, "f32", 0.0, 0.3)
+    rng = rng_state(SEED, 1)
+    r, y, out, dx, dr = (torch.empty_like(x) for _ in range(5))
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    Z.zero_dropout_layernorm_fwd(r, y, mean, rstd, x, res, bias, w, b, EPS, 0.25, rng, 2)
+    Z.zero_dropout_fwd(out, x, 0.25, rng, 2, residual=res, bias=bias)
+    assert torch.equal(out, r)
+    y2 = torch.empty_like(x)
+    Z.zero_layernorm_fwd(y2, None, None, r, w, b, EPS)
+    assert torch.equal(y2, y)
+    sums = [torch.empty(cols, device="cuda") for _ in range(3)]
+    Z.zero_dropout_layernorm_bwd(dx, dr, *sums, dy, dres, r, mean, rstd, w, 0.25, rng, 2,
+                                 workspace=dirty_workspace(rows, cols))
+    s = O.scale(0.25)
+    for first in (0, rows // 2, rows - 40):
+        at = slice(first, first + 40)
+        kept = O.keep(40, cols, 0.25, SEED, 1, 2, first_row=first)
+        same_bits(r[at], expect_r(x[at], res[at], bias, kept, s), "r")
+        _check_fwd(r[at], y[at], mean[at], rstd[at], w, b, kind)
+        want, bound = O.norm_bwd(f64(dy[at]), f64(r[at]), f64(mean[at]), f64(rstd[at]), f64(w)[None], f64(dres[at]))
+        e, e_e = want[0], 1.01 * bound[0]
+        close(dr[at], e, O.stored(e_e, e, kind), "dr")
+        d = O.dropped(e, kept, s)
+        close(dx[at], d, O.stored(O.dropped(e_e, kept, s) + O.U * np.abs(d), d, kind), "dx")
+    # sums: d = rows / 256 + 40 additions in a chain is still far above what a column takes; bounded by all of them
+    chain = (rows + 32.0) * O.U
+    h = (r.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    for name, got, term in (("dw", sums[0], dy.double() * h), ("db", sums[1], dy.double())):
+        close(got, f64(term.sum(0)), f64(term.abs().sum(0)) * min(chain, 1e-3) + 1e-30, name)
+    del h
+    # dbias: the stored dx is off by half a step of its type from what is summed
+    t = dx.double()
+    close(sums[2], f64(t.sum(0)), f64(t.abs().sum(0)) * (min(chain, 1e-3) + 1.01 * O.half_step(kind)) + 1e-30, "dbias")
+    # the other backward passes over the same rows
+    Z.zero_layernorm_bwd(y2, sums[0], sums[1], dy, r, mean, rstd, w, dres=dres)
+    same = (y2 == dr) | ((y2.float() - dr.float()).abs() <= dr.float().abs() * 4 * O.half_step(kind) + 1e-6)
+    assert bool(same.all())
+    t = out
+    Z.zero_dropout_bwd(t, dy, 0.25, rng, 2, dbias=sums[2])
+    close(sums[2], f64(t.double().sum(0)), f64(t.double().abs().sum(0)) * (min(chain, 1e-3) + 1.01 * O.half_step(kind))
+          + 1e-30, "dbias of dropout alone")
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_subnormal_values(kind):
+    """Values below the type's smallest normal one go through as they are (no
+    flush to zero on any path)."""
+    rows, cols = 7, 333
+    g = gen("subnormal", kind)
+    tiny = {"f16": 2.0 ** -20, "bf16": 2.0 ** -130}[kind]
+    x, dy = matrix(g, rows, cols, kind, tiny), matrix(g, rows, cols, kind, tiny)
+    out = empty(rows, cols, kind)
+    log("subnormal", kind)
+    Z.zero_dropout_fwd(out, x, 0.5, rng_state(SEED, 0), 1, residual=dy)
+    same_bits(out, expect_r(x, dy, None, O.keep(rows, cols, 0.5, SEED, 0, 1), 2.0), "out")
+    r = matrix(g, rows, cols, kind, 1.0)
+    mean, rstd = _stats(r)
+    dx, db = empty(rows, cols, kind), torch.empty(cols, device="cuda")
+    Z.zero_layernorm_bwd(dx, None, db, dy, r, mean, rstd, None)
+    want, bound = O.norm_bwd(f64(dy), f64(r), f64(mean), f64(rstd), np.ones((1, cols)), None)
+    close(dx, want[0], O.stored(bound[0] + 2.0 ** -149 * cols, want[0], kind), "dx")
+    close(db, want[2], O.stored(bound[2], want[2], "f32"), "db")

@@ -224,6 +224,10 @@ def test_workspace_size(Z):
     assert W(0, 64) == 0 and W(64, 0) == 0 and W((1 << 40) + 1, 8) == 0 and W(8, (1 << 30) + 1) == 0
     for rows, cols in ((1, 1), (1, 8192), (7, 1601), (16384, 8192), (1 << 20, 64), (1 << 40, 1)):
         assert W(rows, cols) == W(rows, cols) > 0
+    last = 0
+    for rows in [*range(1, 3000), *range(3000, 70_000, 97)]:        # never less for more rows
+        assert W(rows, 1600) >= last
+        last = W(rows, 1600)
     # at the largest sizes it stays a small part of the matrices' own bytes
     assert W(16384, 8192) < 16384 * 8192 * 2
 

@@ -1,4 +1,5 @@
-"""MI355X-native ZeRO partitioned mixed-precision Adam shard step.
+"""MI355X-native ZeRO partitioned mixed-precision Adam shard step, and the
+layer operators of a block's residual stream that produce gradients for it.
 
 The computation is HIP kernels for gfx950 behind the C ABI declared in
 include/zero_mi355x.h (libzero_mi355x.so, built in-tree); this package is the
@@ -20,6 +21,7 @@ from ._lib import (EXPORTS, NORM_PARTIAL_BYTES, ONEBIT_STATE_BYTES, RNG_BYTES, S
                    zero_status_string, zero_step_state_init,
                    zero_stream_copy, zero_host_create, zero_host_destroy, zero_host_threads, zero_host_state_init,
                    zero_host_norm_overflow, zero_host_adam_step, zero_offload_step, zero_host_stream_copy)
+from .layers import LayerRng, ResidualNorm
 from .stepper import AccumStep, HostContext, OffloadStep, OneBitStep, ShardStep, hparams
 
 lib()
@@ -37,4 +39,5 @@ __all__ = ["EXPORTS", "NORM_PARTIAL_BYTES", "STATE_BYTES", "ZERO_F16", "ZERO_F32
            "OneBitStep", "read_onebit_state", "zero_onebit_state_init", "zero_onebit_step",
            "zero_onebit_workspace_bytes", "RNG_BYTES", "RngState", "read_rng", "zero_rng_init", "zero_rng_advance",
            "zero_dropout_fwd", "zero_dropout_bwd", "zero_layernorm_fwd", "zero_layernorm_bwd",
-           "zero_dropout_layernorm_fwd", "zero_dropout_layernorm_bwd", "zero_layer_workspace_bytes"]
+           "zero_dropout_layernorm_fwd", "zero_dropout_layernorm_bwd", "zero_layer_workspace_bytes", "LayerRng",
+           "ResidualNorm"]

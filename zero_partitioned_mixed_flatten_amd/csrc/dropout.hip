@@ -154,7 +154,7 @@ __global__ __launch_bounds__(kDropBlock) void dropout_kernel(DropoutArgs<T> a)
             f32x8 v = splat(-0.0f);                // x + -0 is x, -0 too
             if (a.bias)
                 v = load8_vector<T>(a.bias, a.bias_f32, c * 8, int(a.cols) - int(c * 8), -0.0f);
-            v = dropped(settle(xp) + v, a.drop, rng_key(a.drop), base + mine);
+            v = dropped(settle(xp) + v, a.drop, mask_bits(a.drop, rng_key(a.drop), base + mine));
             if (a.residual)
                 v = settle(rp) + v;
             Words w = __builtin_bit_cast(Words, v);
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kDropBlock) void dropout_kernel(DropoutArgs<T> a)
                 if (a.residual)
                     res = settle16<T>(res, at.shift);
             }
-            v = dropped(raw_plus<T>(x, v, one), a.drop, rng_key(a.drop), base + mine);
+            v = dropped(raw_plus<T>(x, v, one), a.drop, mask_bits(a.drop, rng_key(a.drop), base + mine));
             if (a.residual)
                 v = raw_plus<T>(res, v, one);
             store8<HINT>(a.out + row * a.ld_out + c * 8, narrow<T>(v), at.k);

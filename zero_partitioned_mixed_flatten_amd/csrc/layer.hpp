@@ -437,17 +437,25 @@ __device__ __forceinline__ u32x4 philox(RngKey key, uint32_t site, uint64_t grou
     return u32x4{c0, c1, c2, c3};
 }
 
+// The random bits of a group, which depend on nothing that is loaded: a pass
+// draws them while its loads are on their way.
+__device__ __forceinline__ u32x4 mask_bits(const Drop& d, RngKey key, uint64_t group)
+{
+    if (d.threshold - 1 > 0xfffeu)                 // none or all dropped
+        return u32x4{0, 0, 0, 0};
+    return philox(key, d.site, group);
+}
+
 // D(v): a dropped element is 0 whatever it holds (a select, not a product, so
 // an inf or NaN there does not come through).  The 16-bit words are compared
 // in the upper half of a register: the odd ones as they are, what is below
 // them does not change the order.
-__device__ __forceinline__ f32x8 dropped(f32x8 v, const Drop& d, RngKey key, uint64_t group)
+__device__ __forceinline__ f32x8 dropped(f32x8 v, const Drop& d, u32x4 bits)
 {
     if (!d.threshold)
         return v;
     if (d.threshold > 0xffffu)
         return splat(0.0f);
-    const u32x4 bits = philox(key, d.site, group);
     const uint32_t limit = d.threshold << 16;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {

@@ -87,6 +87,11 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
         if (first + stride < a.rows)
             fetch(row + stride, next);
         const bool live = row < a.rows;
+        u32x4 bits[VPT];
+        if (JOIN)
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                bits[i] = mask_bits(a.drop, key, row * groups + part(i).group);
         V raw[VPT];                                // 0 past the row's end, the sum needs no test
         f32x8 x[VPT];
         float s[1] = {0.0f}, q[1] = {0.0f};
@@ -96,7 +101,7 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
             raw[i] = at.settle(cur.x[i], ragged);
             if (JOIN) {
                 f32x8 v = raw_plus<T>(raw[i], bias[i], one);
-                v = dropped(v, a.drop, key, row * groups + at.group);
+                v = dropped(v, a.drop, bits[i]);
                 if (a.residual)
                     v = raw_plus<T>(at.settle(cur.res[i], ragged), v, one);
                 raw[i] = narrow<T>(v);
@@ -168,7 +173,7 @@ __global__ __launch_bounds__(kWideBlock) void norm_fwd_wide_kernel(FwdArgs<T> a)
             if (JOIN) {
                 const Group g = group_at(at.group * 8, a.cols);
                 f32x8 v = raw_plus<T>(raw, load8_vector_at<T>(a.bias, a.vec_f32, g, ragged, -0.0f), one);
-                v = dropped(v, a.drop, key, row * groups + at.group);
+                v = dropped(v, a.drop, mask_bits(a.drop, key, row * groups + at.group));
                 if (a.residual)
                     v = raw_plus<T>(at.settle(res, ragged), v, one);
                 if (at.k <= 0)

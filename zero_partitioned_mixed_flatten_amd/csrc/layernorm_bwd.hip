@@ -86,6 +86,12 @@ __global__ __launch_bounds__(BLOCK) void rows_bwd_kernel(BwdArgs<T> a)
         sum[q] = splat(0.0f);
     auto work = [&](uint64_t row, Row& cur) {
         const bool live = row < a.rows;
+        // the mask ahead of the loads' use; binary32 rows leave no registers to
+        // keep it (8192 x 1600 joined 63 us so, 56 with it drawn at the end)
+        constexpr bool kEarly = sizeof(T) == 2;
+        u32x4 bits;
+        if (DROP && kEarly)
+            bits = mask_bits(a.drop, key, row * groups + at.group);
         const V dy = at.settle(cur.dy, ragged);    // 0 past the row's end
         f32x8 e;
         if (NORM) {
@@ -122,7 +128,9 @@ __global__ __launch_bounds__(BLOCK) void rows_bwd_kernel(BwdArgs<T> a)
         if (DROP) {
             if (NORM)
                 at.template store<HINT>(a.dr + row * a.ld_dr, narrow<T>(e), live);
-            e = dropped(e, a.drop, key, row * groups + at.group);
+            if (!kEarly)
+                bits = mask_bits(a.drop, key, row * groups + at.group);
+            e = dropped(e, a.drop, bits);
             if (live)
                 sum[kSums - 1] = sum[kSums - 1] + e;
         }
@@ -258,6 +266,9 @@ __global__ __launch_bounds__(kWideBlock) void strips_kernel(BwdArgs<T> a)
     for (int q = 0; q < kSums; ++q)
         sum[q] = splat(0.0f);
     auto work = [&](uint64_t row, Row& cur) {
+        u32x4 bits;
+        if (DROP)
+            bits = mask_bits(a.drop, key, row * groups + at.group);
         const V dy = at.settle(cur.dy, ragged);
         f32x8 e;
         if (NORM) {
@@ -279,7 +290,7 @@ __global__ __launch_bounds__(kWideBlock) void strips_kernel(BwdArgs<T> a)
         if (DROP) {
             if (NORM)
                 at.template store<kStreamed>(a.dr + row * a.ld_dr, narrow<T>(e), true);
-            e = dropped(e, a.drop, key, row * groups + at.group);
+            e = dropped(e, a.drop, bits);
             sum[kSums - 1] = sum[kSums - 1] + e;
         }
         at.template store<kStreamed>(a.dx + row * a.ld_dx, narrow<T>(e), true);
@@ -301,44 +312,44 @@ __global__ __launch_bounds__(kWideBlock) void strips_kernel(BwdArgs<T> a)
     }
 }
 
-// Adds the partials of each column in their order and stores the sum, or adds
-// it to what is there, rounded once to the gradient's type.  A workgroup
-// takes 64 columns; each of its 16 waves adds every 16th partial, its loads in
-// flight together, and the waves' sums are added in order.
+// Adds the partials of each column in a fixed order and stores the sum, or adds
+// it to what is there, rounded once to the gradient's type.  A workgroup takes
+// 32 columns; each of its 32 half waves adds every 32nd partial, its loads in
+// flight together (all of them up to 256 partials), and the half waves' sums
+// are added in order.
 constexpr int kFoldBlock = 1024;
-constexpr uint32_t kFoldCols = 64;
+constexpr uint32_t kFoldCols = 32;
 
 template <typename T>
 __global__ __launch_bounds__(kFoldBlock) void fold_kernel(SumOut out, const float* __restrict__ partials, uint32_t chunks,
                                                           uint32_t cols)
 {
-    __shared__ float part[kFoldBlock / 64][kFoldCols];
+    constexpr uint32_t kParts = kFoldBlock / kFoldCols;
+    __shared__ float part[kParts][kFoldCols];
     const int i = blockIdx.y;
     if (!out.dst[i])
         return;
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t lane = threadIdx.x % kFoldCols, first = threadIdx.x / kFoldCols;
     const uint32_t col = blockIdx.x * kFoldCols + lane;
     float s = 0.0f;
     if (col < cols) {
         const float* p = partials + uint64_t(i) * cols + col;
         const uint64_t step = uint64_t(3) * cols;
-        for (uint32_t c = wave; c < chunks; c += 8 * 16) {
+        for (uint32_t c = first; c < chunks; c += 8 * kParts) {
             float v[8];
 #pragma unroll
             for (uint32_t u = 0; u < 8; ++u)
-                v[u] = c + 16 * u < chunks ? p[(c + 16 * u) * step] : 0.0f;
-#pragma unroll
-            for (uint32_t u = 0; u < 8; ++u)
-                s += v[u];
+                v[u] = c + kParts * u < chunks ? p[(c + kParts * u) * step] : 0.0f;
+            s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
         }
     }
-    part[wave][lane] = s;
+    part[first][lane] = s;
     __syncthreads();
-    if (wave || col >= cols)
+    if (first || col >= cols)
         return;
     s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kFoldBlock / 64; ++k)
+    for (uint32_t k = 0; k < kParts; ++k)
         s += part[k][lane];
     if (out.f32) {
         float* d = static_cast<float*>(out.dst[i]) + col;

@@ -225,8 +225,11 @@ struct Part {
             Words x = __builtin_bit_cast(Words, v);
 #pragma unroll
             for (int p = 0; p < kPieces; ++p) {
-                if (ragged)
-                    shift_down<kWords, 8 * int(sizeof(T))>(x.d[p], shift[p]);
+                if (ragged) {
+                    uint32_t by = shift[p];
+                    asm volatile("" : "+v"(by));   // its tests stay in this branch
+                    shift_down<kWords, 8 * int(sizeof(T))>(x.d[p], by);
+                }
                 if (ZERO)
 #pragma unroll
                     for (int i = 0; i < kWords; ++i)
@@ -423,7 +426,10 @@ __device__ __forceinline__ RngKey rng_key(const Drop& d)
 __device__ __forceinline__ u32x4 philox(RngKey key, uint32_t site, uint64_t group)
 {
     uint32_t c0 = uint32_t(group), c1 = uint32_t(group >> 32), c2 = site, c3 = key.step;
-    uint32_t k0 = key.k0, k1 = key.k1;
+    uint32_t k0 = __builtin_amdgcn_readfirstlane(key.k0), k1 = __builtin_amdgcn_readfirstlane(key.k1);
+    // the ten rounds' keys are scalar additions next to the vector work; kept
+    // from one call to the next they would push other scalars out
+    asm volatile("" : "+s"(k0), "+s"(k1));
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t a = uint64_t(0xD2511F53u) * c0, b = uint64_t(0xCD9E8D57u) * c2;

@@ -45,6 +45,9 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
     typedef typename Raw<T>::type V;
     typedef Part<T, TPR> P;
     constexpr int kRows = BLOCK / TPR;
+    // r of a joined 16-bit row is made 0 past the row's end once, when it is
+    // rounded, instead of x and residual
+    constexpr bool kZero = !JOIN || sizeof(T) == 4;
     __shared__ alignas(16) float scratch[2 * BLOCK / 64];
     uint32_t parity = 0;
     const RngKey key = rng_key(a.drop);
@@ -93,23 +96,27 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
             for (int i = 0; i < VPT; ++i)
                 bits[i] = mask_bits(a.drop, key, row * groups + part(i).group);
         V raw[VPT];                                // 0 past the row's end, the sum needs no test
-        f32x8 x[VPT];
+        f32x8 x[VPT], s8;
         float s[1] = {0.0f}, q[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const P at = part(i);
-            raw[i] = at.settle(cur.x[i], ragged);
+            raw[i] = at.template settle<kZero>(cur.x[i], ragged);
             if (JOIN) {
                 f32x8 v = raw_plus<T>(raw[i], bias[i], one);
                 v = dropped(v, a.drop, bits[i]);
                 if (a.residual)
-                    v = raw_plus<T>(at.settle(cur.res[i], ragged), v, one);
+                    v = raw_plus<T>(at.template settle<kZero>(cur.res[i], ragged), v, one);
                 raw[i] = narrow<T>(v);
+                if (!kZero && at.k < 8)            // a short or absent group: 0 past the row's end
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        raw[i][j] = j < at.k ? raw[i][j] : T(0.0f);
                 at.template store<HINT>(a.r + row * a.ld_r, raw[i], live);
             }
-            const f32x8 v = widen<T>(raw[i]);
-            s[0] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+            s8 = i ? raw_plus<T>(raw[i], s8, one) : widen<T>(raw[i]);
         }
+        s[0] = ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
         row_sum<BLOCK, TPR>(s, scratch, parity);
         const float mean = over(s[0], n, inv);
         float qb = 0.0f;

@@ -577,11 +577,12 @@ int zero_host_stream_copy(zero_host_ctx_t* ctx, void* dst, const void* src, uint
  *   - an output matrix may be one of the call's input matrices (the same
  *     address and ld); two outputs must differ, and any other overlap of an
  *     output with another argument gives undefined results;
+ *   - the stream belongs to the current device, and so does every pointer;
  *   - rows may be 0 (then the row sums dw, db, dbias are sums of nothing: 0, or
  *     with accumulate left as they are);
  *   - results do not depend on timing: equal calls give equal bits.
  * Errors of all of them: ZERO_EINVAL (a required pointer NULL with rows > 0,
- * a bad type, two equal outputs, eps not finite and > 0 in binary32, p not in
+ * a bad type, two equal outputs (mean and rstd among them), eps not finite and > 0 in binary32, p not in
  * [0, 1]), ZERO_EALIGN, ZERO_ERANGE (rows > 2^40, cols > 2^30, cols = 0 for a
  * norm, ld < cols, rows * ld > 2^56, a workspace too small), ZERO_EHIP. */
 

@@ -451,13 +451,15 @@ def test_no_rows(kind, accumulate):
                        torch.empty(5, 0, dtype=KINDS[kind], device="cuda"), 0.1, rng)
 
 
-@pytest.mark.parametrize("rows,cols", [(65, 1600), (3, 77), (4, 8192), (2, 20001)])
-def test_in_place(rows, cols):
+@pytest.mark.parametrize("rows,cols,kind", [(65, 1600, "bf16"), (3, 77, "bf16"), (4, 8192, "bf16"), (2, 20001, "bf16"),
+                                            (5000, 1601, "f32"), (9000, 1100, "f16"), (700, 9001, "f32"), (4001, 5, "f16"),
+                                            (20000, 333, "f32")])
+def test_in_place(rows, cols, kind):
     """Outputs on the inputs' own memory give the same bits as apart."""
-    log("in place", rows, cols)
+    log("in place", rows, cols, kind)
     g = gen("inplace", rows, cols)
-    x, res = (matrix(g, rows, cols, "bf16").contiguous() for _ in range(2))
-    dy, dres = (matrix(g, rows, cols, "bf16").contiguous() for _ in range(2))
+    x, res = (matrix(g, rows, cols, kind).contiguous() for _ in range(2))
+    dy, dres = (matrix(g, rows, cols, kind).contiguous() for _ in range(2))
     bias, w, b = (vector(g, cols, "f32", a, 0.3) for a in (0.0, 1.0, 0.0))
     rng = rng_state(SEED, 0)
     stats = lambda: [torch.empty(rows, device="cuda") for _ in range(2)]
@@ -656,6 +658,32 @@ def test_more_groups_than_32_bits_count():
     for first in (0, (1 << 30) - 50, (1 << 32) - 95):
         k = O.keep(100, 1, 0.5, SEED, 1, 3, first_row=first)
         assert np.array_equal(f64(x[first:first + 100]), k * 2.0), first
+
+
+def test_very_wide_rows():
+    """A flat tensor as one row of 2^30 columns, and sums over two rows of more
+    columns than the fold's grid covers at once."""
+    cols = 1 << 30
+    log("one row of 2^30")
+    x = torch.ones(1, cols, dtype=torch.float16, device="cuda")
+    rng = rng_state(SEED, 1)
+    Z.zero_dropout_fwd(x, x, 0.5, rng, 3)
+    assert np.array_equal(f64(x[:, :800]), O.keep(1, 800, 0.5, SEED, 1, 3) * 2.0)
+    out = O.philox4x32(((cols - 8) // 8, 0, 3, 1), (SEED & 0xFFFFFFFF, SEED >> 32))     # the last group
+    want = [((int(o) >> s) & 0xFFFF) >= 32768 for o in out for s in (0, 16)]
+    assert [bool(v) for v in x[0, -8:]] == want
+    del x
+    cols = (1 << 21) + 4099                          # past 65536 blocks of 32 columns
+    log("two rows of 2^21 + 4099")
+    dy = torch.randn(2, cols, device="cuda")
+    db = torch.empty(cols, device="cuda")
+    dx = torch.empty_like(dy)
+    Z.zero_dropout_bwd(dx, dy, 0.25, rng, 3, dbias=db)
+    assert torch.equal(db, dx[0] + dx[1])
+    w = torch.rand(cols, device="cuda") + 0.5
+    y, st = torch.empty_like(dy), [torch.empty(2, device="cuda") for _ in range(2)]
+    Z.zero_layernorm_fwd(y, *st, dy, w, None, EPS)
+    _check_fwd(dy, y, *st, w, None, "f32")
 
 
 @pytest.mark.parametrize("rows,cols", [((1 << 20) + 77, 8), (70_001, 24)])

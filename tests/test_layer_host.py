@@ -175,6 +175,7 @@ def test_norm_forward_arguments_are_checked(Z, fn):
     assert _call(Z, fn, rstd=FAKE + 1) == E.ZERO_EALIGN
     if fn == "zero_dropout_layernorm_fwd":
         assert _call(Z, fn, r=FAKE, y=FAKE) == E.ZERO_EINVAL
+    assert _call(Z, fn, mean=FAKE, rstd=FAKE) == E.ZERO_EINVAL
     assert _call(Z, fn, rows=0) == E.ZERO_OK                               # nothing to do
 
 
@@ -311,6 +312,12 @@ def test_binding_refuses_other_devices_types_and_shapes(Z, monkeypatch):
         call(bias=_Fake(1, (64,), stride=(64, 1)))
     with pytest.raises(Z.ZeroError):                                # a broadcast row: the library refuses ld < cols
         call(x=_Fake(0, (4, 64), stride=(0, 1)))
+    for site in (-1, 1 << 32):
+        with pytest.raises(ValueError, match="site"):
+            Z.zero_dropout_fwd(_Fake(0), _Fake(0), 0.0, None, site=site)
+    for seed in (-1, 1 << 64):
+        with pytest.raises(ValueError, match="seed"):
+            Z.zero_rng_init(FAKE, seed)
     with pytest.raises(TypeError, match="share one type"):
         Z.zero_layernorm_fwd(_Fake(0), None, None, _Fake(0), _Fake(0, (64,), stride=(64, 1)),
                              _Fake(0, (64,), dtype=torch.float32, stride=(64, 1)))

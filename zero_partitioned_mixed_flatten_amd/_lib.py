@@ -637,6 +637,11 @@ class _LayerCall:
             raise ValueError(f"{self.fn}: expected a contiguous generator state of {RNG_BYTES} bytes")
         return dev_rng.data_ptr()
 
+    def site(self, site: int) -> int:
+        if not 0 <= site < 1 << 32:
+            raise ValueError(f"{self.fn}: site {site} is not in [0, 2^32)")
+        return site
+
     def workspace(self, ws, stream):
         """(tensor, address, bytes).  None: taken from torch's allocator on the
         call's stream, so neither streams nor captured graphs share it."""
@@ -661,6 +666,8 @@ class _LayerCall:
 
 def zero_rng_init(dev_rng, seed: int, stream=None) -> None:
     _need("zero_rng_init", dev_rng, RNG_BYTES)
+    if not 0 <= seed < 1 << 64:
+        raise ValueError(f"zero_rng_init: seed {seed} is not in [0, 2^64)")
     _check("zero_rng_init", lib().zero_rng_init(_ptr(dev_rng), seed, _stream(stream)))
 
 
@@ -683,7 +690,7 @@ def zero_dropout_fwd(out, x, p: float, dev_rng, site: int = 0, residual=None, bi
     c = _LayerCall("zero_dropout_fwd", out, stream)
     bias_, btype = c.vecs(bias)
     c.check(lib().zero_dropout_fwd(*c.mat(out), *c.mat(x), *c.mat(residual), bias_, btype, c.rows, c.cols, c.code, p,
-                                   c.rng(dev_rng), site, c.stream))
+                                   c.rng(dev_rng), c.site(site), c.stream))
 
 
 def zero_dropout_bwd(dx, dout, p: float, dev_rng, site: int = 0, dbias=None, accumulate: bool = False, workspace=None,
@@ -693,7 +700,7 @@ def zero_dropout_bwd(dx, dout, p: float, dev_rng, site: int = 0, dbias=None, acc
     dbias_, gtype = c.vecs(dbias)
     ws, wptr, wbytes = c.workspace(workspace, stream) if dbias is not None else (None, 0, 0)
     c.check(lib().zero_dropout_bwd(*c.mat(dx), dbias_, gtype, int(bool(accumulate)), *c.mat(dout), c.rows, c.cols,
-                                   c.code, p, c.rng(dev_rng), site, wptr, wbytes, c.stream))
+                                   c.code, p, c.rng(dev_rng), c.site(site), wptr, wbytes, c.stream))
 
 
 def zero_layernorm_fwd(y, mean, rstd, x, w, b, eps: float = 1e-5, stream=None) -> None:
@@ -723,7 +730,7 @@ def zero_dropout_layernorm_fwd(r, y, mean, rstd, x, residual, bias, w, b, eps: f
     bias_, w_, b_, vtype = c.vecs(bias, w, b)
     c.check(lib().zero_dropout_layernorm_fwd(*c.mat(r), *c.mat(y), c.stat(mean), c.stat(rstd), *c.mat(x),
                                              *c.mat(residual), bias_, w_, b_, vtype, c.rows, c.cols, c.code, eps, p,
-                                             c.rng(dev_rng), site, c.stream))
+                                             c.rng(dev_rng), c.site(site), c.stream))
 
 
 def zero_dropout_layernorm_bwd(dx, dr, dw, db, dbias, dy, dres, r, mean, rstd, w, p: float, dev_rng, site: int = 0,
@@ -735,4 +742,4 @@ def zero_dropout_layernorm_bwd(dx, dr, dw, db, dbias, dy, dres, r, mean, rstd, w
     ws, wptr, wbytes = c.workspace(workspace, stream)
     c.check(lib().zero_dropout_layernorm_bwd(*c.mat(dx), *c.mat(dr), dw_, db_, dbias_, gtype, int(bool(accumulate)),
                                              *c.mat(dy), *c.mat(dres), *c.mat(r), c.stat(mean), c.stat(rstd), w_, vtype,
-                                             c.rows, c.cols, c.code, p, c.rng(dev_rng), site, wptr, wbytes, c.stream))
+                                             c.rows, c.cols, c.code, p, c.rng(dev_rng), c.site(site), wptr, wbytes, c.stream))

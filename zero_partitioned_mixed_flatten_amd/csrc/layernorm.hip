@@ -329,7 +329,7 @@ int check_fwd(const FwdCall& c, bool join)
         return rc;
     if ((c.mean && !is_aligned(c.mean, 4)) || (c.rstd && !is_aligned(c.rstd, 4)))
         return ZERO_EALIGN;
-    if (join && c.rows && c.r == c.y)
+    if (c.rows && ((join && c.r == c.y) || (c.mean && c.mean == c.rstd)))
         return ZERO_EINVAL;
     return ZERO_OK;
 }

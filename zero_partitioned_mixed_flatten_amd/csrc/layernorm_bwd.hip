@@ -330,33 +330,36 @@ __global__ __launch_bounds__(kFoldBlock) void fold_kernel(SumOut out, const floa
     if (!out.dst[i])
         return;
     const uint32_t lane = threadIdx.x % kFoldCols, first = threadIdx.x / kFoldCols;
-    const uint32_t col = blockIdx.x * kFoldCols + lane;
-    float s = 0.0f;
-    if (col < cols) {
-        const float* p = partials + uint64_t(i) * cols + col;
-        const uint64_t step = uint64_t(3) * cols;
-        for (uint32_t c = first; c < chunks; c += 8 * kParts) {
-            float v[8];
+    for (uint32_t block = blockIdx.x; block * kFoldCols < cols; block += gridDim.x) {
+        const uint32_t col = block * kFoldCols + lane;
+        float s = 0.0f;
+        if (col < cols) {
+            const float* p = partials + uint64_t(i) * cols + col;
+            const uint64_t step = uint64_t(3) * cols;
+            for (uint32_t c = first; c < chunks; c += 8 * kParts) {
+                float v[8];
 #pragma unroll
-            for (uint32_t u = 0; u < 8; ++u)
-                v[u] = c + kParts * u < chunks ? p[(c + kParts * u) * step] : 0.0f;
-            s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+                for (uint32_t u = 0; u < 8; ++u)
+                    v[u] = c + kParts * u < chunks ? p[(c + kParts * u) * step] : 0.0f;
+                s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+            }
         }
-    }
-    part[first][lane] = s;
-    __syncthreads();
-    if (first || col >= cols)
-        return;
-    s = 0.0f;
+        part[first][lane] = s;
+        __syncthreads();
+        if (first == 0 && col < cols) {
+            s = 0.0f;
 #pragma unroll
-    for (uint32_t k = 0; k < kParts; ++k)
-        s += part[k][lane];
-    if (out.f32) {
-        float* d = static_cast<float*>(out.dst[i]) + col;
-        *d = out.accumulate ? *d + s : s;
-    } else {
-        T* d = static_cast<T*>(out.dst[i]) + col;
-        *d = T(out.accumulate ? float(*d) + s : s);
+            for (uint32_t k = 0; k < kParts; ++k)
+                s += part[k][lane];
+            if (out.f32) {
+                float* d = static_cast<float*>(out.dst[i]) + col;
+                *d = out.accumulate ? *d + s : s;
+            } else {
+                T* d = static_cast<T*>(out.dst[i]) + col;
+                *d = T(out.accumulate ? float(*d) + s : s);
+            }
+        }
+        __syncthreads();                           // part is free for the next columns
     }
 }
 
@@ -493,8 +496,9 @@ int run_bwd(const BwdCall& c, hipStream_t s)
     if (!c.dw && !c.db && !c.dbias)
         return ZERO_OK;
     const SumOut out{{c.dw, c.db, c.dbias}, c.grad_dtype == ZERO_F32, c.accumulate};
-    hipLaunchKernelGGL(fold_kernel<T>, dim3(uint32_t((c.cols + kFoldCols - 1) / kFoldCols), 3), dim3(kFoldBlock), 0, s,
-                       out, a.partials, uint32_t(chunks), uint32_t(c.cols));
+    const uint64_t blocks = (c.cols + kFoldCols - 1) / kFoldCols;
+    hipLaunchKernelGGL(fold_kernel<T>, dim3(uint32_t(blocks < 65536 ? blocks : 65536), 3), dim3(kFoldBlock), 0, s, out,
+                       a.partials, uint32_t(chunks), uint32_t(c.cols));
     return launch_status();
 }
 

@@ -38,7 +38,8 @@ struct FwdArgs {
 // Rows that fit the registers of TPR threads, VPT groups of 8 columns each:
 // one pass over memory, the row kept as it was loaded.  A persistent workgroup
 // takes every gridDim.x-th block of BLOCK / TPR rows, the next rows' loads in
-// flight while it works on the present ones, w, b and bias in registers.
+// flight while it works on the present ones, w, b and bias in registers (but
+// see kLate).
 template <typename T, bool JOIN, int BLOCK, int TPR, int VPT, int HINT>
 __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
 {
@@ -48,6 +49,13 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
     // r of a joined 16-bit row is made 0 past the row's end once, when it is
     // rounded, instead of x and residual
     constexpr bool kZero = !JOIN || sizeof(T) == 4;
+    // 1024 threads have 128 registers each, too few for two joined binary32
+    // groups with the next row's and the vectors: the next row is fetched when
+    // this one is summed up, into the same registers, and the vectors are read
+    // again from the caches (1000 x 16384 49 us, 300 x 16384 20; with the rest's
+    // way and 38 registers spilt 76 and 34, and three passes 70 and 28; 3000 x
+    // 10240, 640 threads, 99 so and 91 the rest's way)
+    constexpr bool kLate = JOIN && sizeof(T) == 4 && BLOCK == 1024;
     __shared__ alignas(16) float scratch[2 * BLOCK / 64];
     uint32_t parity = 0;
     const RngKey key = rng_key(a.drop);
@@ -77,17 +85,22 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
     Row cur, next;
     fetch(first + slot, cur);
     f32x8 w[VPT], b[VPT], bias[VPT];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
+    auto load_w = [&](int i) {
         const P at = part(i);
         w[i] = load8_vector<T>(a.w, a.vec_f32, at.group * 8, at.k, 1.0f);
         b[i] = load8_vector<T>(a.b, a.vec_f32, at.group * 8, at.k, 0.0f);
-        if (JOIN)
+    };
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const P at = part(i);
+        if (!kLate)
+            load_w(i);
+        if (JOIN && !kLate)
             bias[i] = load8_vector<T>(a.bias, a.vec_f32, at.group * 8, at.k, -0.0f);   // x + -0 is x, -0 too
     }
     for (; first < a.rows; first += stride) {
         const uint64_t row = first + slot;
-        if (first + stride < a.rows)
+        if (!kLate && first + stride < a.rows)
             fetch(row + stride, next);
         const bool live = row < a.rows;
         u32x4 bits[VPT];
@@ -103,6 +116,8 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
             const P at = part(i);
             raw[i] = at.template settle<kZero>(cur.x[i], ragged);
             if (JOIN) {
+                if (kLate)
+                    bias[i] = load8_vector<T>(a.bias, a.vec_f32, at.group * 8, at.k, -0.0f);
                 f32x8 v = raw_plus<T>(raw[i], bias[i], one);
                 v = dropped(v, a.drop, bits[i]);
                 if (a.residual)
@@ -116,6 +131,8 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
             }
             s8 = i ? raw_plus<T>(raw[i], s8, one) : widen<T>(raw[i]);
         }
+        if (kLate && first + stride < a.rows)
+            fetch(row + stride, cur);
         s[0] = ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
         row_sum<BLOCK, TPR>(s, scratch, parity);
         const float mean = over(s[0], n, inv);
@@ -140,6 +157,8 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             f32x8 v;
+            if (kLate)
+                load_w(i);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[j] = __builtin_fmaf(x[i][j] * rstd, w[i][j], b[i][j]);
@@ -149,7 +168,8 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
-        cur = next;
+        if (!kLate)
+            cur = next;
     }
 }
 

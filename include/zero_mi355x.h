@@ -582,9 +582,10 @@ int zero_host_stream_copy(zero_host_ctx_t* ctx, void* dst, const void* src, uint
  *     with accumulate left as they are);
  *   - results do not depend on timing: equal calls give equal bits.
  * Errors of all of them: ZERO_EINVAL (a required pointer NULL with rows > 0,
- * a bad type, two equal outputs (mean and rstd among them), eps not finite and > 0 in binary32, p not in
- * [0, 1]), ZERO_EALIGN, ZERO_ERANGE (rows > 2^40, cols > 2^30, cols = 0 for a
- * norm, ld < cols, rows * ld > 2^56, a workspace too small), ZERO_EHIP. */
+ * a bad type, two equal outputs (mean and rstd among them), eps not finite and
+ * > 0 in binary32, p not in [0, 1]), ZERO_EALIGN, ZERO_ERANGE (rows > 2^40,
+ * cols > 2^30, cols = 0 for a norm, ld < cols, rows * ld > 2^56, a workspace
+ * too small), ZERO_EHIP. */
 
 /* The state of the dropout generator in DEVICE memory (16 bytes, 8-byte
  * aligned).  The mask of a call is a function of (seed, step, site, rows'

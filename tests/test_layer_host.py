@@ -323,3 +323,9 @@ def test_binding_refuses_other_devices_types_and_shapes(Z, monkeypatch):
                              _Fake(0, (64,), dtype=torch.float32, stride=(64, 1)))
     with pytest.raises(ValueError, match="one per row"):
         Z.zero_layernorm_fwd(_Fake(0), _Fake(0, (3,), dtype=torch.float32, stride=(3, 1)), None, _Fake(0), None, None)
+
+
+@pytest.mark.parametrize("max_rows,cols", [(-1, 8), (4, 0), (4, -8)])
+def test_residual_norm_refuses_shapes_without_columns(Z, max_rows, cols):
+    with pytest.raises(ValueError, match="ResidualNorm"):
+        Z.ResidualNorm(max_rows, cols, None)

@@ -551,8 +551,8 @@ _torch = None
 def _layer_setup():
     global _dtype_codes, _torch
     import torch
-    _torch = torch
     _dtype_codes = {torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32}
+    _torch = torch                                 # last: another thread's call takes it as the sign
 
 
 class _LayerCall:

@@ -47,6 +47,8 @@ class ResidualNorm:
     def __init__(self, max_rows: int, cols: int, w, b=None, bias=None, p: float = 0.0, rng: Optional[LayerRng] = None,
                  site: int = 0, eps: float = 1e-5, dtype=None, device="cuda"):
         import torch
+        if max_rows < 0 or cols < 1:
+            raise ValueError(f"ResidualNorm: {max_rows} rows of {cols} columns")
         self.cols, self.w, self.b, self.bias = int(cols), w, b, bias
         self.p, self.rng, self.site, self.eps = float(p), rng, int(site), float(eps)
         self.dtype = torch.float16 if dtype is None else dtype

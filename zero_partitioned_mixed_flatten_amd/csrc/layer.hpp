@@ -290,9 +290,9 @@ __device__ __forceinline__ f32x8 widen(typename Raw<T>::type v)
     return __builtin_convertvector(v, f32x8);
 }
 
-// raw * a + b and raw + b, elementwise, rounded once.  binary16 elements are
-// widened inside the instruction (v_fma_mix_f32), which the compiler forms
-// only for a product: `one` is a 1 that it cannot see.
+// raw + b, raw * a, raw * a + b and v * a + raw, elementwise, rounded once.
+// binary16 elements are widened inside the instruction (v_fma_mix_f32), which
+// the compiler forms only for a product: `one` is a 1 that it cannot see.
 __device__ __forceinline__ float opaque_one()
 {
     float one = 1.0f;
@@ -311,12 +311,31 @@ __device__ __forceinline__ f32x8 raw_plus(typename Raw<T>::type raw, f32x8 b, fl
 }
 
 template <typename T>
-__device__ __forceinline__ f32x8 raw_times(typename Raw<T>::type raw, float a)
+__device__ __forceinline__ f32x8 raw_times(typename Raw<T>::type raw, f32x8 a)
 {
     f32x8 v;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        v[j] = __is_same(T, _Float16) ? __builtin_fmaf(float(raw[j]), a, -0.0f) : float(raw[j]) * a;
+        v[j] = __is_same(T, _Float16) ? __builtin_fmaf(float(raw[j]), a[j], -0.0f) : float(raw[j]) * a[j];
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ f32x8 raw_fma(typename Raw<T>::type raw, f32x8 a, f32x8 b)
+{
+    f32x8 v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = __builtin_fmaf(float(raw[j]), a[j], b[j]);
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ f32x8 fma_raw(f32x8 v, float a, typename Raw<T>::type raw)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = __builtin_fmaf(v[j], a, float(raw[j]));
     return v;
 }
 

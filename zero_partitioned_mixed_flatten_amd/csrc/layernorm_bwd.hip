@@ -7,8 +7,10 @@
 //   dr = e, dx = D(e)                         (layer norm alone: dx = e)
 //   dw = sum_rows dy * h, db = sum_rows dy, dbias = sum_rows D(e)
 //
-// h is recomputed from the saved mean and rstd.  The masks of D come from the
-// generator's counters again.  Sums are binary32.
+// h is recomputed from the saved mean and rstd, and only it, dy and w enter the
+// sums: rstd alone, squared or times dy, may leave binary32's range where the
+// gradients do not.  The masks of D come from the generator's counters again.
+// Sums are binary32.
 #include "layer.hpp"
 
 namespace zero {
@@ -30,10 +32,17 @@ struct BwdArgs {
     uint32_t cols, chunks;
     bool vec_f32;
     Drop drop;
-    float* row_sums;                               // c1, c2 of each row
+    float* row_sums;                               // -c1, -c2 of each row
     float* partials;                               // [chunk][3][cols]
     bool want[3];                                  // dw, db, dbias
 };
+
+// h = (r - mean) * rstd of a group.
+template <typename T>
+__device__ __forceinline__ f32x8 normalised(typename Raw<T>::type r, float mean, float rstd, float one)
+{
+    return raw_plus<T>(r, splat(-mean), one) * rstd;
+}
 
 // Rows that fit the registers of TPR threads, a group of 8 columns each, in
 // one pass: a persistent workgroup takes every gridDim.x-th block of
@@ -95,13 +104,10 @@ __global__ __launch_bounds__(BLOCK) void rows_bwd_kernel(BwdArgs<T> a)
         const V dy = at.settle(cur.dy, ragged);    // 0 past the row's end
         f32x8 e;
         if (NORM) {
-            // with d = dy * rstd and x = r - mean: g rstd = d w, h rstd = x rstd^2
-            const f32x8 d = raw_times<T>(dy, cur.rstd);
-            const f32x8 x = raw_plus<T>(at.template settle<false>(cur.r, ragged), splat(-cur.mean), one), g = d * w;
+            const f32x8 h = normalised<T>(at.template settle<false>(cur.r, ragged), cur.mean, cur.rstd, one);
+            const f32x8 g = raw_times<T>(dy, w);
             if (live) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    sum[0][j] = __builtin_fmaf(d[j], x[j], sum[0][j]);
+                sum[0] = raw_fma<T>(dy, h, sum[0]);
                 sum[1] = raw_plus<T>(dy, sum[1], one);
             }
             float c[2] = {0.0f, 0.0f}, c0b = 0.0f, c1b = 0.0f;
@@ -109,19 +115,21 @@ __global__ __launch_bounds__(BLOCK) void rows_bwd_kernel(BwdArgs<T> a)
             for (int j = 0; j < 8; j += 2) {
                 c[0] += g[j];
                 c0b += g[j + 1];
-                c[1] = __builtin_fmaf(g[j], x[j], c[1]);
-                c1b = __builtin_fmaf(g[j + 1], x[j + 1], c1b);
+                c[1] = __builtin_fmaf(g[j], h[j], c[1]);
+                c1b = __builtin_fmaf(g[j + 1], h[j + 1], c1b);
             }
             c[0] += c0b;
             c[1] += c1b;
             row_sum<BLOCK, TPR>(c, scratch, parity);
             c[0] = -over(c[0], n, inv);
-            c[1] = -(over(c[1], n, inv) * cur.rstd * cur.rstd);
+            c[1] = -over(c[1], n, inv);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                e[j] = __builtin_fmaf(x[j], c[1], g[j] + c[0]);
+                e[j] = __builtin_fmaf(h[j], c[1], g[j] + c[0]);
             if (a.dres)
-                e = raw_plus<T>(at.template settle<false>(cur.dres, ragged), e, one);
+                e = fma_raw<T>(e, cur.rstd, at.template settle<false>(cur.dres, ragged));
+            else
+                e = e * cur.rstd;
         } else {
             e = widen<T>(dy);
         }
@@ -217,18 +225,18 @@ __global__ __launch_bounds__(kWideBlock) void row_sums_kernel(BwdArgs<T> a)
             const typename Raw<T>::type dy = at.template load<kCached>(a.dy + row * a.ld_dy);
             const typename Raw<T>::type r = at.template load<kCached>(a.r + row * a.ld_r);
             const f32x8 w = load8_vector_at<T>(a.w, a.vec_f32, group_at(at.group * 8, a.cols), ragged, 1.0f);
-            const f32x8 g = raw_times<T>(at.settle(dy, ragged), rstd) * w;       // 0 past the row's end
-            const f32x8 x = raw_plus<T>(at.settle(r, ragged), splat(-mean), one);
+            const f32x8 g = raw_times<T>(at.settle(dy, ragged), w);              // 0 past the row's end
+            const f32x8 h = normalised<T>(at.settle(r, ragged), mean, rstd, one);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 c[0] += g[j];
-                c[1] = __builtin_fmaf(g[j], x[j], c[1]);
+                c[1] = __builtin_fmaf(g[j], h[j], c[1]);
             }
         }
         row_sum<kWideBlock, kWideBlock>(c, scratch, parity);
         if (threadIdx.x == 0) {
             a.row_sums[2 * row] = -over(c[0], n, inv);
-            a.row_sums[2 * row + 1] = -(over(c[1], n, inv) * rstd * rstd);
+            a.row_sums[2 * row + 1] = -over(c[1], n, inv);
         }
     }
 }
@@ -274,16 +282,17 @@ __global__ __launch_bounds__(kWideBlock) void strips_kernel(BwdArgs<T> a)
         if (NORM) {
             const float mean = a.mean[row], rstd = a.rstd[row];
             const float c0 = a.row_sums[2 * row], c1 = a.row_sums[2 * row + 1];
-            const f32x8 d = raw_times<T>(dy, rstd);
-            const f32x8 x = raw_plus<T>(at.template settle<false>(cur.r, ragged), splat(-mean), one), g = d * w;
+            const f32x8 h = normalised<T>(at.template settle<false>(cur.r, ragged), mean, rstd, one);
+            const f32x8 g = raw_times<T>(dy, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                sum[0][j] = __builtin_fmaf(d[j], x[j], sum[0][j]);
-                e[j] = __builtin_fmaf(x[j], c1, g[j] + c0);
-            }
+            for (int j = 0; j < 8; ++j)
+                e[j] = __builtin_fmaf(h[j], c1, g[j] + c0);
+            sum[0] = raw_fma<T>(dy, h, sum[0]);
             sum[1] = raw_plus<T>(dy, sum[1], one);
             if (a.dres)
-                e = raw_plus<T>(at.template settle<false>(cur.dres, ragged), e, one);
+                e = fma_raw<T>(e, rstd, at.template settle<false>(cur.dres, ragged));
+            else
+                e = e * rstd;
         } else {
             e = widen<T>(dy);
         }

@@ -1,0 +1,40 @@
+"""CPU checks of what the layer operators and ResidualNorm refuse, and of what
+a refused call leaves behind."""
+import pytest
+
+FAKE = 1 << 20          # an aligned address that is never dereferenced
+
+
+@pytest.fixture(scope="module")
+def Z():
+    import os
+
+    from zero_partitioned_mixed_flatten_amd import build
+    if not os.path.exists(build.LIB):
+        build.build()
+    import zero_partitioned_mixed_flatten_amd as Z
+    return Z
+
+
+# ---- eps -------------------------------------------------------------------------------
+
+def _norm_fwd(Z, eps):
+    """A layer norm of no rows: the arguments are checked, nothing is enqueued."""
+    return Z.lib().zero_layernorm_fwd(None, 0, None, None, None, 0, None, None, Z.ZERO_F32, 0, 64, Z.ZERO_F16, eps, None)
+
+
+def _joined_fwd(Z, eps):
+    return Z.lib().zero_dropout_layernorm_fwd(None, 0, None, 0, None, None, None, 0, None, 0, None, None, None, Z.ZERO_F32,
+                                              0, 64, Z.ZERO_F16, eps, 0.0, None, 0, None)
+
+
+FLT_MAX = float.fromhex("0x1.fffffep127")
+
+
+@pytest.mark.parametrize("call", [_norm_fwd, _joined_fwd])
+def test_eps_is_finite_and_positive_in_binary32(Z, call):
+    # above FLT_MAX a binary64 value rounds to inf, from half a step on; below half of the smallest subnormal, to 0
+    for eps in (1e39, 1e300, float.fromhex("0x1.ffffffp127"), 2.0 ** 128, 2.0 ** -150, 5e-324):
+        assert call(Z, eps) == Z._lib.ZERO_EINVAL, eps
+    for eps in (FLT_MAX, float.fromhex("0x1.fffffefffffffp127"), 1e38, 2.0 ** -149, 1e-5):
+        assert call(Z, eps) == Z._lib.ZERO_OK, eps

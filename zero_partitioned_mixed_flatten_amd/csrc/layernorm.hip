@@ -334,7 +334,8 @@ int check_fwd(const FwdCall& c, bool join)
     int rc = check_shape(c.rows, c.cols, c.dtype);
     if (rc)
         return rc;
-    if (!(c.eps > 0.0) || !isfinite(c.eps) || !(float(c.eps) > 0.0f))
+    const float eps = float(c.eps);                // what the kernels add: a binary64 value may round to 0 or inf
+    if (!(eps > 0.0f) || !isfinite(eps))
         return ZERO_EINVAL;
     if (!c.cols)
         return ZERO_ERANGE;

@@ -38,3 +38,21 @@ def test_eps_is_finite_and_positive_in_binary32(Z, call):
         assert call(Z, eps) == Z._lib.ZERO_EINVAL, eps
     for eps in (FLT_MAX, float.fromhex("0x1.fffffefffffffp127"), 1e38, 2.0 ** -149, 1e-5):
         assert call(Z, eps) == Z._lib.ZERO_OK, eps
+
+
+# ---- ResidualNorm -------------------------------------------------------------------------
+
+def _place(Z, max_rows=16, cols=64):
+    """A place with its buffers on the host: every call's checks run, none gets
+    past the binding's check of the device."""
+    import torch
+    return Z.ResidualNorm(max_rows, cols, torch.ones(cols), dtype=torch.float32, device="cpu")
+
+
+def test_a_refused_forward_leaves_the_last_one(Z):
+    import torch
+    place = _place(Z)
+    place.rows = 3                                  # as a forward pass of 3 rows leaves it
+    with pytest.raises(ValueError, match="device tensor"):
+        place.forward(torch.zeros(5, 64))
+    assert place.rows == 3 and place.r.shape == (3, 64)

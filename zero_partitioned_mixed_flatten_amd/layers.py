@@ -83,11 +83,11 @@ class ResidualNorm:
         x = x.view(rows, self.cols) if x.dim() != 2 else x
         if residual is not None and residual.dim() != 2:
             residual = residual.view(rows, self.cols)
-        self.rows = rows
         if y is None:
             y = torch.empty(rows, self.cols, dtype=self.dtype, device=self.device)
-        Z.zero_dropout_layernorm_fwd(self.r, y, self._mean[:rows], self._rstd[:rows], x, residual, self.bias, self.w,
-                                     self.b, self.eps, self.p, self.rng.state if self.rng else None, self.site)
+        Z.zero_dropout_layernorm_fwd(self._r[:rows], y, self._mean[:rows], self._rstd[:rows], x, residual, self.bias,
+                                     self.w, self.b, self.eps, self.p, self.rng.state if self.rng else None, self.site)
+        self.rows = rows                            # a refused call leaves the last one's
         return y
 
     def backward(self, dy, dres=None, dx=None, dr=None, grads=None, accumulate: bool = False):

@@ -56,3 +56,26 @@ def test_a_refused_forward_leaves_the_last_one(Z):
     with pytest.raises(ValueError, match="device tensor"):
         place.forward(torch.zeros(5, 64))
     assert place.rows == 3 and place.r.shape == (3, 64)
+
+
+@pytest.mark.parametrize("shape", [(2, 3, 32), (2, 1, 128), (64,) * 2 + (1,), (128,), ()])
+def test_other_widths_are_not_taken_for_rows(Z, shape):
+    """A batch whose last dimension is not the place's width is refused, also
+    where its elements would fill whole rows."""
+    import torch
+    place = _place(Z, max_rows=4096)
+    with pytest.raises(ValueError, match="64 columns"):
+        place.forward(torch.zeros(shape))
+    with pytest.raises(ValueError, match="64 columns"):
+        place.forward(torch.zeros(6, 64), torch.zeros(shape))
+
+
+def test_batches_of_other_lengths_are_not_taken_for_rows(Z):
+    import torch
+    place = _place(Z)
+    for residual in (torch.zeros(2, 2, 64), torch.zeros(1, 7, 64)):
+        with pytest.raises(ValueError):
+            place.forward(torch.zeros(6, 64), residual)
+    padded = torch.zeros(2, 3, 80)[:, :, :64]       # a batch of sequences inside wider rows: one matrix
+    with pytest.raises(ValueError, match="device tensor"):
+        place.forward(padded, padded)

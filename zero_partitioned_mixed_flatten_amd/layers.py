@@ -74,15 +74,21 @@ class ResidualNorm:
         """The gradient tensors of (w, b, bias), in that order, without the absent ones."""
         return tuple(g for g in (self.dw, self.db, self.dbias) if g is not None)
 
+    def _matrix(self, t, rows):
+        """A batch of any number of dimensions, the last of them the columns, as a matrix."""
+        if t.dim() < 1 or t.shape[-1] != self.cols or t.numel() != rows * self.cols:
+            raise ValueError(f"ResidualNorm.forward: expected {rows} rows of {self.cols} columns, got {tuple(t.shape)}")
+        return t if t.dim() == 2 else t.view(rows, self.cols)
+
     def forward(self, x, residual=None, y=None):
-        """y of the rows of x; r stays in self.r."""
+        """y of the rows of x (any shape whose last dimension is the columns); r
+        stays in self.r."""
         import torch
         rows = x.numel() // self.cols
         if rows > self.max_rows:
             raise ValueError(f"ResidualNorm.forward: {rows} rows, made for {self.max_rows}")
-        x = x.view(rows, self.cols) if x.dim() != 2 else x
-        if residual is not None and residual.dim() != 2:
-            residual = residual.view(rows, self.cols)
+        x = self._matrix(x, rows)
+        residual = None if residual is None else self._matrix(residual, rows)
         if y is None:
             y = torch.empty(rows, self.cols, dtype=self.dtype, device=self.device)
         Z.zero_dropout_layernorm_fwd(self._r[:rows], y, self._mean[:rows], self._rstd[:rows], x, residual, self.bias,

@@ -79,3 +79,66 @@ def test_batches_of_other_lengths_are_not_taken_for_rows(Z):
     padded = torch.zeros(2, 3, 80)[:, :, :64]       # a batch of sequences inside wider rows: one matrix
     with pytest.raises(ValueError, match="device tensor"):
         place.forward(padded, padded)
+
+
+# ---- the generator's state -------------------------------------------------------------------
+
+class _State:
+    """A generator state's face, on a device that need not be there."""
+    is_cuda = True
+
+    def __init__(self, device, nbytes=16):
+        self._d, self._n, self.device = device, nbytes, f"cuda:{device}"
+
+    def get_device(self):
+        return self._d
+
+    def numel(self):
+        return self._n
+
+    def element_size(self):
+        return 1
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return FAKE
+
+
+class _Stream:
+    cuda_stream = 0
+
+    def __init__(self, device):
+        self.device_index = device
+
+
+@pytest.mark.parametrize("name", ["init", "advance"])
+def test_generator_calls_refuse_other_devices(Z, monkeypatch, name):
+    """The kernel would be enqueued on the current device's stream and write
+    another device's memory."""
+    import torch
+    calls = []
+
+    class Lib:
+        def zero_rng_init(self, *a):
+            calls.append(a)
+            return 0
+
+        def zero_rng_advance(self, *a):
+            calls.append(a)
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(Z._lib, "lib", lambda: Lib())
+    monkeypatch.setattr(Z._lib, "_stream", lambda s: 0)
+    call = (lambda t, s=None: Z.zero_rng_init(t, 1, stream=s)) if name == "init" else \
+        (lambda t, s=None: Z.zero_rng_advance(t, stream=s))
+    for bad in (lambda: call(_State(1)), lambda: call(_State(0), _Stream(1)), lambda: call(_State(0, 8)),
+                lambda: call(torch.zeros(16, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            bad()
+    assert not calls
+    call(_State(0))
+    call(_State(0), _Stream(0))
+    assert len(calls) == 2

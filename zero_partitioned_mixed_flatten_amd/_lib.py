@@ -664,16 +664,32 @@ class _LayerCall:
             _check(self.fn, rc)
 
 
+def _rng_address(fn: str, dev_rng, stream) -> int:
+    """The address of a generator's state, which lies on the current device as
+    the stream does: the kernel writes it from there."""
+    _need(fn, dev_rng, RNG_BYTES)
+    addr = _ptr(dev_rng)
+    if dev_rng is not None and not isinstance(dev_rng, int):
+        import torch
+        device = dev_rng.get_device()
+        if device != torch.cuda.current_device():
+            raise ValueError(f"{fn}: the state is on device {device}, the current device is "
+                             f"{torch.cuda.current_device()}")
+        if stream is not None and stream.device_index != device:
+            raise ValueError(f"{fn}: the stream belongs to device {stream.device_index}, the state is on {device}")
+    return addr
+
+
 def zero_rng_init(dev_rng, seed: int, stream=None) -> None:
-    _need("zero_rng_init", dev_rng, RNG_BYTES)
     if not 0 <= seed < 1 << 64:
         raise ValueError(f"zero_rng_init: seed {seed} is not in [0, 2^64)")
-    _check("zero_rng_init", lib().zero_rng_init(_ptr(dev_rng), seed, _stream(stream)))
+    addr = _rng_address("zero_rng_init", dev_rng, stream)
+    _check("zero_rng_init", lib().zero_rng_init(addr, seed, _stream(stream)))
 
 
 def zero_rng_advance(dev_rng, stream=None) -> None:
-    _need("zero_rng_advance", dev_rng, RNG_BYTES)
-    _check("zero_rng_advance", lib().zero_rng_advance(_ptr(dev_rng), _stream(stream)))
+    addr = _rng_address("zero_rng_advance", dev_rng, stream)
+    _check("zero_rng_advance", lib().zero_rng_advance(addr, _stream(stream)))
 
 
 def read_rng(dev_rng) -> RngState:

@@ -590,12 +590,14 @@ int zero_host_stream_copy(zero_host_ctx_t* ctx, void* dst, const void* src, uint
 /* The state of the dropout generator in DEVICE memory (16 bytes, 8-byte
  * aligned).  The mask of a call is a function of (seed, step, site, rows'
  * index, column, cols): keep it unchanged between a forward pass and its
- * backward (or recomputed forward) pass, and advance it once per training
- * step.  Being in device memory, it lets a captured graph draw new masks at
- * every replay. */
+ * backward (or recomputed forward) pass, and advance it after each backward
+ * pass, so once per micro-batch where a training step accumulates over
+ * several: two that share a step share their masks too.  For the same reason
+ * ranks that train on different data need different seeds.  Being in device
+ * memory, it lets a captured graph draw new masks at every replay. */
 typedef struct {
     uint64_t seed;
-    uint32_t step;
+    uint32_t step;              /* forward/backward passes so far */
     uint32_t reserved;          /* 0 */
 } zero_rng_t;
 
@@ -618,7 +620,7 @@ int zero_rng_advance(zero_rng_t* dev_rng, void* stream);
  * so the drop probability is p to the nearest 2^-16 and the expectation is
  * kept exactly for it; t = 0 draws nothing (dev_rng may then be NULL), t =
  * 65536 drops everything.  A dropped element is 0 whatever it held, inf and
- * NaN too.  site tells apart the dropouts of one step (layer and place).
+ * NaN too.  site tells apart the dropouts of one pass (layer and place).
  * dev_rng: device, 8-byte aligned, read when the kernel runs. */
 int zero_dropout_fwd(void* out, uint64_t ld_out, const void* x, uint64_t ld_x, const void* residual,
                      uint64_t ld_residual, const void* bias, int bias_dtype, uint64_t rows, uint64_t cols, int dtype,

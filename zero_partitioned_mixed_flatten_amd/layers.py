@@ -16,10 +16,14 @@ from . import _lib as Z
 
 
 class LayerRng:
-    """A dropout generator: 16 bytes of device memory holding the seed and the
-    training step.  One generator serves every ResidualNorm of a model (each
-    has its own site); advance() once per training step, after the backward
-    pass, inside the captured graph where there is one."""
+    """A dropout generator: 16 bytes of device memory holding the seed and a
+    count of passes.  One generator serves every ResidualNorm of a model (each
+    has its own site); advance() after each backward pass, inside the captured
+    graph where there is one.  A training step of several micro-batches
+    (AccumStep) advances after each of them: masks are a function of the seed,
+    the count, the site and the element, so micro-batches under one count would
+    all drop the same elements.  Ranks that train on different data take
+    different seeds for the same reason."""
 
     def __init__(self, seed: int, device="cuda"):
         import torch

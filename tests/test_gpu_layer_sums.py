@@ -137,3 +137,31 @@ def test_a_missing_block_would_show():
     for bad in (torch.zeros_like(good), good - dy[:4].double().sum(0), good - dy[-3:].double().sum(0)):
         with pytest.raises(AssertionError):
             check("db", bad, dy)
+
+
+# ---- no rows -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("cols", [3, 40, 9001])
+def test_sums_of_no_rows(kind, accumulate, cols):
+    """An empty batch: each call stores 0 to (or, accumulating, leaves) the
+    gradients it has, and touches no other."""
+    log("no rows", kind, accumulate, cols)
+    x, s = torch.empty(0, cols, dtype=KINDS[kind], device="cuda"), torch.empty(0, device="cuda")
+    rng = torch.zeros(Z.RNG_BYTES, dtype=torch.uint8, device="cuda")
+    Z.zero_rng_init(rng, SEED)
+    calls = {
+        (2,): lambda t: Z.zero_dropout_bwd(x, x, 0.1, rng, dbias=t[2], accumulate=accumulate),
+        (0, 1): lambda t: Z.zero_layernorm_bwd(x, t[0], t[1], x, x, s, s, None, accumulate=accumulate),
+        (0,): lambda t: Z.zero_layernorm_bwd(x, t[0], None, x, x, s, s, None, accumulate=accumulate),
+        (0, 1, 2): lambda t: Z.zero_dropout_layernorm_bwd(x, torch.empty_like(x), *t, x, x, x, s, s, None, 0.1, rng,
+                                                          accumulate=accumulate),
+        (1, 2): lambda t: Z.zero_dropout_layernorm_bwd(x, torch.empty_like(x), None, t[1], t[2], x, x, x, s, s, None, 0.1,
+                                                       rng, accumulate=accumulate)}
+    for own, call in calls.items():
+        t = [torch.full((cols,), 5.0, device="cuda") for _ in range(3)]
+        call(t)
+        for i in range(3):
+            want = 5.0 if accumulate or i not in own else 0.0
+            assert bool((t[i] == want).all()), (own, i)

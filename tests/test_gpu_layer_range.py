@@ -1,7 +1,8 @@
 """The norms' backward passes over the range of binary32 and bfloat16: rows of
 a spread whose reciprocal squared, or whose reciprocal times the gradient, is
 below or above what binary32 holds, where the gradients themselves are well
-inside it.  Against the 64-bit forms, within their bounds."""
+inside it, against the 64-bit forms, within their bounds.  And dropout over
+more groups than one launch has threads."""
 import zlib
 
 import numpy as np
@@ -72,3 +73,29 @@ def test_backward_over_the_range(kind, cols, spread, scale):
     close(db, want[2], O.stored(bound[2], want[2], "f32"), "joined db")
     total, e_t = O.column_sum(d, e_d)
     close(dbias, total, O.stored(e_t, total, "f32"), "dbias")
+
+
+@pytest.mark.parametrize("rows,cols,kind", [((1 << 29) + 41, 9, "f16"), ((1 << 29) + 41, 9, "f32"),
+                                            ((1 << 22) + 3, 2050, "bf16"), ((1 << 22) + 3, 2050, "f32")])
+def test_dropout_past_one_launch(rows, cols, kind):
+    """More groups of 8 columns than the threads of a launch: the grid goes
+    around.  In place, with a residual and a bias, rows of few groups and of
+    more than a workgroup's threads, an odd width and an even one; p = 1/2 and
+    whole numbers, so every value is exact."""
+    groups = -(-cols // 8)
+    assert rows * groups > 1 << 30
+    print("[range] past one launch", rows, cols, kind, flush=True)
+    x = torch.ones(rows, cols, dtype={"f16": torch.float16, **KINDS}[kind], device="cuda")
+    bias = (torch.arange(cols) % 5).float().cuda()
+    rng = torch.zeros(Z.RNG_BYTES, dtype=torch.uint8, device="cuda")
+    Z.zero_rng_init(rng, SEED)
+    Z.zero_dropout_fwd(x, x, 0.5, rng, 8, residual=x, bias=bias)
+    most = 3.0 + 2.0 * bias                                       # 1 + 2 (1 + bias) where kept, else 1
+    around = (1 << 30) // groups                                  # where the second round begins
+    for first in (0, 1234567, around - 50, around, rows - 100):
+        kept = torch.from_numpy(O.keep(100 if first + 100 <= rows else rows - first, cols, 0.5, SEED, 0, 8, first_row=first))
+        want = torch.where(kept, most.cpu(), 1.0)
+        assert torch.equal(x[first:first + kept.shape[0]].float().cpu(), want), first
+    for part in x.split(1 << 26 if cols < 100 else 1 << 18):      # every element was written, once
+        v = part.float()
+        assert bool(((v == 1.0) | (v == most)).all())

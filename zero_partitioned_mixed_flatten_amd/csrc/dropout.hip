@@ -82,10 +82,11 @@ __device__ __forceinline__ typename Raw<T>::type settle16(typename Raw<T>::type 
 // of a division and before the generator's state is waited for (16384 x 8192
 // fp16, no residual: 84.5 us = 6.35 TB/s; with a 64-bit division and the state
 // first 97.0 us; a copy 81.2 us).  NARROW: rows of fewer than 8 columns, loaded
-// by elements.  FAR: 2^32 groups or more, or more workgroups than a launch
-// takes (the grid then goes around).  Binary32 goes by the traded pieces of
-// layer.hpp, over the 64 consecutive groups of a wave whatever rows they are
-// in.
+// by elements.  FAR: more than 2^22 workgroups' worth, 2^30 groups; the grid is
+// then 2^22 workgroups that go around, and positions are counted in 64 bits
+// (below it, a launch's threads and all group numbers are well inside the 32
+// bits that they have).  Binary32 goes by the traded pieces of layer.hpp, over
+// the 64 consecutive groups of a wave whatever rows they are in.
 template <typename T, int HINT, bool NARROW, bool FAR>
 __global__ __launch_bounds__(kDropBlock) void dropout_kernel(DropoutArgs<T> a)
 {
@@ -205,7 +206,7 @@ int launch(void* out, uint64_t ld_out, const void* x, uint64_t ld_x, const void*
                      bias_dtype == ZERO_F32, d};
     const uint64_t grid = (rows * a.groups + kDropBlock - 1) / kDropBlock;
     const uint64_t bytes = rows * cols * sizeof(T) * (residual ? 3 : 2);
-    constexpr uint64_t kMost = 1u << 22;
+    constexpr uint64_t kMost = 1u << 22;           // past it: FAR
     const dim3 block(kDropBlock);
     if (grid > kMost) {
         if (cols < 8)

@@ -142,3 +142,10 @@ def test_generator_calls_refuse_other_devices(Z, monkeypatch, name):
     call(_State(0))
     call(_State(0), _Stream(0))
     assert len(calls) == 2
+
+
+def test_the_package_exports_every_entry_point(Z):
+    """`from zero_partitioned_mixed_flatten_amd import *` has each function and constant of the binding."""
+    public = {n for n in dir(Z) if n.startswith(("zero_", "ZERO_"))}
+    assert public <= set(Z.__all__), public - set(Z.__all__)
+    assert set(Z.__all__) <= set(dir(Z))

@@ -26,8 +26,8 @@ from .stepper import AccumStep, HostContext, OffloadStep, OneBitStep, ShardStep,
 
 lib()
 
-__all__ = ["EXPORTS", "NORM_PARTIAL_BYTES", "STATE_BYTES", "ZERO_F16", "ZERO_F32", "AccumStep", "BucketPlan", "HParams",
-           "Segment", "ShardStep", "StepState", "ZeroError", "hparams", "lib", "make_segments", "read_state",
+__all__ = ["EXPORTS", "NORM_PARTIAL_BYTES", "STATE_BYTES", "ZERO_BF16", "ZERO_F16", "ZERO_F32", "AccumStep", "BucketPlan",
+           "HParams", "Segment", "ShardStep", "StepState", "ZeroError", "hparams", "lib", "make_segments", "read_state",
            "zero_bucket_segments", "zero_decide_workspace_bytes", "zero_flatten_bucket", "zero_flatten_buckets",
            "zero_flatten_norm_bucket", "zero_flatten_norm_bucket_f32", "zero_flatten_norm_partials",
            "zero_norm_workspace_bytes", "zero_shard_adam_step", "zero_shard_adam_step_f32", "zero_shard_decide", "zero_shard_decide_f32",

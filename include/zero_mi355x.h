@@ -563,8 +563,8 @@ int zero_host_stream_copy(zero_host_ctx_t* ctx, void* dst, const void* src, uint
 /* ---- layer operators ---------------------------------------------------
  *
  * The operators below work on matrices of `rows` rows (tokens) of `cols`
- * elements (the hidden size), rows * ld elements apart: element (i, j) of x is
- * x[i * ld_x + j].  Common to all of them:
+ * elements (the hidden size), ld elements from one row to the next: element
+ * (i, j) of x is x[i * ld_x + j].  Common to all of them:
  *   - dtype is the type of every matrix: ZERO_F16, ZERO_BF16 or ZERO_F32.
  *     vec_dtype is the type of w, b and bias, grad_dtype that of dw, db and
  *     dbias: dtype or ZERO_F32, and not looked at when all of them are NULL;
@@ -584,8 +584,8 @@ int zero_host_stream_copy(zero_host_ctx_t* ctx, void* dst, const void* src, uint
  * Errors of all of them: ZERO_EINVAL (a required pointer NULL with rows > 0,
  * a bad type, two equal outputs (mean and rstd among them), eps not finite and
  * > 0 in binary32, p not in [0, 1]), ZERO_EALIGN, ZERO_ERANGE (rows > 2^40,
- * cols > 2^30, cols = 0 for a norm, ld < cols, rows * ld > 2^56, a workspace
- * too small), ZERO_EHIP. */
+ * cols > 2^30, cols = 0 for a norm, with rows > 1 ld < cols, ld > 2^50 or
+ * rows * ld > 2^56, a workspace too small), ZERO_EHIP. */
 
 /* The state of the dropout generator in DEVICE memory (16 bytes, 8-byte
  * aligned).  The mask of a call is a function of (seed, step, site, rows'

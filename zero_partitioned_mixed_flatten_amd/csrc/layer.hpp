@@ -22,10 +22,15 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 // global access serves in one instruction (rows of an odd width start
 // anywhere).
 
-// Cache hints of a pass: bit 0, loads nontemporal; bit 1, stores.  Stores
-// always are; loads only in a call that moves more than kStreamBytes: what a
-// smaller one reads, the operator before it has mostly left in the 256 MB
-// cache, while a larger one runs a little better past it.  Measured, plain
+// Cache hints of a pass: bit 0, loads nontemporal; bit 1, stores.  The passes
+// that read each element once store so always and load so in a call that moves
+// more than kStreamBytes: what a smaller one reads, the operator before it has
+// mostly left in the 256 MB cache, while a larger one runs a little better past
+// it.  What does not follow this: rows too wide for the registers are loaded
+// plainly in the forward passes and the first time of a backward pass (the
+// joined form's r is stored plainly too, it is read again), nontemporally the
+// second time; what goes by elements (rows of fewer than 8 columns, a row's
+// short last group when stored) and partial sums are plain.  Measured, plain
 // against nontemporal loads: layer norm forward 1600 x 8192 fp16 (52 MB) 11.0
 // and 13.3 us, backward 800 x 8192 (39 MB) 17.4 and 22.6 us, joined forward
 // 1600 x 8192 (105 MB) 23.7 and 22.7 us, 16384 x 8192 (1.07 GB) 203 and 183 us.

@@ -7,9 +7,9 @@
 //   y = (r - mean) * rstd * w + b
 //
 // The variance is summed from the deviations, after the mean, so a row far
-// from zero loses nothing.  The joined form rounds r to the element type
-// once, where it stores it, and normalises the stored value: what the backward
-// pass reads again.
+// from zero loses only what its mean does, summed and rounded in binary32.  The
+// joined form rounds r to the element type once, where it stores it, and
+// normalises the stored value: what the backward pass reads again.
 #include "layer.hpp"
 
 namespace zero {
@@ -54,7 +54,9 @@ __global__ __launch_bounds__(BLOCK) void norm_fwd_kernel(FwdArgs<T> a)
     // this one is summed up, into the same registers, and the vectors are read
     // again from the caches (1000 x 16384 49 us, 300 x 16384 20; with the rest's
     // way and 38 registers spilt 76 and 34, and three passes 70 and 28; 3000 x
-    // 10240, 640 threads, 99 so and 91 the rest's way)
+    // 10240, 640 threads, 99 so and 91 the rest's way).  No vector register is
+    // spilt so, but 140 scalars are, to lanes of vector registers (the other
+    // joined forms spill up to 32 of them)
     constexpr bool kLate = JOIN && sizeof(T) == 4 && BLOCK == 1024;
     __shared__ alignas(16) float scratch[2 * BLOCK / 64];
     uint32_t parity = 0;

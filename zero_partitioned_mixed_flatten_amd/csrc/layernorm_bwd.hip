@@ -96,7 +96,7 @@ __global__ __launch_bounds__(BLOCK) void rows_bwd_kernel(BwdArgs<T> a)
     auto work = [&](uint64_t row, Row& cur) {
         const bool live = row < a.rows;
         // the mask ahead of the loads' use; binary32 rows leave no registers to
-        // keep it (8192 x 1600 joined 63 us so, 56 with it drawn at the end)
+        // keep it (8192 x 1600 joined 58.4 us so, 56.2 with it drawn at the end)
         constexpr bool kEarly = sizeof(T) == 2;
         u32x4 bits;
         if (DROP && kEarly)
@@ -431,7 +431,9 @@ uint64_t workspace_need(uint64_t rows, uint64_t cols)
 
 // Rows in flight ahead of the present one: as many as the registers hold
 // (layer norm alone, 16-bit elements, two: 8192 x 1600 21.8 us against 22.1 with
-// one, 1600 x 8192 28.5 against 29.3).
+// one, 1600 x 8192 28.5 against 29.3).  The binary32 joined form has one and
+// still spills vector registers at some widths: 9 with 8 or 16 threads a row,
+// 12 with 32, 2 with 128 to 512, none with 1, 64 or 1024.
 template <typename T, bool NORM, bool DROP, int TPR>
 void launch_rows(const BwdArgs<T>& a, uint64_t chunks, hipStream_t s)
 {

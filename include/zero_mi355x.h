@@ -690,6 +690,160 @@ int zero_dropout_layernorm_bwd(void* dx, uint64_t ld_dx, void* dr, uint64_t ld_d
                                const zero_rng_t* dev_rng, uint32_t site, void* workspace, size_t workspace_bytes,
                                void* stream);
 
+/* ---- attention operators -------------------------------------------------
+ *
+ * The attention side of a transformer block, beside the layer operators: the
+ * norms of queries and keys with the position rotation, and causal attention
+ * with a window, first tokens that stay visible and a learned bias.  Common to
+ * them:
+ *   - tokens are packed: those of a batch's sequences one after another.  An
+ *     activation is tokens x heads x dim elements, (i, h, d) at
+ *     i * ld + h * hs + d: ld and hs of at least dim take a slice of a joint
+ *     projection's output, heads before or after queries, keys and values;
+ *   - the elements between are neither read nor written;
+ *   - arithmetic and sums are binary32, a stored value is rounded once, to
+ *     nearest even; what the matrix units take in between is named below;
+ *   - pointers are device memory, aligned to their element and no more;
+ *   - the stream belongs to the current device, and so does every pointer;
+ *   - tokens may be 0 (weight gradients are then sums of nothing: 0, or with
+ *     accumulate left as they are);
+ *   - results do not depend on timing: equal calls give equal bits. */
+
+/* The norms of queries and keys over each head, with the position rotation in
+ * the same pass.  For each token and head of x (q: tokens x heads x dim, k:
+ * tokens x kv_heads x dim), over the head's elements:
+ *   rstd = 1 / sqrt(mean(x^2) + eps),  u = x * rstd * w  (w NULL: 1),
+ *   out = u with its first `rot` elements turned in pairs: for the pair p <
+ *   rot / 2 with the position's (cos, sin),
+ *     (a, b) -> (a cos - b sin, b cos + a sin),
+ *   elements (p, p + rot / 2), or with interleaved (2p, 2p + 1).
+ * dtype: ZERO_F16, ZERO_BF16 or ZERO_F32; wq and wk: dim elements of vec_dtype,
+ * dtype or ZERO_F32.  dim even and at most 256, rot even and at most dim (0:
+ * no rotation, table not looked at).  kv_heads may be 0 (k, k_out and wk NULL).
+ * table: device, table_rows x rot / 2 x (cos, sin) binary32, 16-byte aligned
+ * (zero_rope_table).  A token's position is dev_positions[i] (device), or where
+ * that is NULL i mod period (period 0: i); one not in the table gives NaN.
+ * An output may be its own input (the same address, ld and hs).
+ * Errors: ZERO_EINVAL (NULL, a type, heads = 0, dim or rot odd or 0, rot > dim,
+ *         eps not finite and > 0 in binary32, rot without a table, q_out ==
+ *         k_out, k's arguments without kv_heads), ZERO_EALIGN, ZERO_ERANGE (dim
+ *         > 256, more than 2^30 tokens or table rows, 65536 heads or 2^34 heads
+ *         of all tokens, ld or hs < dim or > 2^50, an extent > 2^56), ZERO_EHIP. */
+int zero_qk_norm_rope_fwd(void* q_out, uint64_t ld_q_out, uint64_t hs_q_out, void* k_out, uint64_t ld_k_out,
+                          uint64_t hs_k_out, const void* q, uint64_t ld_q, uint64_t hs_q, const void* k, uint64_t ld_k,
+                          uint64_t hs_k, const void* wq, const void* wk, int vec_dtype, uint64_t tokens, uint32_t heads,
+                          uint32_t kv_heads, uint32_t dim, int dtype, double eps, const float* table,
+                          uint64_t table_rows, uint32_t rot, int interleaved, const int32_t* dev_positions,
+                          uint64_t period, void* stream);
+
+/* Bytes of device workspace zero_qk_norm_rope_bwd needs (any type and rot); 0
+ * for no tokens or a refused shape. */
+size_t zero_qk_workspace_bytes(uint64_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t dim);
+
+/* The backward pass, from the x of the forward pass (q, k) and the gradients
+ * at its outputs:
+ *   g' = the gradient turned back,  h = x * rstd,  g = g' * w,
+ *   dx = rstd * (g - h * mean(g * h)),
+ *   dw = sum over tokens and heads of g' * h (of the unrounded values)
+ * dwq and dwk (NULL: not wanted): dim elements of grad_dtype, dtype or
+ * ZERO_F32, stored, or with accumulate added to what is there, then rounded
+ * once.  dq may be dq_out or q, dk likewise (the same address, ld and hs).
+ * workspace: device, 16-byte aligned, >= zero_qk_workspace_bytes(...), not
+ * looked at where neither dwq nor dwk is wanted; contents need no
+ * initialisation; calls that share it must be ordered. */
+int zero_qk_norm_rope_bwd(void* dq, uint64_t ld_dq, uint64_t hs_dq, void* dk, uint64_t ld_dk, uint64_t hs_dk, void* dwq,
+                          void* dwk, int grad_dtype, int accumulate, const void* dq_out, uint64_t ld_dq_out,
+                          uint64_t hs_dq_out, const void* dk_out, uint64_t ld_dk_out, uint64_t hs_dk_out, const void* q,
+                          uint64_t ld_q, uint64_t hs_q, const void* k, uint64_t ld_k, uint64_t hs_k, const void* wq,
+                          const void* wk, int vec_dtype, uint64_t tokens, uint32_t heads, uint32_t kv_heads,
+                          uint32_t dim, int dtype, double eps, const float* table, uint64_t table_rows, uint32_t rot,
+                          int interleaved, const int32_t* dev_positions, uint64_t period, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Enqueue the angles of positions 0 ... positions-1: table[t][p] = (cos, sin) of
+ * t * base^(-2p / rot), p < rot / 2, formed in binary64 and rounded once.
+ * table: device, positions x rot / 2 x 2 binary32, 16-byte aligned.
+ * Errors: ZERO_EINVAL (NULL, base not finite and > 0, rot odd), ZERO_EALIGN,
+ *         ZERO_ERANGE (positions > 2^30, rot > 256), ZERO_EHIP. */
+int zero_rope_table(float* table, uint64_t positions, uint32_t rot, double base, void* stream);
+
+#define ZERO_MAX_BUCKETS 64
+
+/* What a model's attention is, the same for every call. */
+typedef struct {
+    uint32_t heads;             /* of queries; a multiple of kv_heads, <= 65536 */
+    uint32_t kv_heads;          /* of keys and values: query head h reads h / (heads / kv_heads) */
+    uint32_t dim;               /* elements of a head: a multiple of 8, <= 128 */
+    uint32_t sinks;             /* first tokens of a sequence that stay visible */
+    uint64_t window;            /* keys a query sees: itself and window - 1 before it; 0: no limit */
+    double scale;               /* > 0 */
+    uint32_t buckets;           /* of the bias; 0: no bias; <= ZERO_MAX_BUCKETS */
+    uint32_t reserved;          /* 0 */
+    uint32_t starts[ZERO_MAX_BUCKETS]; /* bucket b holds the distances starts[b] ... starts[b+1]-1, the last all beyond; ascending, starts[0] = 0 */
+} zero_attention_t;
+
+/* The usual borders for `buckets` buckets, into starts[buckets]: with half =
+ * buckets / 2 the first half one distance each, 0 ... half-1, and bucket
+ * half + b from the distance half * (max_distance / half)^(b / (buckets -
+ * half)) on, rounded up (a whole number stays; at least one past the bucket
+ * before).  Compared in whole numbers, so a distance on a border is in the
+ * bucket that begins there.  Host only.
+ * Errors: ZERO_EINVAL (NULL, buckets = 0, max_distance <= half for more than
+ *         one bucket), ZERO_ERANGE (too many, max_distance > 2^30), ZERO_ENOMEM. */
+int zero_attention_buckets(uint32_t* starts, uint32_t buckets, uint32_t max_distance);
+
+/* Causal attention.  Token i of a sequence sees token j of the same where
+ * j <= i and (i - j < window or j < sinks):
+ *   s = scale * q_i . k_j (+ bias[h][bucket(i - j)]),   p = softmax(s),
+ *   o_i = sum over j of p v_j,   lse[h][i] = log of the sum over j of exp(s)
+ * q and o: tokens x heads x dim; k and v: tokens x kv_heads x dim; all of type
+ * dtype, ZERO_F16 or ZERO_BF16.  lse: binary32, heads x tokens (NULL: not
+ * kept; the backward pass needs it).  bias: heads x buckets of dtype or
+ * ZERO_F32 (vec_dtype); NULL exactly where buckets is 0.
+ * dev_offsets: device, sequences + 1 ascending token indices: sequence n is
+ * the tokens dev_offsets[n] ... dev_offsets[n+1]-1 (its length may be 0); rows
+ * of o and lse outside all sequences stay as they are.  NULL: sequences of
+ * equal length, tokens / sequences.  (Indices out of order or range are
+ * clamped to the tensors; which rows are then computed is undefined.)
+ * The unnormalised weights are rounded to dtype for the product with v.
+ * o must not overlap an input.
+ * Errors: ZERO_EINVAL (NULL, a type, heads, dim or scale out of the above,
+ *         sequences = 0 with tokens, tokens not a multiple of sequences
+ *         without offsets, starts not ascending from 0, bias without buckets
+ *         or the other way round), ZERO_EALIGN, ZERO_ERANGE (more than 2^30
+ *         tokens or sequences, heads * (tokens / 128 + sequences) >= 2^31, ld
+ *         or hs < dim or > 2^50, an extent > 2^56, dim > 128), ZERO_EHIP. */
+int zero_attention_fwd(void* o, uint64_t ld_o, uint64_t hs_o, float* lse, const void* q, uint64_t ld_q, uint64_t hs_q,
+                       const void* k, uint64_t ld_k, uint64_t hs_k, const void* v, uint64_t ld_v, uint64_t hs_v,
+                       const void* bias, int vec_dtype, const zero_attention_t* params, uint64_t tokens,
+                       const int32_t* dev_offsets, uint64_t sequences, int dtype, void* stream);
+
+/* Bytes of device workspace zero_attention_bwd needs; 0 for no tokens or a
+ * refused shape. */
+size_t zero_attention_workspace_bytes(const zero_attention_t* params, uint64_t tokens, uint64_t sequences);
+
+/* The backward pass of zero_attention_fwd, from the o and lse it stored:
+ *   p = exp(s - lse),   ds = p * (do_i . v_j - do_i . o_i),
+ *   dq_i = scale * sum over j of ds k_j,   dk_j = scale * sum over i of ds q_i,
+ *   dv_j = sum over i of p do_i,   dbias[h][b] = sum of ds over the pairs of b
+ * dk and dv are sums over the query heads that share a key head, too.  p and
+ * ds are rounded to dtype for the products (ds for binary16 in units that go
+ * by the size of do); dbias is a sum of the unrounded ds.  dbias (NULL: not
+ * wanted): heads x buckets of grad_dtype, dtype or ZERO_F32, stored, or with
+ * accumulate added to what is there, then rounded once.
+ * dq, dk and dv must not overlap an input or each other.  Rows outside all
+ * sequences stay as they are.  workspace: device, 16-byte aligned, >=
+ * zero_attention_workspace_bytes(params, tokens, sequences); contents need no
+ * initialisation; calls that share it must be ordered.
+ * Errors: as for zero_attention_fwd, and ZERO_ERANGE for a workspace too small. */
+int zero_attention_bwd(void* dq, uint64_t ld_dq, uint64_t hs_dq, void* dk, uint64_t ld_dk, uint64_t hs_dk, void* dv,
+                       uint64_t ld_dv, uint64_t hs_dv, void* dbias, int grad_dtype, int accumulate, const void* dout,
+                       uint64_t ld_dout, uint64_t hs_dout, const void* o, uint64_t ld_o, uint64_t hs_o,
+                       const float* lse, const void* q, uint64_t ld_q, uint64_t hs_q, const void* k, uint64_t ld_k,
+                       uint64_t hs_k, const void* v, uint64_t ld_v, uint64_t hs_v, const void* bias, int vec_dtype,
+                       const zero_attention_t* params, uint64_t tokens, const int32_t* dev_offsets, uint64_t sequences,
+                       int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- measurement reference ------------------------------------------ */
 
 /* A plain streaming copy of `bytes` bytes (dst and src device, 16-byte

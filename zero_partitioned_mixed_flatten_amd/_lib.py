@@ -25,7 +25,9 @@ EXPORTS = ("zero_status_string", "zero_state_bytes", "zero_bucket_segments", "ze
            "zero_offload_step", "zero_host_stream_copy", "zero_onebit_state_init", "zero_onebit_workspace_bytes",
            "zero_onebit_step", "zero_shard_norm_overflow_noalloc", "zero_shard_decide_f32", "zero_rng_init",
            "zero_rng_advance", "zero_dropout_fwd", "zero_dropout_bwd", "zero_layer_workspace_bytes",
-           "zero_layernorm_fwd", "zero_layernorm_bwd", "zero_dropout_layernorm_fwd", "zero_dropout_layernorm_bwd")
+           "zero_layernorm_fwd", "zero_layernorm_bwd", "zero_dropout_layernorm_fwd", "zero_dropout_layernorm_bwd",
+           "zero_rope_table", "zero_qk_norm_rope_fwd", "zero_qk_workspace_bytes", "zero_qk_norm_rope_bwd",
+           "zero_attention_buckets", "zero_attention_fwd", "zero_attention_workspace_bytes", "zero_attention_bwd")
 NORM_PARTIAL_BYTES = 16
 
 
@@ -74,6 +76,16 @@ class OneBitState(C.Structure):
 
 class RngState(C.Structure):
     _fields_ = [("seed", C.c_uint64), ("step", C.c_uint32), ("reserved", C.c_uint32)]
+
+
+ZERO_MAX_BUCKETS = 64
+
+
+class AttentionParams(C.Structure):
+    """What a model's attention is (attention_params makes one)."""
+    _fields_ = [("heads", C.c_uint32), ("kv_heads", C.c_uint32), ("dim", C.c_uint32), ("sinks", C.c_uint32),
+                ("window", C.c_uint64), ("scale", C.c_double), ("buckets", C.c_uint32), ("reserved", C.c_uint32),
+                ("starts", C.c_uint32 * ZERO_MAX_BUCKETS)]
 
 
 RNG_BYTES = C.sizeof(RngState)
@@ -150,10 +162,26 @@ def lib():
                                                  i32, f64, f64, vp, u32, vp]
         L.zero_dropout_layernorm_bwd.argtypes = [vp, u64, vp, u64, vp, vp, vp, i32, i32, vp, u64, vp, u64, vp, u64, vp,
                                                  vp, vp, i32, u64, u64, i32, f64, vp, u32, vp, C.c_size_t, vp]
+        heads = [vp, u64, u64]                      # address, token stride, head stride
+        L.zero_rope_table.argtypes = [vp, u64, u32, f64, vp]
+        L.zero_qk_norm_rope_fwd.argtypes = heads * 4 + [vp, vp, i32, u64, u32, u32, u32, i32, f64, vp, u64, u32, i32, vp,
+                                                        u64, vp]
+        L.zero_qk_workspace_bytes.argtypes = [u64, u32, u32, u32]
+        L.zero_qk_workspace_bytes.restype = C.c_size_t
+        L.zero_qk_norm_rope_bwd.argtypes = heads * 2 + [vp, vp, i32, i32] + heads * 4 + [
+            vp, vp, i32, u64, u32, u32, u32, i32, f64, vp, u64, u32, i32, vp, u64, vp, C.c_size_t, vp]
+        L.zero_attention_buckets.argtypes = [C.POINTER(u32), u32, u32]
+        params = C.POINTER(AttentionParams)
+        L.zero_attention_fwd.argtypes = heads + [vp] + heads * 3 + [vp, i32, params, u64, vp, u64, i32, vp]
+        L.zero_attention_workspace_bytes.argtypes = [params, u64, u64]
+        L.zero_attention_workspace_bytes.restype = C.c_size_t
+        L.zero_attention_bwd.argtypes = heads * 3 + [vp, i32, i32] + heads * 2 + [vp] + heads * 3 + [
+            vp, i32, params, u64, vp, u64, i32, vp, C.c_size_t, vp]
         for name in EXPORTS:
             if name not in ("zero_status_string", "zero_norm_workspace_bytes", "zero_flatten_norm_partials",
                             "zero_decide_workspace_bytes", "zero_host_destroy", "zero_onebit_workspace_bytes",
-                            "zero_layer_workspace_bytes"):
+                            "zero_layer_workspace_bytes", "zero_qk_workspace_bytes",
+                            "zero_attention_workspace_bytes"):
                 getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -759,3 +787,212 @@ def zero_dropout_layernorm_bwd(dx, dr, dw, db, dbias, dy, dres, r, mean, rstd, w
     c.check(lib().zero_dropout_layernorm_bwd(*c.mat(dx), *c.mat(dr), dw_, db_, dbias_, gtype, int(bool(accumulate)),
                                              *c.mat(dy), *c.mat(dres), *c.mat(r), c.stat(mean), c.stat(rstd), w_, vtype,
                                              c.rows, c.cols, c.code, p, c.rng(dev_rng), c.site(site), wptr, wbytes, c.stream))
+
+
+# ---- attention operators -------------------------------------------------------------
+# Activations are torch tensors of shape (tokens, heads, dim) whose last
+# dimension is contiguous, the others any distance apart (a slice of a joint
+# projection's output).  Every tensor lives on the current device, which the
+# stream belongs to.
+
+class _HeadsCall(_LayerCall):
+    """One call's tokens, type and device (from its first tensor) and the checks
+    of its tensors."""
+    __slots__ = ("dim",)
+
+    def __init__(self, fn: str, ref, stream):
+        super().__init__(fn, ref, stream)
+        if len(self.shape) != 3:
+            raise ValueError(f"{fn}: expected (tokens, heads, dim), got {tuple(self.shape)}")
+        self.rows, self.dim = self.shape[0], self.shape[2]
+
+    def heads(self, t, heads: int) -> Tuple[int, int, int]:
+        """(address, token stride, head stride) of a tokens x heads x dim tensor."""
+        if t.dtype is not self.dtype or t.get_device() != self.device:
+            raise TypeError(f"{self.fn}: expected {self.dtype} on device {self.device}, got {t.dtype} on {t.device}")
+        if t.shape != (self.rows, heads, self.dim):
+            raise ValueError(f"{self.fn}: expected {(self.rows, heads, self.dim)}, got {tuple(t.shape)}")
+        ld, hs, one = t.stride()
+        if one != 1 and self.dim > 1:
+            raise ValueError(f"{self.fn}: expected a contiguous last dimension")
+        return t.data_ptr(), ld, hs
+
+    def vector(self, t, shape) -> Tuple[int, int]:
+        """(address, type) of a contiguous parameter of the activations' type or float32; (0, theirs) for None."""
+        if t is None:
+            return 0, self.code
+        if t.get_device() != self.device or (t.dtype is not self.dtype and t.dtype is not _torch.float32):
+            raise TypeError(f"{self.fn}: expected {self.dtype} or torch.float32 on device {self.device}, got {t.dtype} on "
+                            f"{t.device}")
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{self.fn}: expected a contiguous {tuple(shape)}, got {tuple(t.shape)}")
+        return t.data_ptr(), self.code if t.dtype is self.dtype else ZERO_F32
+
+    def pair(self, a, b) -> Tuple[int, int, int]:
+        """Two vectors over dim (None: absent) that share a type: their addresses and it."""
+        pa, ta = self.vector(a, (self.dim,))
+        pb, tb = self.vector(b, (self.dim,))
+        if a is not None and b is not None and ta != tb:
+            raise TypeError(f"{self.fn}: the vectors are {a.dtype} and {b.dtype}: they share one type")
+        return pa, pb, ta if a is not None else tb
+
+    def ints(self, t, count) -> int:
+        """The address of a contiguous int32 vector (count None: of any length; 0 for None)."""
+        if t is None:
+            return 0
+        if t.dtype is not _torch.int32 or t.get_device() != self.device:
+            raise TypeError(f"{self.fn}: expected torch.int32 on device {self.device}, got {t.dtype} on {t.device}")
+        if t.dim() != 1 or not t.is_contiguous() or (count is not None and t.numel() != count):
+            raise ValueError(f"{self.fn}: expected a contiguous vector{'' if count is None else f' of {count} elements'}, got "
+                             f"{tuple(t.shape)}")
+        return t.data_ptr()
+
+    def space(self, ws, need, stream):
+        """(tensor, address, bytes) as workspace(), for a size that need() gives."""
+        if ws is None:
+            size = max(16, need())
+            if stream is None:
+                ws = _torch.empty(size, dtype=_torch.uint8, device=f"cuda:{self.device}")
+            else:
+                with _torch.cuda.stream(stream):
+                    ws = _torch.empty(size, dtype=_torch.uint8, device=f"cuda:{self.device}")
+            return ws, ws.data_ptr(), size
+        return self.workspace(ws, stream)
+
+
+def zero_rope_table(table, base: float = 10000.0, stream=None) -> None:
+    """table[t, p] = (cos, sin) of t * base^(-2p / rot); table: float32 of shape (positions, rot / 2, 2)."""
+    fn = "zero_rope_table"
+    c = _LayerCall(fn, table, stream)
+    if c.code != ZERO_F32 or table.dim() != 3 or c.shape[2] != 2 or not table.is_contiguous():
+        raise ValueError(f"{fn}: expected a contiguous float32 (positions, rot / 2, 2), got {table.dtype} {tuple(c.shape)}")
+    c.check(lib().zero_rope_table(table.data_ptr(), c.shape[0], 2 * c.shape[1], base, c.stream))
+
+
+def _table(c, table) -> Tuple[int, int, int]:
+    """(address, rows, rot) of a rotation table; zeros for None."""
+    if table is None:
+        return 0, 0, 0
+    if table.dtype is not _torch.float32 or table.get_device() != c.device:
+        raise TypeError(f"{c.fn}: expected a float32 table on device {c.device}, got {table.dtype} on {table.device}")
+    if table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous():
+        raise ValueError(f"{c.fn}: expected a contiguous table (positions, rot / 2, 2), got {tuple(table.shape)}")
+    return table.data_ptr(), table.shape[0], 2 * table.shape[1]
+
+
+def _side(c, *ts):
+    """The heads of a tensor's group and each one's (address, strides); all None: none."""
+    if all(t is None for t in ts):
+        return 0, [0, 0, 0] * len(ts)
+    if any(t is None for t in ts):
+        raise ValueError(f"{c.fn}: the keys' tensors go together")
+    n = ts[0].shape[1] if ts[0].dim() == 3 else -1
+    return n, [x for t in ts for x in c.heads(t, n)]
+
+
+def zero_qk_workspace_bytes(tokens: int, heads: int, kv_heads: int, dim: int) -> int:
+    return int(lib().zero_qk_workspace_bytes(tokens, heads, kv_heads, dim))
+
+
+def zero_qk_norm_rope_fwd(q_out, k_out, q, k, wq, wk, table, eps: float = 1e-6, positions=None, period: int = 0,
+                          interleaved: bool = False, stream=None) -> None:
+    """q_out and k_out: each head of q and k normed (times wq, wk), then turned by its token's position.  k and k_out may be None."""
+    c = _HeadsCall("zero_qk_norm_rope_fwd", q_out, stream)
+    hq, qs = _side(c, q_out, q)
+    hk, ks = _side(c, k_out, k)
+    c.check(lib().zero_qk_norm_rope_fwd(*qs[:3], *ks[:3], *qs[3:], *ks[3:], *c.pair(wq, wk), c.rows, hq, hk, c.dim, c.code, eps,
+                                        *_table(c, table), int(bool(interleaved)), c.ints(positions, c.rows), period,
+                                        c.stream))
+
+
+def zero_qk_norm_rope_bwd(dq, dk, dwq, dwk, dq_out, dk_out, q, k, wq, wk, table, eps: float = 1e-6, positions=None,
+                          period: int = 0, interleaved: bool = False, accumulate: bool = False, workspace=None,
+                          stream=None) -> None:
+    """dq and dk: the gradients at q and k from those at the outputs; dwq and dwk: the norms' weights' (None: not wanted)."""
+    c = _HeadsCall("zero_qk_norm_rope_bwd", dq, stream)
+    hq, qs = _side(c, dq, dq_out, q)
+    hk, ks = _side(c, dk, dk_out, k)
+    ws, wptr, wbytes = None, 0, 0
+    if dwq is not None or dwk is not None:
+        ws, wptr, wbytes = c.space(workspace, lambda: lib().zero_qk_workspace_bytes(c.rows, hq, hk, c.dim), stream)
+    c.check(lib().zero_qk_norm_rope_bwd(*qs[:3], *ks[:3], *c.pair(dwq, dwk), int(bool(accumulate)), *qs[3:6], *ks[3:6], *qs[6:],
+                                        *ks[6:], *c.pair(wq, wk), c.rows, hq, hk, c.dim, c.code, eps, *_table(c, table),
+                                        int(bool(interleaved)), c.ints(positions, c.rows), period, wptr, wbytes, c.stream))
+
+
+def zero_attention_buckets(buckets: int, max_distance: int) -> List[int]:
+    """The first distance of each of `buckets` buckets: the first half of one distance each, the others in equal ratios."""
+    out = (C.c_uint32 * max(1, buckets))()
+    _check("zero_attention_buckets", lib().zero_attention_buckets(out, buckets, max_distance))
+    return list(out)
+
+
+def attention_params(heads: int, kv_heads: int, dim: int, window: int = 0, sinks: int = 0, scale: Optional[float] = None,
+                     starts: Optional[Sequence[int]] = None) -> AttentionParams:
+    """window: keys a query sees, itself the last (0: no limit); sinks: first tokens that stay visible; scale None:
+    dim^-0.5; starts: the first distance of each bucket of the bias (None: no bias)."""
+    starts = [] if starts is None else list(starts)
+    for name, v, most in [("heads", heads, 32), ("kv_heads", kv_heads, 32), ("dim", dim, 32), ("sinks", sinks, 32),
+                          ("window", window, 64)] + [("starts", v, 32) for v in starts]:
+        if not 0 <= v < 1 << most:
+            raise ValueError(f"attention_params: {name} {v} is not in [0, 2^{most})")
+    if len(starts) > ZERO_MAX_BUCKETS:
+        raise ValueError(f"attention_params: {len(starts)} buckets, at most {ZERO_MAX_BUCKETS}")
+    if dim < 1:
+        raise ValueError("attention_params: dim 0")
+    return AttentionParams(heads, kv_heads, dim, sinks, window, dim ** -0.5 if scale is None else scale, len(starts), 0,
+                           (C.c_uint32 * ZERO_MAX_BUCKETS)(*starts))
+
+
+def zero_attention_workspace_bytes(params: AttentionParams, tokens: int, sequences: int) -> int:
+    return int(lib().zero_attention_workspace_bytes(C.byref(params), tokens, sequences))
+
+
+def _lse(c, lse, heads: int) -> int:
+    if lse is None:
+        return 0
+    if lse.dtype is not _torch.float32 or lse.get_device() != c.device:
+        raise TypeError(f"{c.fn}: expected torch.float32 on device {c.device}, got {lse.dtype} on {lse.device}")
+    if lse.shape != (heads, c.rows) or not lse.is_contiguous():
+        raise ValueError(f"{c.fn}: expected a contiguous {(heads, c.rows)}, got {tuple(lse.shape)}")
+    return lse.data_ptr()
+
+
+def _sequences(c, offsets, sequences) -> Tuple[int, int]:
+    """(address of the offsets, number of sequences)."""
+    if offsets is None:
+        if sequences < 0:
+            raise ValueError(f"{c.fn}: {sequences} sequences")
+        return 0, sequences
+    addr = c.ints(offsets, None)
+    if offsets.numel() < 1:
+        raise ValueError(f"{c.fn}: offsets has one element more than there are sequences")
+    return addr, offsets.numel() - 1
+
+
+def zero_attention_fwd(o, lse, q, k, v, params: AttentionParams, bias=None, offsets=None, sequences: int = 1,
+                       stream=None) -> None:
+    """o = softmax(scale q k^T + bias) v over the visible keys; lse: the log of each row's sum (None: not kept).
+    offsets: int32 on the device, the sequences' first tokens and the end; None: `sequences` of equal length."""
+    c = _HeadsCall("zero_attention_fwd", o, stream)
+    hq, hk = params.heads, params.kv_heads
+    c.dim = params.dim
+    bias_, btype = c.vector(bias, (hq, params.buckets))
+    c.check(lib().zero_attention_fwd(*c.heads(o, hq), _lse(c, lse, hq), *c.heads(q, hq), *c.heads(k, hk), *c.heads(v, hk),
+                                     bias_, btype, params, c.rows, *_sequences(c, offsets, sequences), c.code, c.stream))
+
+
+def zero_attention_bwd(dq, dk, dv, dbias, dout, o, lse, q, k, v, params: AttentionParams, bias=None, offsets=None,
+                       sequences: int = 1, accumulate: bool = False, workspace=None, stream=None) -> None:
+    """The gradients of zero_attention_fwd from the o and lse it stored; dbias None: not wanted."""
+    c = _HeadsCall("zero_attention_bwd", dq, stream)
+    hq, hk = params.heads, params.kv_heads
+    c.dim = params.dim
+    bias_, btype = c.vector(bias, (hq, params.buckets))
+    dbias_, gtype = c.vector(dbias, (hq, params.buckets))
+    offsets_, n = _sequences(c, offsets, sequences)
+    ws, wptr, wbytes = c.space(workspace, lambda: lib().zero_attention_workspace_bytes(params, c.rows, n), stream)
+    c.check(lib().zero_attention_bwd(*c.heads(dq, hq), *c.heads(dk, hk), *c.heads(dv, hk), dbias_, gtype,
+                                     int(bool(accumulate)), *c.heads(dout, hq), *c.heads(o, hq), _lse(c, lse, hq),
+                                     *c.heads(q, hq), *c.heads(k, hk), *c.heads(v, hk), bias_, btype, params, c.rows,
+                                     offsets_, n, c.code, wptr, wbytes, c.stream))

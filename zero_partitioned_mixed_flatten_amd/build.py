@@ -24,7 +24,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libzero_mi355x.so")
 SOURCES = ["host.hip", "flatten.hip", "norm.hip", "adam.hip", "onebit.hip", "dropout.hip", "layernorm.hip",
-           "layernorm_bwd.hip"]
+           "layernorm_bwd.hip", "qk_norm_rope.hip", "attention.hip", "attention_bwd.hip"]
 HOST_SOURCES = ["host_step.cpp"]          # plain C++ (the CPU side of the offloaded step)
 ARCH = "gfx950"
 

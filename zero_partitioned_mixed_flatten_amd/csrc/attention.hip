@@ -1,0 +1,308 @@
+// attention.hip -- causal attention over packed sequences with a sliding
+// window, first tokens that stay visible and a learned relative position bias
+// by buckets, forward.
+//
+//   s_ij = scale q_i.k_j + bias[h][bucket(i - j)]   for visible (i, j)
+//   o_i = sum_j exp(s_ij - lse_i) v_j,   lse_i = log sum_j exp(s_ij)
+//
+// One pass over the visible keys with a running maximum and sum of each row.
+#include <type_traits>
+#include <vector>
+
+#include "attention.hpp"
+
+namespace zero {
+namespace attention {
+namespace {
+
+template <typename T>
+struct FwdArgs {
+    Heads<T> o;
+    float* lse;
+    Heads<const T> q, k, v;
+    Shape s;
+    Buckets b;
+    uint32_t slots;
+};
+
+template <typename T, int DIM, bool BIAS>
+__global__ __launch_bounds__(kBlock) void attention_fwd_kernel(FwdArgs<T> a)
+{
+    typedef Tile<DIM> L;
+    __shared__ alignas(16) T keys[2][L::kElems];
+    __shared__ alignas(16) T values[2][L::kElems];
+    __shared__ typename std::conditional<BIAS, BiasLds, int>::type bias;
+
+    const Shape& s = a.s;
+    const uint32_t work = die_local(blockIdx.x, gridDim.x);
+    if (work >= a.slots * s.heads)
+        return;
+    const uint32_t head = work / a.slots;
+    Piece at;
+    if (!find_piece(s, a.slots - 1 - (work - head * a.slots), &at))      // a head's long rows first
+        return;
+    const uint32_t lane = threadIdx.x & 63, c = lane % 32, h = lane / 32;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const uint32_t first = at.first + 32 * wave, mine = first + c;       // the wave's queries, the lane's
+    const uint32_t row = mine < at.len ? mine : at.len - 1;
+    const T* kp = a.k.p + uint64_t(at.start) * a.k.ld + uint64_t(head / s.group) * a.k.hs;
+    const T* vp = a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(head / s.group) * a.v.hs;
+
+    const KeyTiles tiles(s, at.first, kOwn, at.len);
+    Staged<T, DIM> nk, nv;
+    uint32_t t = tiles.begin();
+    fetch<T, DIM>(nk, kp, a.k.ld, t * kTile, at.len, s.dim);
+    fetch<T, DIM>(nv, vp, a.v.ld, t * kTile, at.len, s.dim);
+    Operand<T, DIM> q;
+    load_operand<T, DIM>(q, a.q.p + uint64_t(at.start) * a.q.ld + uint64_t(head) * a.q.hs, a.q.ld, row, s.dim);
+    if constexpr (BIAS) {
+        if (threadIdx.x < a.b.count) {
+            bias.value[threadIdx.x] = bias_value<T>(a.b, head, threadIdx.x) * kLog2e;
+            bias.starts[threadIdx.x] = a.b.starts[threadIdx.x];
+        }
+        __syncthreads();
+    }
+
+    // a tile's bias: one value for each distance, from that of the farthest pair down
+    auto draw_line = [&](uint32_t tile, int buf) {
+        if constexpr (BIAS)
+            if (threadIdx.x < kOwn + kTile - 1) {
+                const int d = int(at.first + kOwn - 1) - int(tile * kTile) - int(threadIdx.x);
+                bias.line[buf][threadIdx.x] = bias.value[bucket_of(bias.starts, a.b.count, d > 0 ? d : 0)];
+            }
+    };
+
+    f32x16 acc[DIM / 32] = {};
+    float m = -INFINITY, sum = 0.0f;               // in units of log2; the sum over this half of the keys
+    put<T, DIM>(keys[0], nk);
+    put<T, DIM>(values[0], nv);
+    draw_line(t, 0);
+    int buf = 0;
+    while (true) {
+        const uint32_t next = tiles.next(t);
+        const bool more = next < tiles.end;
+        __syncthreads();
+        if (more) {
+            fetch<T, DIM>(nk, kp, a.k.ld, next * kTile, at.len, s.dim);
+            fetch<T, DIM>(nv, vp, a.v.ld, next * kTile, at.len, s.dim);
+        }
+        const uint32_t j0 = t * kTile;
+        const Seen see = seen(s, first, 32, j0, kTile);
+        if (see != kNone) {
+            f32x16 x[2];
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub)
+                x[sub] = rows_times<T, DIM>(keys[buf], sub, q);
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const uint32_t j = 32 * sub + row_of(r, h);
+                    float v = x[sub][r] * s.scale2;
+                    if constexpr (BIAS)
+                        v += bias.line[buf][kOwn - 1 - 32 * wave - c + j];
+                    x[sub][r] = see == kAll || visible(s, mine, j0 + j) ? v : -INFINITY;
+                }
+            float top = m;
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    top = fmaxf(top, x[sub][r]);
+            top = halves_max(top);
+            const float base = top == -INFINITY ? 0.0f : top;
+            const float fall = __builtin_amdgcn_exp2f(m - base);
+            m = top;
+            sum *= fall;
+#pragma unroll
+            for (int n = 0; n < DIM / 32; ++n)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    acc[n][r] *= fall;
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    x[sub][r] = __builtin_amdgcn_exp2f(x[sub][r] - base);
+                    sum += x[sub][r];
+                }
+            // the weights are rounded to the element type, as the matrix instruction takes them: half a step of each, where the
+            // binary32 sum they are divided by is of the unrounded ones
+#pragma unroll
+            for (int step = 0; step < 4; ++step)
+                columns_times<T, DIM>(acc, values[buf], step, rounded<T>(x[step / 2], step % 2));
+        }
+        if (!more)
+            break;
+        t = next;
+        buf ^= 1;
+        put<T, DIM>(keys[buf], nk);
+        put<T, DIM>(values[buf], nv);
+        draw_line(t, buf);
+    }
+    sum = halves_sum(sum);
+    const bool live = mine < at.len;
+    store_columns<T, DIM>(a.o.p + uint64_t(at.start) * a.o.ld + uint64_t(head) * a.o.hs, a.o.ld, mine, live, s.dim, acc, 1.0f / sum);
+    if (a.lse && live && h == 0)
+        a.lse[uint64_t(head) * s.tokens + at.start + mine] = (m + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+template <typename T, int DIM>
+int launch(const FwdArgs<T>& a, hipStream_t stream)
+{
+    const uint32_t blocks = uint32_t((uint64_t(a.slots) * a.s.heads + 7) / 8 * 8);
+    if (a.b.table)
+        hipLaunchKernelGGL((attention_fwd_kernel<T, DIM, true>), dim3(blocks), dim3(kBlock), 0, stream, a);
+    else
+        hipLaunchKernelGGL((attention_fwd_kernel<T, DIM, false>), dim3(blocks), dim3(kBlock), 0, stream, a);
+    return launch_status();
+}
+
+}  // namespace
+
+int make_shape(const zero_attention_t* a, uint64_t tokens, const int32_t* dev_offsets, uint64_t sequences, int dtype,
+               const void* bias, int vec_dtype, Shape* s, Buckets* b)
+{
+    if (!a || (dtype != ZERO_F16 && dtype != ZERO_BF16))
+        return ZERO_EINVAL;
+    if (!a->heads || !a->kv_heads || a->heads % a->kv_heads || !a->dim || a->dim % 8)
+        return ZERO_EINVAL;
+    const float scale = float(a->scale), scale2 = float(a->scale * 1.4426950408889634);
+    if (!(scale > 0.0f) || !isfinite(scale) || !(scale2 > 0.0f) || !isfinite(scale2))
+        return ZERO_EINVAL;
+    if (a->heads > kMaxHeads || a->dim > 128 || tokens > kMaxTokens || sequences > kMaxTokens || a->buckets > ZERO_MAX_BUCKETS)
+        return ZERO_ERANGE;
+    if (!!bias != !!a->buckets)
+        return ZERO_EINVAL;
+    if (tokens && (!sequences || (!dev_offsets && tokens % sequences)))
+        return ZERO_EINVAL;
+    if (dev_offsets && !is_aligned(dev_offsets, 4))
+        return ZERO_EALIGN;
+    for (uint32_t i = 0; i < a->buckets; ++i)
+        if (i ? a->starts[i] <= a->starts[i - 1] : a->starts[i] != 0)
+            return ZERO_EINVAL;
+    const int rc = layer::check_vector(bias, vec_dtype, dtype);
+    if (rc)
+        return rc;
+    s->offsets = dev_offsets;
+    s->tokens = uint32_t(tokens);
+    s->sequences = uint32_t(sequences);
+    s->length = sequences ? uint32_t(tokens / sequences) : 0;
+    s->heads = a->heads;
+    s->group = a->heads / a->kv_heads;
+    s->dim = a->dim;
+    s->window = a->window && a->window < 0xffffffffu ? uint32_t(a->window) : 0xffffffffu;
+    s->sinks = a->sinks;
+    s->scale = scale;
+    s->scale2 = scale2;
+    b->table = bias;
+    b->count = a->buckets;
+    b->f32 = vec_dtype == ZERO_F32;
+    for (uint32_t i = 0; i < ZERO_MAX_BUCKETS; ++i)
+        b->starts[i] = i < a->buckets ? a->starts[i] : 0xffffffffu;
+    if (tokens && slots_of(s->tokens, s->sequences, dev_offsets != nullptr) * a->heads >= kMaxPieces)
+        return ZERO_ERANGE;
+    return ZERO_OK;
+}
+
+namespace {
+
+template <typename T>
+int run_fwd(void* o, uint64_t ld_o, uint64_t hs_o, float* lse, const void* q, uint64_t ld_q, uint64_t hs_q, const void* k, uint64_t ld_k,
+            uint64_t hs_k, const void* v, uint64_t ld_v, uint64_t hs_v, const Shape& s, const Buckets& b, hipStream_t stream)
+{
+    const FwdArgs<T> a{{static_cast<T*>(o), ld_o, hs_o}, lse, {static_cast<const T*>(q), ld_q, hs_q}, {static_cast<const T*>(k), ld_k, hs_k},
+                       {static_cast<const T*>(v), ld_v, hs_v}, s, b, uint32_t(slots_of(s.tokens, s.sequences, s.offsets != nullptr))};
+    return s.dim <= 64 ? launch<T, 64>(a, stream) : launch<T, 128>(a, stream);
+}
+
+// A natural number of any size, for comparing powers.
+struct Natural {
+    std::vector<uint32_t> d{1};
+    void times(uint32_t f)
+    {
+        uint64_t carry = 0;
+        for (uint32_t& x : d) {
+            carry += uint64_t(x) * f;
+            x = uint32_t(carry);
+            carry >>= 32;
+        }
+        if (carry)
+            d.push_back(uint32_t(carry));
+    }
+    bool below(const Natural& o) const
+    {
+        if (d.size() != o.d.size())
+            return d.size() < o.d.size();
+        for (size_t i = d.size(); i--;)
+            if (d[i] != o.d[i])
+                return d[i] < o.d[i];
+        return false;
+    }
+};
+
+}  // namespace
+}  // namespace attention
+}  // namespace zero
+
+using namespace zero;
+using namespace zero::attention;
+
+extern "C" int zero_attention_buckets(uint32_t* starts, uint32_t buckets, uint32_t max_distance)
+{
+    if (!starts || !buckets)
+        return ZERO_EINVAL;
+    const uint32_t half = buckets / 2, n = buckets - half;
+    if (buckets > ZERO_MAX_BUCKETS || max_distance > (1u << 30))
+        return ZERO_ERANGE;
+    if (buckets == 1) {
+        starts[0] = 0;
+        return ZERO_OK;
+    }
+    if (max_distance <= half)
+        return ZERO_EINVAL;
+    for (uint32_t b = 0; b < half; ++b)
+        starts[b] = b;
+    try {
+        for (uint32_t b = 0; b < n; ++b) {
+            // the smallest d with d^n half^b >= max_distance^b half^n: bisected in whole numbers
+            Natural most;
+            for (uint32_t i = 0; i < b; ++i) most.times(max_distance);
+            for (uint32_t i = 0; i < n; ++i) most.times(half);
+            uint32_t low = half, high = max_distance;          // high always reaches it
+            while (low < high) {
+                const uint32_t mid = low + (high - low) / 2;
+                Natural x;
+                for (uint32_t i = 0; i < n; ++i) x.times(mid);
+                for (uint32_t i = 0; i < b; ++i) x.times(half);
+                if (x.below(most)) low = mid + 1;
+                else high = mid;
+            }
+            starts[half + b] = low > starts[half + b - 1] ? low : starts[half + b - 1] + 1;
+        }
+    } catch (const std::bad_alloc&) {
+        return ZERO_ENOMEM;
+    }
+    return ZERO_OK;
+}
+
+extern "C" int zero_attention_fwd(void* o, uint64_t ld_o, uint64_t hs_o, float* lse, const void* q, uint64_t ld_q, uint64_t hs_q,
+                                  const void* k, uint64_t ld_k, uint64_t hs_k, const void* v, uint64_t ld_v, uint64_t hs_v,
+                                  const void* bias, int vec_dtype, const zero_attention_t* params, uint64_t tokens,
+                                  const int32_t* dev_offsets, uint64_t sequences, int dtype, void* stream)
+{
+    Shape s;
+    Buckets b;
+    int rc = make_shape(params, tokens, dev_offsets, sequences, dtype, bias, vec_dtype, &s, &b);
+    if (!rc) rc = check_heads(o, ld_o, hs_o, tokens, params->heads, params->dim, dtype);
+    if (!rc) rc = check_heads(q, ld_q, hs_q, tokens, params->heads, params->dim, dtype);
+    if (!rc) rc = check_heads(k, ld_k, hs_k, tokens, params->kv_heads, params->dim, dtype);
+    if (!rc) rc = check_heads(v, ld_v, hs_v, tokens, params->kv_heads, params->dim, dtype);
+    if (!rc && lse && !is_aligned(lse, 4)) rc = ZERO_EALIGN;
+    if (rc || !tokens)
+        return rc;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (dtype == ZERO_F16)
+        return run_fwd<_Float16>(o, ld_o, hs_o, lse, q, ld_q, hs_q, k, ld_k, hs_k, v, ld_v, hs_v, s, b, st);
+    return run_fwd<bf16>(o, ld_o, hs_o, lse, q, ld_q, hs_q, k, ld_k, hs_k, v, ld_v, hs_v, s, b, st);
+}

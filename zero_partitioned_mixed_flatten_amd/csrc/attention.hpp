@@ -1,0 +1,412 @@
+// attention.hpp -- what the attention kernels share (attention.hip,
+// attention_bwd.hip): the arguments, the place of a workgroup's tile in the
+// packed sequences, which keys a tile of queries sees, tiles in LDS and the
+// matrix products on them.
+//
+// All products are 32 x 32 x 16 matrix instructions on binary16 or bfloat16
+// operands with binary32 sums.  Lane l of a wave (c = l % 32, h = l / 32)
+// holds of such a product
+//   A (32 x 16):  row c, columns 8h .. 8h + 7
+//   B (16 x 32):  column c, rows 8h .. 8h + 7
+//   C (32 x 32):  column c, rows row_of(r, h), r = 0 .. 15
+// so each lane owns one column of C: scores are formed with the operand that
+// stays (a wave's 32 queries in the forward pass and for dq, its 32 keys for
+// dk and dv) as the columns, a softmax row is then one lane pair's own, and
+// registers 8n .. 8n + 7 of C, rounded, are a B operand whose 16 rows are the
+// tile's rows 16n + {4h, .. 4h + 3, 8 + 4h, .. 8 + 4h + 3}: the order in which
+// the other operand's rows are read is the same, and no lane exchange is needed.
+#pragma once
+
+#include "layer.hpp"
+
+namespace zero {
+namespace attention {
+
+typedef layer::bf16 bf16;
+typedef layer::bf16x8 bf16x8;
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kWaves = 4;                          // waves of a workgroup
+constexpr int kBlock = 64 * kWaves;
+constexpr int kOwn = 32 * kWaves;                  // rows a workgroup owns: 32 a wave, the columns of its scores
+constexpr int kTile = 64;                          // rows of the tiles it goes over
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
+
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<_Float16> {
+    typedef f16x8 type;
+    static __device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Vec8<bf16> {
+    typedef bf16x8 type;
+    static __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+// The row of C that register r of a lane of half h holds.
+__device__ __forceinline__ constexpr int row_of(int r, int h) { return 8 * (r / 4) + 4 * h + r % 4; }
+
+// tokens x heads x dim elements: (i, h, d) at i * ld + h * hs + d.
+template <typename T>
+struct Heads {
+    T* p;
+    uint64_t ld, hs;
+};
+
+// What the kernels need of the call's geometry.
+struct Shape {
+    const int32_t* offsets;                        // sequences + 1 token indices, or NULL: equal lengths
+    uint32_t tokens, sequences, length;            // length: of each sequence where offsets is NULL
+    uint32_t heads, group, dim;                    // group: query heads that share a key head
+    uint32_t window, sinks;                        // window: 0xffffffff where there is no limit
+    float scale, scale2;                           // scale2: scale * log2(e)
+};
+
+struct Buckets {
+    const void* table;                             // heads x count, NULL: no bias
+    uint32_t count;
+    bool f32;                                      // type of the table: binary32, or the activations'
+    uint32_t starts[ZERO_MAX_BUCKETS];
+};
+
+// ---- the tile of a workgroup --------------------------------------------------------
+// The rows of all sequences are dealt out in pieces of kOwn that do not cross a
+// sequence.  Where the lengths are in device memory, sequence s gets the slots
+// from offsets[s] / kOwn + s on: at least as many as it has pieces, so a slot
+// finds its sequence from the offsets alone, and some slots stay empty.
+// Offsets out of order or out of range are clamped: they give wrong tiles, but
+// none outside the tensors.
+struct Piece {
+    uint32_t start, len;                           // the sequence: first token, tokens
+    uint32_t first;                                // the piece's first row in the sequence
+};
+
+__host__ __device__ inline uint64_t slots_of(uint32_t tokens, uint32_t sequences, bool ragged)
+{
+    if (ragged)
+        return uint64_t(tokens) / kOwn + sequences;
+    return uint64_t(sequences) * ((tokens / sequences + kOwn - 1) / kOwn);
+}
+
+__device__ __forceinline__ bool find_piece(const Shape& s, uint32_t slot, Piece* out)
+{
+    if (!s.offsets) {
+        const uint32_t per = (s.length + kOwn - 1) / kOwn, seq = slot / per;
+        out->start = seq * s.length;
+        out->len = s.length;
+        out->first = (slot - seq * per) * kOwn;
+        return true;
+    }
+    const uint32_t lane = threadIdx.x & 63;
+    auto offset = [&](uint32_t i) {
+        const int32_t o = s.offsets[i];
+        return o < 0 ? 0u : uint32_t(o) < s.tokens ? uint32_t(o) : s.tokens;
+    };
+    uint32_t seq = 0;                              // the number of sequences whose slots begin at or before this one
+    for (uint32_t base = 0; base < s.sequences; base += 64) {
+        const uint32_t i = base + lane;
+        const bool before = i < s.sequences && offset(i < s.sequences ? i : 0) / kOwn + i <= slot;
+        const uint32_t n = __popcll(__ballot(before));
+        seq += n;
+        if (n < 64)
+            break;
+    }
+    if (!seq)
+        return false;
+    --seq;
+    const uint32_t start = __builtin_amdgcn_readfirstlane(offset(seq)), end = __builtin_amdgcn_readfirstlane(offset(seq + 1));
+    const uint32_t begin = start / kOwn + seq;
+    out->start = start;
+    out->len = end > start ? end - start : 0;
+    out->first = (slot - begin) * kOwn;
+    return slot >= begin && uint64_t(slot - begin) * kOwn < out->len;
+}
+
+// Blocks go to the eight dies in turn; neighbours that share a head's keys
+// belong on one, whose L2 then holds them: the blocks of a die take a
+// contiguous part of the work.
+__device__ __forceinline__ uint32_t die_local(uint32_t block, uint32_t blocks) { return block % 8 * (blocks / 8) + block / 8; }
+
+// ---- visibility ------------------------------------------------------------------------
+// Position j is visible to i where j <= i and (i - j < window or j < sinks).
+enum Seen { kNone, kSome, kAll };
+
+// Of the keys [j, j + nk) by the queries [i, i + nq).
+__device__ __forceinline__ Seen seen(const Shape& s, uint32_t i, uint32_t nq, uint32_t j, uint32_t nk)
+{
+    if (j > i + nq - 1)
+        return kNone;
+    // the nearest pair is i - (j + nk - 1), at least 0; the farthest i + nq - 1 - j
+    if (i > j + nk - 1 && i - (j + nk - 1) >= s.window && j >= s.sinks)
+        return kNone;
+    if (j + nk - 1 <= i && (i + nq - 1 - j < s.window || j + nk <= s.sinks))
+        return kAll;
+    return kSome;
+}
+
+__device__ __forceinline__ bool visible(const Shape& s, uint32_t i, uint32_t j)
+{
+    return j <= i && (i - j < s.window || j < s.sinks);
+}
+
+// The key tiles that some query of [i, i + nq) sees, in order: those of the
+// first tokens, then those of the window.
+struct KeyTiles {
+    uint32_t sink_end, win_begin, end;             // in tiles
+
+    __device__ __forceinline__ KeyTiles(const Shape& s, uint32_t i, uint32_t nq, uint32_t len)
+    {
+        const uint32_t last = i + nq < len ? i + nq : len;         // keys below this
+        end = (last + kTile - 1) / kTile;
+        win_begin = i >= s.window ? (i - s.window + 1) / kTile : 0;
+        const uint32_t sinks = s.sinks < last ? s.sinks : last;
+        sink_end = s.window == 0xffffffffu ? 0 : (sinks + kTile - 1) / kTile;
+        if (sink_end >= win_begin)
+            sink_end = win_begin = 0;
+    }
+    __device__ __forceinline__ uint32_t begin() const { return sink_end ? 0 : win_begin; }
+    __device__ __forceinline__ uint32_t next(uint32_t t) const { return t + 1 == sink_end ? win_begin : t + 1; }
+};
+
+// ---- tiles in LDS ---------------------------------------------------------------------
+// kTile rows of DIM elements in 16-byte pieces.  The pieces of a row are
+// permuted by the row, so that both ways to read a tile spread over the 64
+// banks: 16 bytes of one column place in consecutive rows (operand A as rows),
+// and 8-byte parts of 4 rows that the transposing read turns (operand A as
+// columns).
+template <int DIM>
+struct Tile {
+    static constexpr int kPieces = DIM / 8;        // a row
+    static constexpr int kPerThread = kTile * kPieces / kBlock;
+    static constexpr int kElems = kTile * DIM;
+
+    static __device__ __forceinline__ uint32_t twist(uint32_t row)
+    {
+        return DIM == 128 ? (row & 3) << 2 | ((row >> 2) & 3) : ((row >> 1) & 1) << 2 | ((row >> 2) & 3);
+    }
+    static __device__ __forceinline__ uint32_t place(uint32_t row, uint32_t piece)   // in elements
+    {
+        return row * DIM + ((piece ^ twist(row)) * 8);
+    }
+};
+
+template <typename T, int DIM>
+struct Staged {                                    // a thread's pieces of a tile, on their way
+    typename Vec8<T>::type v[Tile<DIM>::kPerThread];
+};
+
+// Rows past the sequence's end repeat its last one (what they give is masked);
+// columns past `dim` are 0.
+template <typename T, int DIM>
+__device__ __forceinline__ void fetch(Staged<T, DIM>& r, const T* head, uint64_t ld, uint32_t row0, uint32_t len, uint32_t dim)
+{
+    typedef typename Vec8<T>::type V;
+    typedef V __attribute__((aligned(sizeof(T)))) VU;
+#pragma unroll
+    for (int i = 0; i < Tile<DIM>::kPerThread; ++i) {
+        const uint32_t id = threadIdx.x + i * kBlock, row = id / Tile<DIM>::kPieces, col = id % Tile<DIM>::kPieces * 8;
+        const uint32_t at = row0 + row < len ? row0 + row : len - 1;
+        const bool in = col < dim;
+        const V v = *reinterpret_cast<const VU*>(head + at * ld + (in ? col : 0));
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            r.v[i][j] = in ? v[j] : T(0.0f);
+    }
+}
+
+template <typename T, int DIM>
+__device__ __forceinline__ void put(T* tile, const Staged<T, DIM>& r)
+{
+#pragma unroll
+    for (int i = 0; i < Tile<DIM>::kPerThread; ++i) {
+        const uint32_t id = threadIdx.x + i * kBlock;
+        *reinterpret_cast<typename Vec8<T>::type*>(tile + Tile<DIM>::place(id / Tile<DIM>::kPieces, id % Tile<DIM>::kPieces)) = r.v[i];
+    }
+}
+
+// The operand that stays: a wave's 32 rows as columns of B.
+template <typename T, int DIM>
+struct Operand {
+    typename Vec8<T>::type v[DIM / 16];
+};
+
+template <typename T, int DIM>
+__device__ __forceinline__ void load_operand(Operand<T, DIM>& o, const T* head, uint64_t ld, uint32_t row, uint32_t dim)
+{
+    typedef typename Vec8<T>::type V;
+    typedef V __attribute__((aligned(sizeof(T)))) VU;
+    const uint32_t h = (threadIdx.x & 63) / 32;
+#pragma unroll
+    for (int k = 0; k < DIM / 16; ++k) {
+        const uint32_t col = 16 * k + 8 * h;
+        const bool in = col < dim;
+        const V v = *reinterpret_cast<const VU*>(head + row * ld + (in ? col : 0));
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            o.v[k][j] = in ? v[j] : T(0.0f);
+    }
+}
+
+// C = (rows 32 sub .. of the tile) x operand.
+template <typename T, int DIM>
+__device__ __forceinline__ f32x16 rows_times(const T* tile, int sub, const Operand<T, DIM>& b)
+{
+    const uint32_t lane = threadIdx.x & 63, row = 32 * sub + lane % 32, h = lane / 32;
+    f32x16 c = {};
+#pragma unroll
+    for (int k = 0; k < DIM / 16; ++k)
+        c = Vec8<T>::mfma(*reinterpret_cast<const typename Vec8<T>::type*>(tile + Tile<DIM>::place(row, 2 * k + h)), b.v[k], c);
+    return c;
+}
+
+template <typename T>
+__device__ __forceinline__ typename Vec8<T>::type column_pair(const T* a, const T* b)
+{
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4* P;
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(a)), y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(b));
+    return __builtin_bit_cast(typename Vec8<T>::type, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// acc[n] += (rows 16 step .. 16 step + 15 of the tile, columns 32 n .. 32 n + 31)^T x p, where p holds
+// 16 rows in the order that a score's registers give.
+template <typename T, int DIM>
+__device__ __forceinline__ void columns_times(f32x16 (&acc)[DIM / 32], const T* tile, int step, typename Vec8<T>::type p)
+{
+    const uint32_t lane = threadIdx.x & 63, i = lane % 16, g = lane / 16 % 2, h = lane / 32;
+    const uint32_t row = 16 * step + 4 * h + i / 4;
+#pragma unroll
+    for (int n = 0; n < DIM / 32; ++n) {
+        const uint32_t piece = 4 * n + 2 * g + i % 4 / 2, low = i % 2 * 4;
+        acc[n] = Vec8<T>::mfma(column_pair<T>(tile + Tile<DIM>::place(row, piece) + low, tile + Tile<DIM>::place(row + 8, piece) + low),
+                               p, acc[n]);
+    }
+}
+
+// Registers 8 half .. 8 half + 7, rounded to nearest even.
+template <typename T>
+__device__ __forceinline__ typename Vec8<T>::type rounded(f32x16 c, int half)
+{
+    layer::f32x8 v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = c[8 * half + j];
+    return __builtin_convertvector(v, typename Vec8<T>::type);
+}
+
+// x of the lane and of the one 32 lanes away, which hold the two halves of a column.
+struct Pair {
+    float low, high;
+};
+__device__ __forceinline__ Pair both_halves(float x)
+{
+    const uint32_t bits = __builtin_bit_cast(uint32_t, x);
+    const auto r = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+    const uint32_t low = r[0], high = r[1];        // a bit cast of an element itself would take the first
+    return Pair{__builtin_bit_cast(float, low), __builtin_bit_cast(float, high)};
+}
+__device__ __forceinline__ float halves_sum(float x)
+{
+    const Pair p = both_halves(x);
+    return p.low + p.high;
+}
+__device__ __forceinline__ float halves_max(float x)
+{
+    const Pair p = both_halves(x);
+    return fmaxf(p.low, p.high);
+}
+
+// Stores acc^T * factor (column c of acc is row `row` of the output) with
+// 16-byte stores: the halves of a wave trade 4-element parts first.
+template <typename T, int DIM>
+__device__ __forceinline__ void store_columns(T* head, uint64_t ld, uint32_t row, bool live, uint32_t dim, const f32x16 (&acc)[DIM / 32],
+                                              float factor)
+{
+    typedef typename Vec8<T>::type V;
+    typedef V __attribute__((aligned(sizeof(T)))) VU;
+    const uint32_t h = (threadIdx.x & 63) / 32;
+#pragma unroll
+    for (int n = 0; n < DIM / 32; ++n)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            layer::f32x8 v;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = acc[n][8 * half + j] * factor;
+            struct Words {
+                uint32_t d[4];
+            };
+            const Words w = __builtin_bit_cast(Words, __builtin_convertvector(v, V));
+            Words out;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const auto r = __builtin_amdgcn_permlane32_swap(w.d[j], w.d[j + 2], false, false);
+                out.d[j] = r[0];
+                out.d[j + 2] = r[1];
+            }
+            const uint32_t col = 32 * n + 16 * half + 8 * h;
+            if (live && col < dim)
+                *reinterpret_cast<VU*>(head + row * ld + col) = __builtin_bit_cast(V, out);
+        }
+}
+
+// ---- the bias -------------------------------------------------------------------------
+// bucket(d): the last b with starts[b] <= d.
+__device__ __forceinline__ uint32_t bucket_of(const uint32_t* starts, uint32_t count, uint32_t d)
+{
+    uint32_t b = 0;
+#pragma unroll
+    for (uint32_t step = ZERO_MAX_BUCKETS / 2; step; step >>= 1)
+        if (b + step < count && starts[b + step] <= d)
+            b += step;
+    return b;
+}
+
+template <typename T>
+__device__ __forceinline__ float bias_value(const Buckets& b, uint32_t head, uint32_t i)
+{
+    const uint64_t at = uint64_t(head) * b.count + i;
+    return b.f32 ? static_cast<const float*>(b.table)[at] : float(static_cast<const T*>(b.table)[at]);
+}
+
+// The bias in LDS: the head's table times log2(e), the buckets' borders, and of
+// the present tile one value for each distance between its rows and keys.
+struct BiasLds {
+    float value[ZERO_MAX_BUCKETS];
+    uint32_t starts[ZERO_MAX_BUCKETS];
+    float line[2][kOwn + kTile];                   // line[x]: the distance far - x
+};
+
+// ---- host side --------------------------------------------------------------------------
+constexpr uint64_t kMaxTokens = uint64_t(1) << 30;
+constexpr uint32_t kMaxHeads = 1u << 16;
+constexpr uint64_t kMaxPieces = uint64_t(1) << 31;
+
+inline int check_heads(const void* p, uint64_t ld, uint64_t hs, uint64_t tokens, uint32_t heads, uint32_t dim, int dtype)
+{
+    if (!p)
+        return tokens ? ZERO_EINVAL : ZERO_OK;
+    if (!is_aligned(p, layer::dtype_size(dtype)))
+        return ZERO_EALIGN;
+    if ((tokens > 1 && ld < dim) || (heads > 1 && hs < dim))
+        return ZERO_ERANGE;
+    if (ld > (uint64_t(1) << 50) || hs > (uint64_t(1) << 50) ||
+        (unsigned __int128)tokens * ld + (unsigned __int128)heads * hs > (uint64_t(1) << 56))
+        return ZERO_ERANGE;
+    return ZERO_OK;
+}
+
+// Checks what the calls share and fills the kernels' arguments.
+int make_shape(const zero_attention_t* a, uint64_t tokens, const int32_t* dev_offsets, uint64_t sequences, int dtype,
+               const void* bias, int vec_dtype, Shape* s, Buckets* b);
+
+}  // namespace attention
+}  // namespace zero

@@ -1,0 +1,558 @@
+// attention_bwd.hip -- the gradients of attention.hip's forward pass at the
+// queries, keys, values and the bias table.
+//
+//   p_ij = exp(s_ij - lse_i),  delta_i = do_i.o_i,  ds_ij = p_ij (do_i.v_j - delta_i)
+//   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
+//   dbias[h][b] = sum of ds over the pairs whose distance is in bucket b
+//
+// Two passes over the visible pairs, so that every sum is one workgroup's own:
+// one whose waves own queries (dq, the bias, and delta for the other), one
+// whose waves own keys (dk and dv).  That is 7 products a pair of tiles where
+// one pass would take 5, and no atomic sums, whose order would change the
+// results, nor a binary32 copy of dq.
+#include <type_traits>
+
+#include "attention.hpp"
+
+namespace zero {
+namespace attention {
+namespace {
+
+// binary16 has few exponents below a gradient's: ds is formed in units of
+// 2^-k where 2^k is about |do_i| (its 2-norm, a power of two, so the products
+// are exact), and p of the dv product in units of 2^-6.  bfloat16 needs neither.
+template <typename T>
+constexpr bool kUnits = __is_same(T, _Float16);
+constexpr float kWeightUnits = 64.0f, kWeightShift = 6.0f;
+
+template <typename T>
+struct BwdArgs {
+    Heads<T> dq, dk, dv;
+    Heads<const T> dout, o, q, k, v;
+    const float* lse;
+    float* delta;                                  // heads x tokens
+    float* unit;                                   // heads x tokens: 2^k's inverse (binary16)
+    float* partials;                               // heads x slots x buckets
+    Shape s;
+    Buckets b;
+    uint32_t slots;
+};
+
+struct BinsLds {
+    float bins[kWaves][ZERO_MAX_BUCKETS];
+};
+
+__device__ __forceinline__ float lane_value(float v, uint32_t from)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(int(from * 4), __builtin_bit_cast(int, v)));
+}
+
+// bins[bucket] += the sums of ds along the distances of a 32 x 32 product
+// whose rows are keys: ds[r] of lane (c, h) is the pair at distance base + c - row_of(r, h).
+__device__ __forceinline__ void add_diagonals(float* bins, const BiasLds& bias, uint32_t count, int base, const float (&ds)[16])
+{
+    const uint32_t lane = threadIdx.x & 63;        // takes the distance base + lane - 31
+    float sum = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int c = int(lane) - 31 + row_of(r, half);
+            const float v = lane_value(ds[r], (c & 31) + 32 * half);
+            sum += c >= 0 && c < 32 ? v : 0.0f;
+        }
+    const int d = base + int(lane) - 31;
+    const uint32_t bucket = bucket_of(bias.starts, count, d > 0 ? d : 0);
+    // equal buckets are neighbours: their sum ends up in the last lane of each
+#pragma unroll
+    for (uint32_t step = 1; step < 64; step <<= 1) {
+        const uint32_t from = lane >= step ? lane - step : lane;
+        const float v = lane_value(sum, from);
+        const uint32_t b = __builtin_amdgcn_ds_bpermute(int(from * 4), int(bucket));
+        sum += lane >= step && b == bucket ? v : 0.0f;
+    }
+    const uint32_t after = __builtin_amdgcn_ds_bpermute(int((lane + 1) % 64 * 4), int(bucket));
+    if (lane == 63 || after != bucket)
+        bins[bucket] += sum;
+}
+
+template <typename T, int DIM, bool BIAS>
+__global__ __launch_bounds__(kBlock) void attention_dq_kernel(BwdArgs<T> a)
+{
+    typedef Tile<DIM> L;
+    __shared__ alignas(16) T keys[2][L::kElems];
+    __shared__ alignas(16) T values[2][L::kElems];
+    __shared__ typename std::conditional<BIAS, BiasLds, int>::type bias;
+    __shared__ typename std::conditional<BIAS, BinsLds, int>::type sums;
+
+    const Shape& s = a.s;
+    const uint32_t work = die_local(blockIdx.x, gridDim.x);
+    if (work >= a.slots * s.heads)
+        return;
+    const uint32_t head = work / a.slots, slot = a.slots - 1 - (work - head * a.slots);
+    Piece at;
+    if (!find_piece(s, slot, &at)) {
+        if (BIAS && a.partials && threadIdx.x < a.b.count)
+            a.partials[(uint64_t(head) * a.slots + slot) * a.b.count + threadIdx.x] = 0.0f;
+        return;
+    }
+    const uint32_t lane = threadIdx.x & 63, c = lane % 32, h = lane / 32;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const uint32_t first = at.first + 32 * wave, mine = first + c;
+    const uint32_t row = mine < at.len ? mine : at.len - 1;
+    const bool live = mine < at.len;
+    const T* kp = a.k.p + uint64_t(at.start) * a.k.ld + uint64_t(head / s.group) * a.k.hs;
+    const T* vp = a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(head / s.group) * a.v.hs;
+
+    const KeyTiles tiles(s, at.first, kOwn, at.len);
+    Staged<T, DIM> nk, nv;
+    uint32_t t = tiles.begin();
+    fetch<T, DIM>(nk, kp, a.k.ld, t * kTile, at.len, s.dim);
+    fetch<T, DIM>(nv, vp, a.v.ld, t * kTile, at.len, s.dim);
+    Operand<T, DIM> q, dout;
+    load_operand<T, DIM>(q, a.q.p + uint64_t(at.start) * a.q.ld + uint64_t(head) * a.q.hs, a.q.ld, row, s.dim);
+    load_operand<T, DIM>(dout, a.dout.p + uint64_t(at.start) * a.dout.ld + uint64_t(head) * a.dout.hs, a.dout.ld, row, s.dim);
+    float delta = 0.0f, norm = 0.0f;
+    {
+        Operand<T, DIM> o;
+        load_operand<T, DIM>(o, a.o.p + uint64_t(at.start) * a.o.ld + uint64_t(head) * a.o.hs, a.o.ld, row, s.dim);
+#pragma unroll
+        for (int k = 0; k < DIM / 16; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                delta = __builtin_fmaf(float(dout.v[k][j]), float(o.v[k][j]), delta);
+                norm = __builtin_fmaf(float(dout.v[k][j]), float(dout.v[k][j]), norm);
+            }
+        delta = halves_sum(delta);
+        norm = halves_sum(norm);
+    }
+    const uint64_t stat = uint64_t(head) * s.tokens + at.start + row;
+    const float lse = a.lse[stat] * kLog2e;
+    float unit = 1.0f;
+    if (kUnits<T>) {
+        // a row of zeros gets a large unit, so that it does not set that of the rows beside it
+        unit = norm > 0.0f ? __builtin_ldexpf(1.0f, -((__builtin_amdgcn_frexp_expf(norm) + 1) >> 1)) : 0x1p60f;
+        if (live && h == 0)
+            a.unit[stat] = unit;
+    }
+    if (live && h == 0)
+        a.delta[stat] = delta;
+    delta *= unit;
+
+    if constexpr (BIAS) {
+        if (threadIdx.x < a.b.count) {
+            bias.value[threadIdx.x] = bias_value<T>(a.b, head, threadIdx.x) * kLog2e;
+            bias.starts[threadIdx.x] = a.b.starts[threadIdx.x];
+        }
+        for (uint32_t i = threadIdx.x; i < kWaves * ZERO_MAX_BUCKETS; i += kBlock)
+            sums.bins[i / ZERO_MAX_BUCKETS][i % ZERO_MAX_BUCKETS] = 0.0f;
+        __syncthreads();
+    }
+    auto draw_line = [&](uint32_t tile, int buf) {
+        if constexpr (BIAS)
+            if (threadIdx.x < kOwn + kTile - 1) {
+                const int d = int(at.first + kOwn - 1) - int(tile * kTile) - int(threadIdx.x);
+                bias.line[buf][threadIdx.x] = bias.value[bucket_of(bias.starts, a.b.count, d > 0 ? d : 0)];
+            }
+    };
+    float even = 0.0f;                             // ds of tiles whose distances share a bucket
+    uint32_t even_bucket = 0;
+    auto settle_even = [&] {
+        if constexpr (BIAS) {
+            const float v = layer::lanes_sum<64>(even);
+            if (lane == 0)
+                sums.bins[wave][even_bucket] += v;
+            even = 0.0f;
+        }
+    };
+
+    f32x16 acc[DIM / 32] = {};
+    put<T, DIM>(keys[0], nk);
+    put<T, DIM>(values[0], nv);
+    draw_line(t, 0);
+    int buf = 0;
+    while (true) {
+        const uint32_t next = tiles.next(t);
+        const bool more = next < tiles.end;
+        __syncthreads();
+        if (more) {
+            fetch<T, DIM>(nk, kp, a.k.ld, next * kTile, at.len, s.dim);
+            fetch<T, DIM>(nv, vp, a.v.ld, next * kTile, at.len, s.dim);
+        }
+        const uint32_t j0 = t * kTile;
+        const Seen see = seen(s, first, 32, j0, kTile);
+        if (see != kNone) {
+            bool one_bucket = false;
+            if constexpr (BIAS)
+                if (a.partials) {
+                    const uint32_t near = first > j0 + kTile - 1 ? first - (j0 + kTile - 1) : 0, far = first + 31 - j0;
+                    const uint32_t b0 = __builtin_amdgcn_readfirstlane(bucket_of(bias.starts, a.b.count, near));
+                    one_bucket = b0 == uint32_t(__builtin_amdgcn_readfirstlane(bucket_of(bias.starts, a.b.count, far)));
+                    if (one_bucket && b0 != even_bucket) {
+                        settle_even();
+                        even_bucket = b0;
+                    }
+                }
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+                const f32x16 x = rows_times<T, DIM>(keys[buf], sub, q);
+                const f32x16 dp = rows_times<T, DIM>(values[buf], sub, dout);
+                f32x16 ds;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const uint32_t j = 32 * sub + row_of(r, h);
+                    float v = __builtin_fmaf(x[r], s.scale2, -lse);
+                    if constexpr (BIAS)
+                        v += bias.line[buf][kOwn - 1 - 32 * wave - c + j];
+                    v = __builtin_amdgcn_exp2f(v) * __builtin_fmaf(dp[r], unit, -delta);
+                    ds[r] = see == kAll || visible(s, mine, j0 + j) ? v : 0.0f;
+                }
+                if constexpr (BIAS)
+                    if (a.partials) {
+                        const float back = live ? 1.0f / unit : 0.0f;        // a power of two: exact
+                        if (one_bucket) {
+                            float v = 0.0f;
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                v += ds[r];
+                            even += live ? v * back : 0.0f;
+                        } else {
+                            float w[16];
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                w[r] = live ? ds[r] * back : 0.0f;
+                            add_diagonals(sums.bins[wave], bias, a.b.count, int(first) - int(j0) - 32 * sub, w);
+                        }
+                    }
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    columns_times<T, DIM>(acc, keys[buf], 2 * sub + half, rounded<T>(ds, half));
+            }
+        }
+        if (!more)
+            break;
+        t = next;
+        buf ^= 1;
+        put<T, DIM>(keys[buf], nk);
+        put<T, DIM>(values[buf], nv);
+        draw_line(t, buf);
+    }
+    store_columns<T, DIM>(a.dq.p + uint64_t(at.start) * a.dq.ld + uint64_t(head) * a.dq.hs, a.dq.ld, mine, live, s.dim, acc,
+                          s.scale / unit);
+    if constexpr (BIAS)
+        if (a.partials) {
+            settle_even();
+            __syncthreads();
+            if (threadIdx.x < a.b.count) {
+                float v = 0.0f;
+                for (int w = 0; w < kWaves; ++w)
+                    v += sums.bins[w][threadIdx.x];
+                a.partials[(uint64_t(head) * a.slots + slot) * a.b.count + threadIdx.x] = v;
+            }
+        }
+}
+
+struct RowStats {
+    float lse[kTile], delta[kTile], unit[kTile];
+};
+
+template <typename T, int DIM, bool BIAS>
+__global__ __launch_bounds__(kBlock) void attention_dkv_kernel(BwdArgs<T> a)
+{
+    typedef Tile<DIM> L;
+    __shared__ alignas(16) T queries[2][L::kElems];
+    __shared__ alignas(16) T douts[2][L::kElems];
+    __shared__ alignas(16) RowStats stats[2];
+    __shared__ typename std::conditional<BIAS, BiasLds, int>::type bias;
+
+    const Shape& s = a.s;
+    const uint32_t work = die_local(blockIdx.x, gridDim.x), kv_heads = s.heads / s.group;
+    if (work >= a.slots * kv_heads)
+        return;
+    const uint32_t kv = work / a.slots;
+    Piece at;
+    if (!find_piece(s, work - kv * a.slots, &at))  // the first keys have the most queries
+        return;
+    const uint32_t lane = threadIdx.x & 63, c = lane % 32, h = lane / 32;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const uint32_t first = at.first + 32 * wave, mine = first + c;
+    const uint32_t row = mine < at.len ? mine : at.len - 1;
+    Operand<T, DIM> k, v;
+    load_operand<T, DIM>(k, a.k.p + uint64_t(at.start) * a.k.ld + uint64_t(kv) * a.k.hs, a.k.ld, row, s.dim);
+    load_operand<T, DIM>(v, a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(kv) * a.v.hs, a.v.ld, row, s.dim);
+
+    // the tiles of queries that see one of the keys, for each query head in turn
+    uint32_t last = at.len;                        // queries below this
+    if (at.first >= s.sinks && s.window != 0xffffffffu && at.len - at.first > kOwn - 1 && at.len - at.first - (kOwn - 1) > s.window)
+        last = at.first + (kOwn - 1) + s.window;
+    const uint32_t begin = at.first / kTile, end = (last + kTile - 1) / kTile;
+    uint32_t head = kv * s.group, t = begin;
+    const uint32_t head_end = head + s.group;
+
+    Staged<T, DIM> nq, ndo;
+    float nstat[3] = {};
+    auto ask = [&](uint32_t hd, uint32_t tile) {
+        fetch<T, DIM>(nq, a.q.p + uint64_t(at.start) * a.q.ld + uint64_t(hd) * a.q.hs, a.q.ld, tile * kTile, at.len, s.dim);
+        fetch<T, DIM>(ndo, a.dout.p + uint64_t(at.start) * a.dout.ld + uint64_t(hd) * a.dout.hs, a.dout.ld, tile * kTile, at.len, s.dim);
+        if (threadIdx.x < kTile) {
+            const uint32_t i = tile * kTile + threadIdx.x;
+            const uint64_t stat = uint64_t(hd) * s.tokens + at.start + (i < at.len ? i : at.len - 1);
+            nstat[0] = a.lse[stat];
+            nstat[1] = a.delta[stat];
+            if (kUnits<T>)
+                nstat[2] = a.unit[stat];
+        }
+    };
+    auto load_bias = [&](uint32_t hd) {
+        if constexpr (BIAS)
+            if (threadIdx.x < a.b.count)
+                bias.value[threadIdx.x] = bias_value<T>(a.b, hd, threadIdx.x) * kLog2e;
+    };
+    auto place = [&](int buf, uint32_t tile) {
+        put<T, DIM>(queries[buf], nq);
+        put<T, DIM>(douts[buf], ndo);
+        if (threadIdx.x < kTile) {
+            stats[buf].lse[threadIdx.x] = nstat[0] * kLog2e - (kUnits<T> ? kWeightShift : 0.0f);
+            stats[buf].delta[threadIdx.x] = nstat[1];
+            if (kUnits<T>)
+                stats[buf].unit[threadIdx.x] = nstat[2];
+        }
+        if constexpr (BIAS)
+            if (threadIdx.x < kOwn + kTile - 1) {
+                const int d = int(tile * kTile) - int(at.first + kOwn - 1) + int(threadIdx.x);
+                bias.line[buf][threadIdx.x] = bias.value[bucket_of(bias.starts, a.b.count, d > 0 ? d : 0)];
+            }
+    };
+    if constexpr (BIAS) {
+        if (threadIdx.x < a.b.count)
+            bias.starts[threadIdx.x] = a.b.starts[threadIdx.x];
+        load_bias(head);
+        __syncthreads();
+    }
+    ask(head, t);
+    place(0, t);
+    f32x16 dk[DIM / 32] = {}, dv[DIM / 32] = {};
+    float unit = 0x1p60f;                          // of dk's sums
+    int buf = 0;
+    while (true) {
+        uint32_t next = t + 1, next_head = head;
+        if (next >= end) {
+            next = begin;
+            ++next_head;
+        }
+        const bool more = next_head < head_end;
+        __syncthreads();
+        if (more)
+            ask(next_head, next);
+        const uint32_t i0 = t * kTile;
+        const Seen see = seen(s, i0, kTile, first, 32);
+        if (see != kNone) {
+            const bool whole = see == kAll && i0 + kTile <= at.len;
+            if (kUnits<T>) {
+                float least = stats[buf].unit[lane];               // kTile lanes
+#pragma unroll
+                for (int step = 32; step; step >>= 1)
+                    least = fminf(least, __shfl_xor(least, step));
+                if (least < unit) {                // the same for every lane
+                    const float by = least / unit;
+                    unit = least;
+#pragma unroll
+                    for (int n = 0; n < DIM / 32; ++n)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            dk[n][r] *= by;
+                }
+            }
+            const float ds_unit = kUnits<T> ? unit * (1.0f / kWeightUnits) : 1.0f;
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+                const f32x16 x = rows_times<T, DIM>(queries[buf], sub, k);
+                const f32x16 dp = rows_times<T, DIM>(douts[buf], sub, v);
+                f32x16 p, ds;
+#pragma unroll
+                for (int quad = 0; quad < 4; ++quad) {
+                    const uint32_t i = 32 * sub + 8 * quad + 4 * h;
+                    const f32x4 lse = *reinterpret_cast<const f32x4*>(&stats[buf].lse[i]);
+                    const f32x4 delta = *reinterpret_cast<const f32x4*>(&stats[buf].delta[i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = 4 * quad + e;
+                        float y = __builtin_fmaf(x[r], s.scale2, -lse[e]);
+                        if constexpr (BIAS)
+                            y += bias.line[buf][kOwn - 1 - 32 * wave - c + i + e];
+                        y = __builtin_amdgcn_exp2f(y);
+                        y = whole || (i0 + i + e < at.len && visible(s, i0 + i + e, mine)) ? y : 0.0f;
+                        p[r] = y;
+                        float d = dp[r] - delta[e];
+                        if (kUnits<T>)
+                            d *= ds_unit;
+                        ds[r] = y == 0.0f ? 0.0f : y * d;
+                    }
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    columns_times<T, DIM>(dv, douts[buf], 2 * sub + half, rounded<T>(p, half));
+                    columns_times<T, DIM>(dk, queries[buf], 2 * sub + half, rounded<T>(ds, half));
+                }
+            }
+        }
+        if (!more)
+            break;
+        if constexpr (BIAS)
+            if (next_head != head) {
+                __syncthreads();                   // the line before is read no more
+                load_bias(next_head);
+                __syncthreads();
+            }
+        head = next_head;
+        t = next;
+        buf ^= 1;
+        place(buf, t);
+    }
+    const bool live = mine < at.len;
+    store_columns<T, DIM>(a.dk.p + uint64_t(at.start) * a.dk.ld + uint64_t(kv) * a.dk.hs, a.dk.ld, mine, live, s.dim, dk,
+                          kUnits<T> ? s.scale / unit : s.scale);
+    store_columns<T, DIM>(a.dv.p + uint64_t(at.start) * a.dv.ld + uint64_t(kv) * a.dv.hs, a.dv.ld, mine, live, s.dim, dv,
+                          kUnits<T> ? 1.0f / kWeightUnits : 1.0f);
+}
+
+// A head's bias gradient: its partials added up in their order.
+template <typename T>
+__global__ __launch_bounds__(kBlock) void fold_bias_kernel(void* dst, bool f32, bool accumulate, const float* partials, uint32_t slots,
+                                                           uint32_t count)
+{
+    __shared__ float part[kWaves][ZERO_MAX_BUCKETS];
+    const uint32_t i = threadIdx.x % 64, w = threadIdx.x / 64;
+    float v = 0.0f;
+    if (i < count)
+        for (uint32_t slot = w; slot < slots; slot += kWaves)
+            v += partials[(uint64_t(blockIdx.x) * slots + slot) * count + i];
+    part[w][i] = v;
+    __syncthreads();
+    if (w || i >= count)
+        return;
+    v = (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]);
+    const uint64_t to = uint64_t(blockIdx.x) * count + i;
+    if (f32) {
+        float* d = static_cast<float*>(dst) + to;
+        *d = accumulate ? *d + v : v;
+    } else {
+        T* d = static_cast<T*>(dst) + to;
+        *d = T(accumulate ? float(*d) + v : v);
+    }
+}
+
+// ---- host side --------------------------------------------------------------------------
+// The workspace: delta and (binary16) the units, a value each for every row,
+// then the bias' partials.  Its size takes the larger form of either choice.
+uint64_t rows_bytes(const zero_attention_t& p, uint64_t tokens) { return (uint64_t(p.heads) * tokens * 4 + 255) / 256 * 256; }
+
+uint64_t workspace_need(const zero_attention_t& p, uint64_t tokens, uint64_t sequences)
+{
+    const uint64_t ragged = slots_of(uint32_t(tokens), uint32_t(sequences), true);
+    return 2 * rows_bytes(p, tokens) + uint64_t(p.heads) * ragged * p.buckets * 4;
+}
+
+template <typename T, int DIM, bool BIAS>
+int launch(const BwdArgs<T>& a, hipStream_t stream)
+{
+    auto blocks = [&](uint32_t heads) { return dim3(uint32_t((uint64_t(a.slots) * heads + 7) / 8 * 8)); };
+    hipLaunchKernelGGL((attention_dq_kernel<T, DIM, BIAS>), blocks(a.s.heads), dim3(kBlock), 0, stream, a);
+    const int rc = launch_status();
+    if (rc)
+        return rc;
+    hipLaunchKernelGGL((attention_dkv_kernel<T, DIM, BIAS>), blocks(a.s.heads / a.s.group), dim3(kBlock), 0, stream, a);
+    return launch_status();
+}
+
+template <typename T>
+int run(Heads<void> dq, Heads<void> dk, Heads<void> dv, Heads<const void> dout, Heads<const void> o, Heads<const void> q, Heads<const void> k,
+        Heads<const void> v, const float* lse, const Shape& s, const Buckets& b, void* dbias, int grad_dtype, bool accumulate,
+        char* workspace, uint64_t rows, hipStream_t stream)
+{
+    auto out = [](Heads<void> x) { return Heads<T>{static_cast<T*>(x.p), x.ld, x.hs}; };
+    auto in = [](Heads<const void> x) { return Heads<const T>{static_cast<const T*>(x.p), x.ld, x.hs}; };
+    BwdArgs<T> a{out(dq), out(dk), out(dv), in(dout), in(o), in(q), in(k), in(v), lse, reinterpret_cast<float*>(workspace),
+                 reinterpret_cast<float*>(workspace + rows), dbias ? reinterpret_cast<float*>(workspace + 2 * rows) : nullptr, s, b, 0};
+    a.slots = uint32_t(slots_of(s.tokens, s.sequences, s.offsets != nullptr));
+    int rc;
+    if (s.dim <= 64)
+        rc = b.table ? launch<T, 64, true>(a, stream) : launch<T, 64, false>(a, stream);
+    else
+        rc = b.table ? launch<T, 128, true>(a, stream) : launch<T, 128, false>(a, stream);
+    if (rc || !dbias)
+        return rc;
+    hipLaunchKernelGGL(fold_bias_kernel<T>, dim3(s.heads), dim3(kBlock), 0, stream, dbias, grad_dtype == ZERO_F32, accumulate, a.partials,
+                       a.slots, b.count);
+    return launch_status();
+}
+
+}  // namespace
+}  // namespace attention
+}  // namespace zero
+
+using namespace zero;
+using namespace zero::attention;
+
+extern "C" size_t zero_attention_workspace_bytes(const zero_attention_t* params, uint64_t tokens, uint64_t sequences)
+{
+    if (!params || !tokens || !sequences || tokens > kMaxTokens || sequences > kMaxTokens || params->heads > kMaxHeads ||
+        params->buckets > ZERO_MAX_BUCKETS)
+        return 0;
+    return size_t(workspace_need(*params, tokens, sequences));
+}
+
+extern "C" int zero_attention_bwd(void* dq, uint64_t ld_dq, uint64_t hs_dq, void* dk, uint64_t ld_dk, uint64_t hs_dk, void* dv,
+                                  uint64_t ld_dv, uint64_t hs_dv, void* dbias, int grad_dtype, int accumulate, const void* dout,
+                                  uint64_t ld_dout, uint64_t hs_dout, const void* o, uint64_t ld_o, uint64_t hs_o, const float* lse,
+                                  const void* q, uint64_t ld_q, uint64_t hs_q, const void* k, uint64_t ld_k, uint64_t hs_k, const void* v,
+                                  uint64_t ld_v, uint64_t hs_v, const void* bias, int vec_dtype, const zero_attention_t* params,
+                                  uint64_t tokens, const int32_t* dev_offsets, uint64_t sequences, int dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream)
+{
+    Shape s;
+    Buckets b;
+    int rc = make_shape(params, tokens, dev_offsets, sequences, dtype, bias, vec_dtype, &s, &b);
+    if (rc)
+        return rc;
+    const uint32_t hq = params->heads, hk = params->kv_heads, dim = params->dim;
+    rc = check_heads(dq, ld_dq, hs_dq, tokens, hq, dim, dtype);
+    if (!rc) rc = check_heads(dk, ld_dk, hs_dk, tokens, hk, dim, dtype);
+    if (!rc) rc = check_heads(dv, ld_dv, hs_dv, tokens, hk, dim, dtype);
+    if (!rc) rc = check_heads(dout, ld_dout, hs_dout, tokens, hq, dim, dtype);
+    if (!rc) rc = check_heads(o, ld_o, hs_o, tokens, hq, dim, dtype);
+    if (!rc) rc = check_heads(q, ld_q, hs_q, tokens, hq, dim, dtype);
+    if (!rc) rc = check_heads(k, ld_k, hs_k, tokens, hk, dim, dtype);
+    if (!rc) rc = check_heads(v, ld_v, hs_v, tokens, hk, dim, dtype);
+    if (!rc) rc = layer::check_vector(dbias, grad_dtype, dtype);
+    if (rc)
+        return rc;
+    if (dbias && !bias)
+        return ZERO_EINVAL;
+    if (tokens && (!lse || dq == dk || dq == dv || dk == dv))
+        return ZERO_EINVAL;
+    if (!is_aligned(lse, 4))
+        return ZERO_EALIGN;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (!tokens) {
+        if (!dbias || accumulate)
+            return ZERO_OK;
+        if (dtype == ZERO_F16)
+            hipLaunchKernelGGL(fold_bias_kernel<_Float16>, dim3(hq), dim3(kBlock), 0, st, dbias, grad_dtype == ZERO_F32, false, nullptr, 0,
+                               params->buckets);
+        else
+            hipLaunchKernelGGL(fold_bias_kernel<bf16>, dim3(hq), dim3(kBlock), 0, st, dbias, grad_dtype == ZERO_F32, false, nullptr, 0,
+                               params->buckets);
+        return launch_status();
+    }
+    if (!workspace)
+        return ZERO_EINVAL;
+    if (!is_aligned(workspace, 16))
+        return ZERO_EALIGN;
+    if (workspace_bytes < workspace_need(*params, tokens, sequences))
+        return ZERO_ERANGE;
+    const auto go = dtype == ZERO_F16 ? run<_Float16> : run<bf16>;
+    return go({dq, ld_dq, hs_dq}, {dk, ld_dk, hs_dk}, {dv, ld_dv, hs_dv}, {dout, ld_dout, hs_dout}, {o, ld_o, hs_o}, {q, ld_q, hs_q},
+              {k, ld_k, hs_k}, {v, ld_v, hs_v}, lse, s, b, dbias, grad_dtype, accumulate != 0, static_cast<char*>(workspace),
+              rows_bytes(*params, tokens), st);
+}

@@ -25,8 +25,8 @@ struct FwdArgs {
     uint32_t slots;
 };
 
-template <typename T, int DIM, bool BIAS>
-__global__ __launch_bounds__(kBlock) void attention_fwd_kernel(FwdArgs<T> a)
+template <typename T, int DIM, bool BIAS, bool DIRECT>
+__global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kernel(FwdArgs<T> a)
 {
     typedef Tile<DIM> L;
     __shared__ alignas(16) T keys[2][L::kElems];
@@ -49,10 +49,11 @@ __global__ __launch_bounds__(kBlock) void attention_fwd_kernel(FwdArgs<T> a)
     const T* vp = a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(head / s.group) * a.v.hs;
 
     const KeyTiles tiles(s, at.first, kOwn, at.len);
-    Staged<T, DIM> nk, nv;
+    const Places<DIM> places;
+    Carrier<T, DIM, DIRECT> nk, nv;
     uint32_t t = tiles.begin();
-    fetch<T, DIM>(nk, kp, a.k.ld, t * kTile, at.len, s.dim);
-    fetch<T, DIM>(nv, vp, a.v.ld, t * kTile, at.len, s.dim);
+    nk.fetch(keys[0], kp, a.k.ld, t * kTile, at.len, s.dim);
+    nv.fetch(values[0], vp, a.v.ld, t * kTile, at.len, s.dim);
     Operand<T, DIM> q;
     load_operand<T, DIM>(q, a.q.p + uint64_t(at.start) * a.q.ld + uint64_t(head) * a.q.hs, a.q.ld, row, s.dim);
     if constexpr (BIAS) {
@@ -74,17 +75,17 @@ __global__ __launch_bounds__(kBlock) void attention_fwd_kernel(FwdArgs<T> a)
 
     f32x16 acc[DIM / 32] = {};
     float m = -INFINITY, sum = 0.0f;               // in units of log2; the sum over this half of the keys
-    put<T, DIM>(keys[0], nk);
-    put<T, DIM>(values[0], nv);
+    nk.put(keys[0]);
+    nv.put(values[0]);
     draw_line(t, 0);
     int buf = 0;
     while (true) {
         const uint32_t next = tiles.next(t);
         const bool more = next < tiles.end;
-        __syncthreads();
+        tiles_there<DIRECT>();
         if (more) {
-            fetch<T, DIM>(nk, kp, a.k.ld, next * kTile, at.len, s.dim);
-            fetch<T, DIM>(nv, vp, a.v.ld, next * kTile, at.len, s.dim);
+            nk.fetch(keys[buf ^ 1], kp, a.k.ld, next * kTile, at.len, s.dim);
+            nv.fetch(values[buf ^ 1], vp, a.v.ld, next * kTile, at.len, s.dim);
         }
         const uint32_t j0 = t * kTile;
         const Seen see = seen(s, first, 32, j0, kTile);
@@ -92,52 +93,62 @@ __global__ __launch_bounds__(kBlock) void attention_fwd_kernel(FwdArgs<T> a)
             f32x16 x[2];
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub)
-                x[sub] = rows_times<T, DIM>(keys[buf], sub, q);
+                x[sub] = rows_times<T, DIM>(keys[buf], places, sub, q);
+            if constexpr (BIAS)
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub)
+                for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const uint32_t j = 32 * sub + row_of(r, h);
-                    float v = x[sub][r] * s.scale2;
-                    if constexpr (BIAS)
-                        v += bias.line[buf][kOwn - 1 - 32 * wave - c + j];
-                    x[sub][r] = see == kAll || visible(s, mine, j0 + j) ? v : -INFINITY;
-                }
-            float top = m;
+                    for (int r = 0; r < 16; ++r)
+                        x[sub][r] = __builtin_fmaf(x[sub][r], s.scale2, bias.line[buf][kOwn - 1 - 32 * wave - c + 32 * sub + row_of(r, h)]);
+            if (see == kSome) {
+                const Limits limits(s, mine, j0 + 4 * h);
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        x[sub][r] = limits.sees(32 * sub + row_of(r, 0)) ? x[sub][r] : -INFINITY;
+            }
+            float top = x[0][0];
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
                     top = fmaxf(top, x[sub][r]);
             top = halves_max(top);
-            const float base = top == -INFINITY ? 0.0f : top;
-            const float fall = __builtin_amdgcn_exp2f(m - base);
-            m = top;
-            sum *= fall;
+            if constexpr (!BIAS)
+                top *= s.scale2;
+            // the sums go by the maximum so far until it has been passed by a factor of 2^8: they have the room, and most tiles
+            // need not touch them
+            if (__any(top > m + 8.0f)) {
+                const float higher = fmaxf(top, m), fall = higher == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - higher);
+                m = higher;
+                sum *= fall;
 #pragma unroll
-            for (int n = 0; n < DIM / 32; ++n)
+                for (int n = 0; n < DIM / 32; ++n)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    acc[n][r] *= fall;
+                    for (int r = 0; r < 16; ++r)
+                        acc[n][r] *= fall;
+            }
+            const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    x[sub][r] = __builtin_amdgcn_exp2f(x[sub][r] - base);
+                    x[sub][r] = __builtin_amdgcn_exp2f(BIAS ? x[sub][r] - base : __builtin_fmaf(x[sub][r], s.scale2, -base));
                     sum += x[sub][r];
                 }
             // the weights are rounded to the element type, as the matrix instruction takes them: half a step of each, where the
             // binary32 sum they are divided by is of the unrounded ones
 #pragma unroll
             for (int step = 0; step < 4; ++step)
-                columns_times<T, DIM>(acc, values[buf], step, rounded<T>(x[step / 2], step % 2));
+                columns_times<T, DIM>(acc, values[buf], places, step, rounded<T>(x[step / 2], step % 2));
         }
         if (!more)
             break;
         t = next;
         buf ^= 1;
-        put<T, DIM>(keys[buf], nk);
-        put<T, DIM>(values[buf], nv);
+        nk.put(keys[buf]);
+        nv.put(values[buf]);
         draw_line(t, buf);
     }
     sum = halves_sum(sum);
@@ -147,14 +158,14 @@ __global__ __launch_bounds__(kBlock) void attention_fwd_kernel(FwdArgs<T> a)
         a.lse[uint64_t(head) * s.tokens + at.start + mine] = (m + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
-template <typename T, int DIM>
+template <typename T, int DIM, bool DIRECT>
 int launch(const FwdArgs<T>& a, hipStream_t stream)
 {
     const uint32_t blocks = uint32_t((uint64_t(a.slots) * a.s.heads + 7) / 8 * 8);
     if (a.b.table)
-        hipLaunchKernelGGL((attention_fwd_kernel<T, DIM, true>), dim3(blocks), dim3(kBlock), 0, stream, a);
+        hipLaunchKernelGGL((attention_fwd_kernel<T, DIM, true, DIRECT>), dim3(blocks), dim3(kBlock), 0, stream, a);
     else
-        hipLaunchKernelGGL((attention_fwd_kernel<T, DIM, false>), dim3(blocks), dim3(kBlock), 0, stream, a);
+        hipLaunchKernelGGL((attention_fwd_kernel<T, DIM, false, DIRECT>), dim3(blocks), dim3(kBlock), 0, stream, a);
     return launch_status();
 }
 
@@ -213,7 +224,9 @@ int run_fwd(void* o, uint64_t ld_o, uint64_t hs_o, float* lse, const void* q, ui
 {
     const FwdArgs<T> a{{static_cast<T*>(o), ld_o, hs_o}, lse, {static_cast<const T*>(q), ld_q, hs_q}, {static_cast<const T*>(k), ld_k, hs_k},
                        {static_cast<const T*>(v), ld_v, hs_v}, s, b, uint32_t(slots_of(s.tokens, s.sequences, s.offsets != nullptr))};
-    return s.dim <= 64 ? launch<T, 64>(a, stream) : launch<T, 128>(a, stream);
+    if (direct_dim(s.dim) && direct(k, ld_k, hs_k) && direct(v, ld_v, hs_v))
+        return s.dim == 64 ? launch<T, 64, true>(a, stream) : launch<T, 128, true>(a, stream);
+    return s.dim <= 64 ? launch<T, 64, false>(a, stream) : launch<T, 128, false>(a, stream);
 }
 
 // A natural number of any size, for comparing powers.

@@ -152,10 +152,32 @@ __device__ __forceinline__ Seen seen(const Shape& s, uint32_t i, uint32_t nq, ui
     return kSome;
 }
 
-__device__ __forceinline__ bool visible(const Shape& s, uint32_t i, uint32_t j)
-{
-    return j <= i && (i - j < s.window || j < s.sinks);
-}
+// The same for single pairs, against one number a lane: of the keys j0 + j of a
+// tile, the lane's query sees those with j <= near, and j > far or j < first.
+struct Limits {
+    int near, far, first;
+
+    __device__ __forceinline__ Limits(const Shape& s, uint32_t i, uint32_t j0)
+    {
+        near = int(i) - int(j0);
+        far = s.window > i ? -1 - int(j0) : int(i - s.window) - int(j0);
+        first = s.sinks > j0 ? int(s.sinks - j0 < uint32_t(kTile) ? s.sinks - j0 : uint32_t(kTile)) : 0;
+    }
+    __device__ __forceinline__ bool sees(int j) const { return j <= near && (j > far || j < first); }
+};
+
+// The other way round: of the queries i0 + i of a tile, those that see the lane's key j have i >= near and i < end.
+struct QueryLimits {
+    int near, end;
+
+    __device__ __forceinline__ QueryLimits(const Shape& s, uint32_t j, uint32_t i0, uint32_t len)
+    {
+        near = int(j) - int(i0);
+        const uint32_t last = j < s.sinks || s.window > len || j + s.window > len ? len : j + s.window;
+        end = int(last) - int(i0);
+    }
+    __device__ __forceinline__ bool sees(int i) const { return i >= near && i < end; }
+};
 
 // The key tiles that some query of [i, i + nq) sees, in order: those of the
 // first tokens, then those of the window.
@@ -198,38 +220,82 @@ struct Tile {
     }
 };
 
-template <typename T, int DIM>
-struct Staged {                                    // a thread's pieces of a tile, on their way
-    typename Vec8<T>::type v[Tile<DIM>::kPerThread];
-};
-
+// A tile's way there.  DIRECT: straight into LDS, 16 bytes a lane to consecutive
+// addresses of a wave, so a lane takes the piece that belongs at its address;
+// it needs 16-byte aligned rows of DIM elements.  Else through registers.
 // Rows past the sequence's end repeat its last one (what they give is masked);
 // columns past `dim` are 0.
-template <typename T, int DIM>
-__device__ __forceinline__ void fetch(Staged<T, DIM>& r, const T* head, uint64_t ld, uint32_t row0, uint32_t len, uint32_t dim)
-{
-    typedef typename Vec8<T>::type V;
-    typedef V __attribute__((aligned(sizeof(T)))) VU;
-#pragma unroll
-    for (int i = 0; i < Tile<DIM>::kPerThread; ++i) {
-        const uint32_t id = threadIdx.x + i * kBlock, row = id / Tile<DIM>::kPieces, col = id % Tile<DIM>::kPieces * 8;
-        const uint32_t at = row0 + row < len ? row0 + row : len - 1;
-        const bool in = col < dim;
-        const V v = *reinterpret_cast<const VU*>(head + at * ld + (in ? col : 0));
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            r.v[i][j] = in ? v[j] : T(0.0f);
-    }
-}
+template <typename T, int DIM, bool DIRECT>
+class Carrier;
 
 template <typename T, int DIM>
-__device__ __forceinline__ void put(T* tile, const Staged<T, DIM>& r)
-{
+class Carrier<T, DIM, false> {
+    typedef typename Vec8<T>::type V;
+    typedef V __attribute__((aligned(sizeof(T)))) VU;
+    typedef Tile<DIM> L;
+    V v[L::kPerThread];
+
+public:
+    __device__ __forceinline__ void fetch(T*, const T* head, uint64_t ld, uint32_t row0, uint32_t len, uint32_t dim)
+    {
 #pragma unroll
-    for (int i = 0; i < Tile<DIM>::kPerThread; ++i) {
-        const uint32_t id = threadIdx.x + i * kBlock;
-        *reinterpret_cast<typename Vec8<T>::type*>(tile + Tile<DIM>::place(id / Tile<DIM>::kPieces, id % Tile<DIM>::kPieces)) = r.v[i];
+        for (int i = 0; i < L::kPerThread; ++i) {
+            const uint32_t id = threadIdx.x + i * kBlock, row = id / L::kPieces, col = id % L::kPieces * 8;
+            const uint32_t at = row0 + row < len ? row0 + row : len - 1;
+            const bool in = col < dim;
+            const V x = *reinterpret_cast<const VU*>(head + at * ld + (in ? col : 0));
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] = in ? x[j] : T(0.0f);
+        }
     }
+    __device__ __forceinline__ void put(T* tile)
+    {
+#pragma unroll
+        for (int i = 0; i < L::kPerThread; ++i) {
+            const uint32_t id = threadIdx.x + i * kBlock;
+            *reinterpret_cast<V*>(tile + L::place(id / L::kPieces, id % L::kPieces)) = v[i];
+        }
+    }
+};
+
+template <typename T, int DIM>
+class Carrier<T, DIM, true> {
+    typedef Tile<DIM> L;
+
+public:
+    __device__ __forceinline__ void fetch(T* tile, const T* head, uint64_t ld, uint32_t row0, uint32_t len, uint32_t)
+    {
+        typedef __attribute__((address_space(1))) const void* From;
+        typedef __attribute__((address_space(3))) void* To;
+        constexpr uint32_t kRows = kBlock / L::kPieces;            // of one round; the permutation of a row repeats after it
+        const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+        const uint32_t row = threadIdx.x / L::kPieces, col = (threadIdx.x % L::kPieces ^ L::twist(row)) * 8;
+        static_assert(kRows % 16 == 0, "rows of a round");
+        if (row0 + kTile <= len) {
+            const T* mine = head + row * ld + col;
+#pragma unroll
+            for (int i = 0; i < L::kPerThread; ++i)
+                __builtin_amdgcn_global_load_lds((From)(mine + (row0 + i * kRows) * ld), (To)(tile + (i * kBlock + wave * 64) * 8), 16, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < L::kPerThread; ++i) {
+                const uint32_t at = row0 + i * kRows + row;
+                __builtin_amdgcn_global_load_lds((From)(head + (at < len ? at : len - 1) * ld + col),
+                                                 (To)(tile + (i * kBlock + wave * 64) * 8), 16, 0, 0);
+            }
+        }
+    }
+    __device__ __forceinline__ void put(T*) {}
+};
+
+// What was fetched is in LDS for every wave, and what the waves read before may be written over.
+template <bool DIRECT>
+__device__ __forceinline__ void tiles_there()
+{
+    if (DIRECT)
+        __builtin_amdgcn_s_waitcnt(0x0f70);        // vmcnt(0): the barrier's own fence is not bound to wait for these
+    __syncthreads();
 }
 
 // The operand that stays: a wave's 32 rows as columns of B.
@@ -255,15 +321,30 @@ __device__ __forceinline__ void load_operand(Operand<T, DIM>& o, const T* head, 
     }
 }
 
+// Where a lane reads a tile, in elements from its start: the reads of one way
+// differ from the first by an exclusive or (the piece) and by a constant (the
+// row), since the rows' permutation repeats every 16 rows.
+template <int DIM>
+struct Places {
+    uint32_t row, col, col8;
+
+    __device__ __forceinline__ Places()
+    {
+        const uint32_t lane = threadIdx.x & 63, h = lane / 32, i = lane % 16, g = lane / 16 % 2, r = 4 * h + i / 4;
+        row = Tile<DIM>::place(lane % 32, h);
+        col = Tile<DIM>::place(r, 2 * g + i % 4 / 2) + i % 2 * 4;
+        col8 = Tile<DIM>::place(r + 8, 2 * g + i % 4 / 2) + i % 2 * 4;
+    }
+};
+
 // C = (rows 32 sub .. of the tile) x operand.
 template <typename T, int DIM>
-__device__ __forceinline__ f32x16 rows_times(const T* tile, int sub, const Operand<T, DIM>& b)
+__device__ __forceinline__ f32x16 rows_times(const T* tile, const Places<DIM>& at, int sub, const Operand<T, DIM>& b)
 {
-    const uint32_t lane = threadIdx.x & 63, row = 32 * sub + lane % 32, h = lane / 32;
     f32x16 c = {};
 #pragma unroll
     for (int k = 0; k < DIM / 16; ++k)
-        c = Vec8<T>::mfma(*reinterpret_cast<const typename Vec8<T>::type*>(tile + Tile<DIM>::place(row, 2 * k + h)), b.v[k], c);
+        c = Vec8<T>::mfma(*reinterpret_cast<const typename Vec8<T>::type*>(tile + 32 * DIM * sub + (at.row ^ (16 * k))), b.v[k], c);
     return c;
 }
 
@@ -279,16 +360,13 @@ __device__ __forceinline__ typename Vec8<T>::type column_pair(const T* a, const 
 // acc[n] += (rows 16 step .. 16 step + 15 of the tile, columns 32 n .. 32 n + 31)^T x p, where p holds
 // 16 rows in the order that a score's registers give.
 template <typename T, int DIM>
-__device__ __forceinline__ void columns_times(f32x16 (&acc)[DIM / 32], const T* tile, int step, typename Vec8<T>::type p)
+__device__ __forceinline__ void columns_times(f32x16 (&acc)[DIM / 32], const T* tile, const Places<DIM>& at, int step,
+                                              typename Vec8<T>::type p)
 {
-    const uint32_t lane = threadIdx.x & 63, i = lane % 16, g = lane / 16 % 2, h = lane / 32;
-    const uint32_t row = 16 * step + 4 * h + i / 4;
+    const T* rows = tile + 16 * DIM * step;
 #pragma unroll
-    for (int n = 0; n < DIM / 32; ++n) {
-        const uint32_t piece = 4 * n + 2 * g + i % 4 / 2, low = i % 2 * 4;
-        acc[n] = Vec8<T>::mfma(column_pair<T>(tile + Tile<DIM>::place(row, piece) + low, tile + Tile<DIM>::place(row + 8, piece) + low),
-                               p, acc[n]);
-    }
+    for (int n = 0; n < DIM / 32; ++n)
+        acc[n] = Vec8<T>::mfma(column_pair<T>(rows + (at.col ^ (32 * n)), rows + (at.col8 ^ (32 * n))), p, acc[n]);
 }
 
 // Registers 8 half .. 8 half + 7, rounded to nearest even.
@@ -389,6 +467,10 @@ struct BiasLds {
 constexpr uint64_t kMaxTokens = uint64_t(1) << 30;
 constexpr uint32_t kMaxHeads = 1u << 16;
 constexpr uint64_t kMaxPieces = uint64_t(1) << 31;
+
+// Rows that go straight into LDS: 16-byte aligned, of a whole tile's width.
+inline bool direct(const void* p, uint64_t ld, uint64_t hs) { return is_aligned(p, 16) && ld % 8 == 0 && hs % 8 == 0; }
+inline bool direct_dim(uint32_t dim) { return dim == 64 || dim == 128; }
 
 inline int check_heads(const void* p, uint64_t ld, uint64_t hs, uint64_t tokens, uint32_t heads, uint32_t dim, int dtype)
 {

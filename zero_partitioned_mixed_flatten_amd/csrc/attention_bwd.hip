@@ -76,8 +76,8 @@ __device__ __forceinline__ void add_diagonals(float* bins, const BiasLds& bias, 
         bins[bucket] += sum;
 }
 
-template <typename T, int DIM, bool BIAS>
-__global__ __launch_bounds__(kBlock) void attention_dq_kernel(BwdArgs<T> a)
+template <typename T, int DIM, bool BIAS, bool DIRECT>
+__global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
 {
     typedef Tile<DIM> L;
     __shared__ alignas(16) T keys[2][L::kElems];
@@ -105,10 +105,11 @@ __global__ __launch_bounds__(kBlock) void attention_dq_kernel(BwdArgs<T> a)
     const T* vp = a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(head / s.group) * a.v.hs;
 
     const KeyTiles tiles(s, at.first, kOwn, at.len);
-    Staged<T, DIM> nk, nv;
+    const Places<DIM> places;
+    Carrier<T, DIM, DIRECT> nk, nv;
     uint32_t t = tiles.begin();
-    fetch<T, DIM>(nk, kp, a.k.ld, t * kTile, at.len, s.dim);
-    fetch<T, DIM>(nv, vp, a.v.ld, t * kTile, at.len, s.dim);
+    nk.fetch(keys[0], kp, a.k.ld, t * kTile, at.len, s.dim);
+    nv.fetch(values[0], vp, a.v.ld, t * kTile, at.len, s.dim);
     Operand<T, DIM> q, dout;
     load_operand<T, DIM>(q, a.q.p + uint64_t(at.start) * a.q.ld + uint64_t(head) * a.q.hs, a.q.ld, row, s.dim);
     load_operand<T, DIM>(dout, a.dout.p + uint64_t(at.start) * a.dout.ld + uint64_t(head) * a.dout.hs, a.dout.ld, row, s.dim);
@@ -167,21 +168,22 @@ __global__ __launch_bounds__(kBlock) void attention_dq_kernel(BwdArgs<T> a)
     };
 
     f32x16 acc[DIM / 32] = {};
-    put<T, DIM>(keys[0], nk);
-    put<T, DIM>(values[0], nv);
+    nk.put(keys[0]);
+    nv.put(values[0]);
     draw_line(t, 0);
     int buf = 0;
     while (true) {
         const uint32_t next = tiles.next(t);
         const bool more = next < tiles.end;
-        __syncthreads();
+        tiles_there<DIRECT>();
         if (more) {
-            fetch<T, DIM>(nk, kp, a.k.ld, next * kTile, at.len, s.dim);
-            fetch<T, DIM>(nv, vp, a.v.ld, next * kTile, at.len, s.dim);
+            nk.fetch(keys[buf ^ 1], kp, a.k.ld, next * kTile, at.len, s.dim);
+            nv.fetch(values[buf ^ 1], vp, a.v.ld, next * kTile, at.len, s.dim);
         }
         const uint32_t j0 = t * kTile;
         const Seen see = seen(s, first, 32, j0, kTile);
         if (see != kNone) {
+            const Limits limits(s, mine, j0 + 4 * h);
             bool one_bucket = false;
             if constexpr (BIAS)
                 if (a.partials) {
@@ -193,10 +195,10 @@ __global__ __launch_bounds__(kBlock) void attention_dq_kernel(BwdArgs<T> a)
                         even_bucket = b0;
                     }
                 }
-#pragma unroll
+#pragma unroll DIM == 64 ? 2 : 1
             for (int sub = 0; sub < 2; ++sub) {
-                const f32x16 x = rows_times<T, DIM>(keys[buf], sub, q);
-                const f32x16 dp = rows_times<T, DIM>(values[buf], sub, dout);
+                const f32x16 x = rows_times<T, DIM>(keys[buf], places, sub, q);
+                const f32x16 dp = rows_times<T, DIM>(values[buf], places, sub, dout);
                 f32x16 ds;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
@@ -204,9 +206,12 @@ __global__ __launch_bounds__(kBlock) void attention_dq_kernel(BwdArgs<T> a)
                     float v = __builtin_fmaf(x[r], s.scale2, -lse);
                     if constexpr (BIAS)
                         v += bias.line[buf][kOwn - 1 - 32 * wave - c + j];
-                    v = __builtin_amdgcn_exp2f(v) * __builtin_fmaf(dp[r], unit, -delta);
-                    ds[r] = see == kAll || visible(s, mine, j0 + j) ? v : 0.0f;
+                    ds[r] = __builtin_amdgcn_exp2f(v) * __builtin_fmaf(dp[r], unit, -delta);
                 }
+                if (see == kSome)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        ds[r] = limits.sees(32 * sub + row_of(r, 0)) ? ds[r] : 0.0f;
                 if constexpr (BIAS)
                     if (a.partials) {
                         const float back = live ? 1.0f / unit : 0.0f;        // a power of two: exact
@@ -226,15 +231,15 @@ __global__ __launch_bounds__(kBlock) void attention_dq_kernel(BwdArgs<T> a)
                     }
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
-                    columns_times<T, DIM>(acc, keys[buf], 2 * sub + half, rounded<T>(ds, half));
+                    columns_times<T, DIM>(acc, keys[buf], places, 2 * sub + half, rounded<T>(ds, half));
             }
         }
         if (!more)
             break;
         t = next;
         buf ^= 1;
-        put<T, DIM>(keys[buf], nk);
-        put<T, DIM>(values[buf], nv);
+        nk.put(keys[buf]);
+        nv.put(values[buf]);
         draw_line(t, buf);
     }
     store_columns<T, DIM>(a.dq.p + uint64_t(at.start) * a.dq.ld + uint64_t(head) * a.dq.hs, a.dq.ld, mine, live, s.dim, acc,
@@ -256,8 +261,8 @@ struct RowStats {
     float lse[kTile], delta[kTile], unit[kTile];
 };
 
-template <typename T, int DIM, bool BIAS>
-__global__ __launch_bounds__(kBlock) void attention_dkv_kernel(BwdArgs<T> a)
+template <typename T, int DIM, bool BIAS, bool DIRECT>
+__global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
 {
     typedef Tile<DIM> L;
     __shared__ alignas(16) T queries[2][L::kElems];
@@ -277,6 +282,7 @@ __global__ __launch_bounds__(kBlock) void attention_dkv_kernel(BwdArgs<T> a)
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t first = at.first + 32 * wave, mine = first + c;
     const uint32_t row = mine < at.len ? mine : at.len - 1;
+    const Places<DIM> places;
     Operand<T, DIM> k, v;
     load_operand<T, DIM>(k, a.k.p + uint64_t(at.start) * a.k.ld + uint64_t(kv) * a.k.hs, a.k.ld, row, s.dim);
     load_operand<T, DIM>(v, a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(kv) * a.v.hs, a.v.ld, row, s.dim);
@@ -289,11 +295,11 @@ __global__ __launch_bounds__(kBlock) void attention_dkv_kernel(BwdArgs<T> a)
     uint32_t head = kv * s.group, t = begin;
     const uint32_t head_end = head + s.group;
 
-    Staged<T, DIM> nq, ndo;
+    Carrier<T, DIM, DIRECT> nq, ndo;
     float nstat[3] = {};
-    auto ask = [&](uint32_t hd, uint32_t tile) {
-        fetch<T, DIM>(nq, a.q.p + uint64_t(at.start) * a.q.ld + uint64_t(hd) * a.q.hs, a.q.ld, tile * kTile, at.len, s.dim);
-        fetch<T, DIM>(ndo, a.dout.p + uint64_t(at.start) * a.dout.ld + uint64_t(hd) * a.dout.hs, a.dout.ld, tile * kTile, at.len, s.dim);
+    auto ask = [&](int buf, uint32_t hd, uint32_t tile) {
+        nq.fetch(queries[buf], a.q.p + uint64_t(at.start) * a.q.ld + uint64_t(hd) * a.q.hs, a.q.ld, tile * kTile, at.len, s.dim);
+        ndo.fetch(douts[buf], a.dout.p + uint64_t(at.start) * a.dout.ld + uint64_t(hd) * a.dout.hs, a.dout.ld, tile * kTile, at.len, s.dim);
         if (threadIdx.x < kTile) {
             const uint32_t i = tile * kTile + threadIdx.x;
             const uint64_t stat = uint64_t(hd) * s.tokens + at.start + (i < at.len ? i : at.len - 1);
@@ -309,8 +315,8 @@ __global__ __launch_bounds__(kBlock) void attention_dkv_kernel(BwdArgs<T> a)
                 bias.value[threadIdx.x] = bias_value<T>(a.b, hd, threadIdx.x) * kLog2e;
     };
     auto place = [&](int buf, uint32_t tile) {
-        put<T, DIM>(queries[buf], nq);
-        put<T, DIM>(douts[buf], ndo);
+        nq.put(queries[buf]);
+        ndo.put(douts[buf]);
         if (threadIdx.x < kTile) {
             stats[buf].lse[threadIdx.x] = nstat[0] * kLog2e - (kUnits<T> ? kWeightShift : 0.0f);
             stats[buf].delta[threadIdx.x] = nstat[1];
@@ -329,7 +335,7 @@ __global__ __launch_bounds__(kBlock) void attention_dkv_kernel(BwdArgs<T> a)
         load_bias(head);
         __syncthreads();
     }
-    ask(head, t);
+    ask(0, head, t);
     place(0, t);
     f32x16 dk[DIM / 32] = {}, dv[DIM / 32] = {};
     float unit = 0x1p60f;                          // of dk's sums
@@ -341,13 +347,14 @@ __global__ __launch_bounds__(kBlock) void attention_dkv_kernel(BwdArgs<T> a)
             ++next_head;
         }
         const bool more = next_head < head_end;
-        __syncthreads();
+        tiles_there<DIRECT>();
         if (more)
-            ask(next_head, next);
+            ask(buf ^ 1, next_head, next);
         const uint32_t i0 = t * kTile;
         const Seen see = seen(s, i0, kTile, first, 32);
         if (see != kNone) {
             const bool whole = see == kAll && i0 + kTile <= at.len;
+            const QueryLimits limits(s, mine, i0 + 4 * h, at.len);
             if (kUnits<T>) {
                 float least = stats[buf].unit[lane];               // kTile lanes
 #pragma unroll
@@ -364,10 +371,11 @@ __global__ __launch_bounds__(kBlock) void attention_dkv_kernel(BwdArgs<T> a)
                 }
             }
             const float ds_unit = kUnits<T> ? unit * (1.0f / kWeightUnits) : 1.0f;
-#pragma unroll
+#pragma unroll DIM == 64 ? 2 : 1
             for (int sub = 0; sub < 2; ++sub) {
-                const f32x16 x = rows_times<T, DIM>(queries[buf], sub, k);
-                const f32x16 dp = rows_times<T, DIM>(douts[buf], sub, v);
+                const f32x16 x = rows_times<T, DIM>(queries[buf], places, sub, k);
+                const f32x16 dp = rows_times<T, DIM>(douts[buf], places, sub, v);
+                if (DIM == 128) __builtin_amdgcn_sched_barrier(0);
                 f32x16 p, ds;
 #pragma unroll
                 for (int quad = 0; quad < 4; ++quad) {
@@ -380,19 +388,25 @@ __global__ __launch_bounds__(kBlock) void attention_dkv_kernel(BwdArgs<T> a)
                         float y = __builtin_fmaf(x[r], s.scale2, -lse[e]);
                         if constexpr (BIAS)
                             y += bias.line[buf][kOwn - 1 - 32 * wave - c + i + e];
-                        y = __builtin_amdgcn_exp2f(y);
-                        y = whole || (i0 + i + e < at.len && visible(s, i0 + i + e, mine)) ? y : 0.0f;
-                        p[r] = y;
-                        float d = dp[r] - delta[e];
+                        p[r] = __builtin_amdgcn_exp2f(y);
+                        ds[r] = dp[r] - delta[e];
                         if (kUnits<T>)
-                            d *= ds_unit;
-                        ds[r] = y == 0.0f ? 0.0f : y * d;
+                            ds[r] *= ds_unit;
+                        ds[r] *= p[r];
                     }
                 }
+                if (!whole)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const bool in = limits.sees(32 * sub + row_of(r, 0));
+                        p[r] = in ? p[r] : 0.0f;
+                        ds[r] = in ? ds[r] : 0.0f;
+                    }
+                if (DIM == 128) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    columns_times<T, DIM>(dv, douts[buf], 2 * sub + half, rounded<T>(p, half));
-                    columns_times<T, DIM>(dk, queries[buf], 2 * sub + half, rounded<T>(ds, half));
+                    columns_times<T, DIM>(dv, douts[buf], places, 2 * sub + half, rounded<T>(p, half));
+                    columns_times<T, DIM>(dk, queries[buf], places, 2 * sub + half, rounded<T>(ds, half));
                 }
             }
         }
@@ -453,15 +467,15 @@ uint64_t workspace_need(const zero_attention_t& p, uint64_t tokens, uint64_t seq
     return 2 * rows_bytes(p, tokens) + uint64_t(p.heads) * ragged * p.buckets * 4;
 }
 
-template <typename T, int DIM, bool BIAS>
+template <typename T, int DIM, bool BIAS, bool DIRECT>
 int launch(const BwdArgs<T>& a, hipStream_t stream)
 {
     auto blocks = [&](uint32_t heads) { return dim3(uint32_t((uint64_t(a.slots) * heads + 7) / 8 * 8)); };
-    hipLaunchKernelGGL((attention_dq_kernel<T, DIM, BIAS>), blocks(a.s.heads), dim3(kBlock), 0, stream, a);
+    hipLaunchKernelGGL((attention_dq_kernel<T, DIM, BIAS, DIRECT>), blocks(a.s.heads), dim3(kBlock), 0, stream, a);
     const int rc = launch_status();
     if (rc)
         return rc;
-    hipLaunchKernelGGL((attention_dkv_kernel<T, DIM, BIAS>), blocks(a.s.heads / a.s.group), dim3(kBlock), 0, stream, a);
+    hipLaunchKernelGGL((attention_dkv_kernel<T, DIM, BIAS, DIRECT>), blocks(a.s.heads / a.s.group), dim3(kBlock), 0, stream, a);
     return launch_status();
 }
 
@@ -476,10 +490,17 @@ int run(Heads<void> dq, Heads<void> dk, Heads<void> dv, Heads<const void> dout, 
                  reinterpret_cast<float*>(workspace + rows), dbias ? reinterpret_cast<float*>(workspace + 2 * rows) : nullptr, s, b, 0};
     a.slots = uint32_t(slots_of(s.tokens, s.sequences, s.offsets != nullptr));
     int rc;
-    if (s.dim <= 64)
-        rc = b.table ? launch<T, 64, true>(a, stream) : launch<T, 64, false>(a, stream);
+    auto go = [&](auto dim, auto way) {
+        constexpr int kDim = decltype(dim)::value;
+        constexpr bool kDirect = decltype(way)::value;
+        return b.table ? launch<T, kDim, true, kDirect>(a, stream) : launch<T, kDim, false, kDirect>(a, stream);
+    };
+    const std::integral_constant<int, 64> d64;
+    const std::integral_constant<int, 128> d128;
+    if (direct_dim(s.dim) && direct(q.p, q.ld, q.hs) && direct(k.p, k.ld, k.hs) && direct(v.p, v.ld, v.hs) && direct(dout.p, dout.ld, dout.hs))
+        rc = s.dim == 64 ? go(d64, std::true_type{}) : go(d128, std::true_type{});
     else
-        rc = b.table ? launch<T, 128, true>(a, stream) : launch<T, 128, false>(a, stream);
+        rc = s.dim <= 64 ? go(d64, std::false_type{}) : go(d128, std::false_type{});
     if (rc || !dbias)
         return rc;
     hipLaunchKernelGGL(fold_bias_kernel<T>, dim3(s.heads), dim3(kBlock), 0, stream, dbias, grad_dtype == ZERO_F32, accumulate, a.partials,

@@ -163,7 +163,7 @@ struct Limits {
         far = s.window > i ? -1 - int(j0) : int(i - s.window) - int(j0);
         first = s.sinks > j0 ? int(s.sinks - j0 < uint32_t(kTile) ? s.sinks - j0 : uint32_t(kTile)) : 0;
     }
-    __device__ __forceinline__ bool sees(int j) const { return j <= near && (j > far || j < first); }
+    __device__ __forceinline__ bool sees(int j) const { return (j <= near) & ((j > far) | (j < first)); }
 };
 
 // The other way round: of the queries i0 + i of a tile, those that see the lane's key j have i >= near and i < end.
@@ -176,7 +176,7 @@ struct QueryLimits {
         const uint32_t last = j < s.sinks || s.window > len || j + s.window > len ? len : j + s.window;
         end = int(last) - int(i0);
     }
-    __device__ __forceinline__ bool sees(int i) const { return i >= near && i < end; }
+    __device__ __forceinline__ bool sees(int i) const { return (i >= near) & (i < end); }
 };
 
 // The key tiles that some query of [i, i + nq) sees, in order: those of the
@@ -262,31 +262,43 @@ public:
 template <typename T, int DIM>
 class Carrier<T, DIM, true> {
     typedef Tile<DIM> L;
+    static constexpr uint32_t kRows = kBlock / L::kPieces;         // of one round; the permutation of a row repeats after it
+    static_assert(kRows % 16 == 0, "rows of a round");
 
 public:
+    // The compiler waits for such a load before any read of LDS that it cannot tell apart from it, the other buffer's too: in
+    // assembly it does not, and tiles_there() waits.
     __device__ __forceinline__ void fetch(T* tile, const T* head, uint64_t ld, uint32_t row0, uint32_t len, uint32_t)
     {
-        typedef __attribute__((address_space(1))) const void* From;
-        typedef __attribute__((address_space(3))) void* To;
-        constexpr uint32_t kRows = kBlock / L::kPieces;            // of one round; the permutation of a row repeats after it
         const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
         const uint32_t row = threadIdx.x / L::kPieces, col = (threadIdx.x % L::kPieces ^ L::twist(row)) * 8;
-        static_assert(kRows % 16 == 0, "rows of a round");
-        if (row0 + kTile <= len) {
-            const T* mine = head + row * ld + col;
+        const uint32_t to = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) T*)tile)) + wave * 1024;
+        const T* from = head + row0 * ld;
+        const uint32_t step = uint32_t(ld) * sizeof(T), last = len - 1 - row0;      // ld is below 2^24
+        if (last >= uint32_t(kTile) - 1) {
+            const uint32_t at = row * step + col * uint32_t(sizeof(T));
 #pragma unroll
             for (int i = 0; i < L::kPerThread; ++i)
-                __builtin_amdgcn_global_load_lds((From)(mine + (row0 + i * kRows) * ld), (To)(tile + (i * kBlock + wave * 64) * 8), 16, 0, 0);
+                load(to + i * 16 * kBlock, at, from + i * kRows * ld);
         } else {
 #pragma unroll
             for (int i = 0; i < L::kPerThread; ++i) {
-                const uint32_t at = row0 + i * kRows + row;
-                __builtin_amdgcn_global_load_lds((From)(head + (at < len ? at : len - 1) * ld + col),
-                                                 (To)(tile + (i * kBlock + wave * 64) * 8), 16, 0, 0);
+                const uint32_t r = row + i * kRows;
+                load(to + i * 16 * kBlock, (r < last ? r : last) * step + col * uint32_t(sizeof(T)), from);
             }
         }
     }
     __device__ __forceinline__ void put(T*) {}
+
+private:
+    static __device__ __forceinline__ void load(uint32_t to, uint32_t at, const T* base)
+    {
+        const uint64_t b = reinterpret_cast<uintptr_t>(base);      // the same in every lane
+        const uint64_t from = uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(b >> 32)))) << 32 |
+                              uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(b)));
+        to = __builtin_amdgcn_readfirstlane(to);
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(to), "v"(at), "s"(from) : "memory");
+    }
 };
 
 // What was fetched is in LDS for every wave, and what the waves read before may be written over.
@@ -294,7 +306,7 @@ template <bool DIRECT>
 __device__ __forceinline__ void tiles_there()
 {
     if (DIRECT)
-        __builtin_amdgcn_s_waitcnt(0x0f70);        // vmcnt(0): the barrier's own fence is not bound to wait for these
+        asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
     __syncthreads();
 }
 
@@ -469,7 +481,10 @@ constexpr uint32_t kMaxHeads = 1u << 16;
 constexpr uint64_t kMaxPieces = uint64_t(1) << 31;
 
 // Rows that go straight into LDS: 16-byte aligned, of a whole tile's width.
-inline bool direct(const void* p, uint64_t ld, uint64_t hs) { return is_aligned(p, 16) && ld % 8 == 0 && hs % 8 == 0; }
+inline bool direct(const void* p, uint64_t ld, uint64_t hs)
+{
+    return is_aligned(p, 16) && ld % 8 == 0 && hs % 8 == 0 && ld < (1u << 24);
+}
 inline bool direct_dim(uint32_t dim) { return dim == 64 || dim == 128; }
 
 inline int check_heads(const void* p, uint64_t ld, uint64_t hs, uint64_t tokens, uint32_t heads, uint32_t dim, int dtype)

@@ -727,7 +727,7 @@ int zero_dropout_layernorm_bwd(void* dx, uint64_t ld_dx, void* dr, uint64_t ld_d
  * Errors: ZERO_EINVAL (NULL, a type, heads = 0, dim or rot odd or 0, rot > dim,
  *         eps not finite and > 0 in binary32, rot without a table, q_out ==
  *         k_out, k's arguments without kv_heads), ZERO_EALIGN, ZERO_ERANGE (dim
- *         > 256, more than 2^30 tokens or table rows, 65536 heads or 2^34 heads
+ *         > 256, more than 2^30 tokens or table rows, 65535 heads or 2^34 heads
  *         of all tokens, ld or hs < dim or > 2^50, an extent > 2^56), ZERO_EHIP. */
 int zero_qk_norm_rope_fwd(void* q_out, uint64_t ld_q_out, uint64_t hs_q_out, void* k_out, uint64_t ld_k_out,
                           uint64_t hs_k_out, const void* q, uint64_t ld_q, uint64_t hs_q, const void* k, uint64_t ld_k,
@@ -771,7 +771,7 @@ int zero_rope_table(float* table, uint64_t positions, uint32_t rot, double base,
 
 /* What a model's attention is, the same for every call. */
 typedef struct {
-    uint32_t heads;             /* of queries; a multiple of kv_heads, <= 65536 */
+    uint32_t heads;             /* of queries; a multiple of kv_heads, <= 65535 */
     uint32_t kv_heads;          /* of keys and values: query head h reads h / (heads / kv_heads) */
     uint32_t dim;               /* elements of a head: a multiple of 8, <= 128 */
     uint32_t sinks;             /* first tokens of a sequence that stay visible */
@@ -811,7 +811,7 @@ int zero_attention_buckets(uint32_t* starts, uint32_t buckets, uint32_t max_dist
  *         sequences = 0 with tokens, tokens not a multiple of sequences
  *         without offsets, starts not ascending from 0, bias without buckets
  *         or the other way round), ZERO_EALIGN, ZERO_ERANGE (more than 2^30
- *         tokens or sequences, heads * (tokens / 128 + sequences) >= 2^31, ld
+ *         tokens or sequences, heads * (tokens / 128 + sequences) >= 2^27, ld
  *         or hs < dim or > 2^50, an extent > 2^56, dim > 128), ZERO_EHIP. */
 int zero_attention_fwd(void* o, uint64_t ld_o, uint64_t hs_o, float* lse, const void* q, uint64_t ld_q, uint64_t hs_q,
                        const void* k, uint64_t ld_k, uint64_t hs_k, const void* v, uint64_t ld_v, uint64_t hs_v,

@@ -223,3 +223,19 @@ def test_gradient_scale(do_scale):
         log("scale", do_scale, dtype)
         c = Call([333], 2, 1, 64, dtype, window=100, sinks=2, do_scale=do_scale)
         c.check_bwd(*c.check_fwd())
+
+
+@pytest.mark.parametrize("sinks", [1, 33, 128, 129])
+def test_long_sequences_with_first_tokens(sinks):
+    """The queries behind the window, a thousand at a time, on the keys of the first tokens."""
+    for lengths, heads, kv_heads, dtype, dim in (([2500], 2, 1, F16, 64), ([1100, 40, 2100], 2, 2, BF16, 128)):
+        log("long", sinks, lengths)
+        c = Call(lengths, heads, kv_heads, dim, dtype, window=70, sinks=sinks, after=5)
+        c.check_bwd(*c.check_fwd())
+
+
+def test_long_sequence_with_bias():
+    c = Call([2200], 4, 1, 64, F16, window=600, sinks=9, starts=Z.zero_attention_buckets(32, 1000))
+    c.check_bwd(*c.check_fwd())
+    c = Call([1700], 8, 1, 128, BF16, starts=Z.zero_attention_buckets(16, 300), bias_dtype=F32)
+    c.check_bwd(*c.check_fwd())

@@ -39,7 +39,7 @@ __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kerne
         return;
     const uint32_t head = work / a.slots;
     Piece at;
-    if (!find_piece(s, a.slots - 1 - (work - head * a.slots), &at))      // a head's long rows first
+    if (!find_piece(s, a.slots - 1 - (work - head * a.slots), kOwn, &at))      // a head's long rows first
         return;
     const uint32_t lane = threadIdx.x & 63, c = lane % 32, h = lane / 32;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -211,7 +211,7 @@ int make_shape(const zero_attention_t* a, uint64_t tokens, const int32_t* dev_of
     b->f32 = vec_dtype == ZERO_F32;
     for (uint32_t i = 0; i < ZERO_MAX_BUCKETS; ++i)
         b->starts[i] = i < a->buckets ? a->starts[i] : 0xffffffffu;
-    if (tokens && slots_of(s->tokens, s->sequences, dev_offsets != nullptr) * a->heads >= kMaxPieces)
+    if (tokens && slots_of(s->tokens, s->sequences, dev_offsets != nullptr, kOwn) * a->heads >= kMaxPieces)
         return ZERO_ERANGE;
     return ZERO_OK;
 }
@@ -223,7 +223,7 @@ int run_fwd(void* o, uint64_t ld_o, uint64_t hs_o, float* lse, const void* q, ui
             uint64_t hs_k, const void* v, uint64_t ld_v, uint64_t hs_v, const Shape& s, const Buckets& b, hipStream_t stream)
 {
     const FwdArgs<T> a{{static_cast<T*>(o), ld_o, hs_o}, lse, {static_cast<const T*>(q), ld_q, hs_q}, {static_cast<const T*>(k), ld_k, hs_k},
-                       {static_cast<const T*>(v), ld_v, hs_v}, s, b, uint32_t(slots_of(s.tokens, s.sequences, s.offsets != nullptr))};
+                       {static_cast<const T*>(v), ld_v, hs_v}, s, b, uint32_t(slots_of(s.tokens, s.sequences, s.offsets != nullptr, kOwn))};
     if (direct_dim(s.dim) && direct(k, ld_k, hs_k) && direct(v, ld_v, hs_v))
         return s.dim == 64 ? launch<T, 64, true>(a, stream) : launch<T, 128, true>(a, stream);
     return s.dim <= 64 ? launch<T, 64, false>(a, stream) : launch<T, 128, false>(a, stream);

@@ -24,6 +24,7 @@ namespace attention {
 
 typedef layer::bf16 bf16;
 typedef layer::bf16x8 bf16x8;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kWaves = 4;                          // waves of a workgroup
@@ -78,31 +79,34 @@ struct Buckets {
 };
 
 // ---- the tile of a workgroup --------------------------------------------------------
-// The rows of all sequences are dealt out in pieces of kOwn that do not cross a
+// The rows of all sequences are dealt out in pieces of `own` that do not cross a
 // sequence.  Where the lengths are in device memory, sequence s gets the slots
-// from offsets[s] / kOwn + s on: at least as many as it has pieces, so a slot
+// from offsets[s] / own + s on: at least as many as it has pieces, so a slot
 // finds its sequence from the offsets alone, and some slots stay empty.
 // Offsets out of order or out of range are clamped: they give wrong tiles, but
 // none outside the tensors.
 struct Piece {
-    uint32_t start, len;                           // the sequence: first token, tokens
+    uint32_t seq, start, len;                      // the sequence: its index, first token, tokens
     uint32_t first;                                // the piece's first row in the sequence
+    uint32_t slots;                                // the sequence's first slot
 };
 
-__host__ __device__ inline uint64_t slots_of(uint32_t tokens, uint32_t sequences, bool ragged)
+__host__ __device__ inline uint64_t slots_of(uint32_t tokens, uint32_t sequences, bool ragged, uint32_t own)
 {
     if (ragged)
-        return uint64_t(tokens) / kOwn + sequences;
-    return uint64_t(sequences) * ((tokens / sequences + kOwn - 1) / kOwn);
+        return uint64_t(tokens) / own + sequences;
+    return uint64_t(sequences) * ((tokens / sequences + own - 1) / own);
 }
 
-__device__ __forceinline__ bool find_piece(const Shape& s, uint32_t slot, Piece* out)
+__device__ __forceinline__ bool find_piece(const Shape& s, uint32_t slot, uint32_t own, Piece* out)
 {
     if (!s.offsets) {
-        const uint32_t per = (s.length + kOwn - 1) / kOwn, seq = slot / per;
-        out->start = seq * s.length;
+        const uint32_t per = (s.length + own - 1) / own;
+        out->seq = slot / per;
+        out->start = out->seq * s.length;
         out->len = s.length;
-        out->first = (slot - seq * per) * kOwn;
+        out->slots = out->seq * per;
+        out->first = (slot - out->slots) * own;
         return true;
     }
     const uint32_t lane = threadIdx.x & 63;
@@ -113,7 +117,7 @@ __device__ __forceinline__ bool find_piece(const Shape& s, uint32_t slot, Piece*
     uint32_t seq = 0;                              // the number of sequences whose slots begin at or before this one
     for (uint32_t base = 0; base < s.sequences; base += 64) {
         const uint32_t i = base + lane;
-        const bool before = i < s.sequences && offset(i < s.sequences ? i : 0) / kOwn + i <= slot;
+        const bool before = i < s.sequences && offset(i < s.sequences ? i : 0) / own + i <= slot;
         const uint32_t n = __popcll(__ballot(before));
         seq += n;
         if (n < 64)
@@ -123,11 +127,12 @@ __device__ __forceinline__ bool find_piece(const Shape& s, uint32_t slot, Piece*
         return false;
     --seq;
     const uint32_t start = __builtin_amdgcn_readfirstlane(offset(seq)), end = __builtin_amdgcn_readfirstlane(offset(seq + 1));
-    const uint32_t begin = start / kOwn + seq;
+    out->seq = seq;
     out->start = start;
     out->len = end > start ? end - start : 0;
-    out->first = (slot - begin) * kOwn;
-    return slot >= begin && uint64_t(slot - begin) * kOwn < out->len;
+    out->slots = start / own + seq;
+    out->first = (slot - out->slots) * own;
+    return slot >= out->slots && uint64_t(slot - out->slots) * own < out->len;
 }
 
 // Blocks go to the eight dies in turn; neighbours that share a head's keys
@@ -347,6 +352,8 @@ struct Places {
         col = Tile<DIM>::place(r, 2 * g + i % 4 / 2) + i % 2 * 4;
         col8 = Tile<DIM>::place(r + 8, 2 * g + i % 4 / 2) + i % 2 * 4;
     }
+    // In a loop that is short of registers: the places are formed anew from these three instead of kept.
+    __device__ __forceinline__ void anew() { asm volatile("" : "+v"(row), "+v"(col), "+v"(col8)); }
 };
 
 // C = (rows 32 sub .. of the tile) x operand.
@@ -477,8 +484,8 @@ struct BiasLds {
 
 // ---- host side --------------------------------------------------------------------------
 constexpr uint64_t kMaxTokens = uint64_t(1) << 30;
-constexpr uint32_t kMaxHeads = 1u << 16;
-constexpr uint64_t kMaxPieces = uint64_t(1) << 31;
+constexpr uint32_t kMaxHeads = 65535;
+constexpr uint64_t kMaxPieces = uint64_t(1) << 27;
 
 // Rows that go straight into LDS: 16-byte aligned, of a whole tile's width.
 inline bool direct(const void* p, uint64_t ld, uint64_t hs)

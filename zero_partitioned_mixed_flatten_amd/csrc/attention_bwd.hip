@@ -20,7 +20,8 @@ namespace {
 
 // binary16 has few exponents below a gradient's: ds is formed in units of
 // 2^-k where 2^k is about |do_i| (its 2-norm, a power of two, so the products
-// are exact), and p of the dv product in units of 2^-6.  bfloat16 needs neither.
+// are exact), for dk the largest of the rows so far, and p of the dv product in
+// units of 2^-6.  bfloat16 needs neither.
 template <typename T>
 constexpr bool kUnits = __is_same(T, _Float16);
 constexpr float kWeightUnits = 64.0f, kWeightShift = 6.0f;
@@ -30,12 +31,14 @@ struct BwdArgs {
     Heads<T> dq, dk, dv;
     Heads<const T> dout, o, q, k, v;
     const float* lse;
-    float* delta;                                  // heads x tokens
-    float* unit;                                   // heads x tokens: 2^k's inverse (binary16)
+    f32x2* stats;                                  // heads x tokens: lse in units of log2 (binary16: less the weights' units), delta
+    float* units;                                  // heads x slots x waves: 2^-k of 32 rows' largest (binary16)
     float* partials;                               // heads x slots x buckets
+    float* near;                                   // parts of dk and dv (see dkv_items)
+    float* far;
     Shape s;
     Buckets b;
-    uint32_t slots;
+    uint32_t slots, splits, far_slots;
 };
 
 struct BinsLds {
@@ -91,7 +94,7 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
         return;
     const uint32_t head = work / a.slots, slot = a.slots - 1 - (work - head * a.slots);
     Piece at;
-    if (!find_piece(s, slot, &at)) {
+    if (!find_piece(s, slot, kOwn, &at)) {
         if (BIAS && a.partials && threadIdx.x < a.b.count)
             a.partials[(uint64_t(head) * a.slots + slot) * a.b.count + threadIdx.x] = 0.0f;
         return;
@@ -105,7 +108,7 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
     const T* vp = a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(head / s.group) * a.v.hs;
 
     const KeyTiles tiles(s, at.first, kOwn, at.len);
-    const Places<DIM> places;
+    Places<DIM> places;
     Carrier<T, DIM, DIRECT> nk, nv;
     uint32_t t = tiles.begin();
     nk.fetch(keys[0], kp, a.k.ld, t * kTile, at.len, s.dim);
@@ -133,11 +136,15 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
     if (kUnits<T>) {
         // a row of zeros gets a large unit, so that it does not set that of the rows beside it
         unit = norm > 0.0f ? __builtin_ldexpf(1.0f, -((__builtin_amdgcn_frexp_expf(norm) + 1) >> 1)) : 0x1p60f;
-        if (live && h == 0)
-            a.unit[stat] = unit;
+        float least = unit;
+#pragma unroll
+        for (int step = 16; step; step >>= 1)
+            least = fminf(least, __shfl_xor(least, step));
+        if (lane == 0)
+            a.units[(uint64_t(head) * a.slots + slot) * kWaves + wave] = least;
     }
     if (live && h == 0)
-        a.delta[stat] = delta;
+        a.stats[stat] = f32x2{lse - (kUnits<T> ? kWeightShift : 0.0f), delta};
     delta *= unit;
 
     if constexpr (BIAS) {
@@ -197,6 +204,8 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
                 }
 #pragma unroll DIM == 64 ? 2 : 1
             for (int sub = 0; sub < 2; ++sub) {
+                if (DIM == 128)
+                    places.anew();
                 const f32x16 x = rows_times<T, DIM>(keys[buf], places, sub, q);
                 const f32x16 dp = rows_times<T, DIM>(values[buf], places, sub, dout);
                 f32x16 ds;
@@ -257,9 +266,31 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
         }
 }
 
+// ---- dk and dv ----------------------------------------------------------------------
+// A workgroup goes over the tiles of queries that see its keys, for each query
+// head that shares the key head: a list of (head, tile) steps.  Two things
+// would leave a few workgroups with most of the work:
+//   - few keys in all: the list is then cut into `splits` parts, whose binary32
+//     sums go to the workspace and are added up by dkv_sum_kernel;
+//   - a window with first tokens that stay visible: the piece of keys that holds
+//     them is seen by every query of the sequence.  Its list ends with the
+//     window, and the queries behind are taken kFar at a time by workgroups of
+//     their own, whose sums are added likewise.
+constexpr uint32_t kFar = 1024;
+
 struct RowStats {
-    float lse[kTile], delta[kTile], unit[kTile];
+    float lse[kTile], delta[kTile];
 };
+
+// Whether the queries behind the window are taken apart: where the first tokens are in one piece.
+__host__ __device__ inline bool far_apart(const Shape& s) { return s.sinks && s.sinks <= kOwn && s.window != 0xffffffffu; }
+
+// The queries below this are in the list of the piece of keys at `first`.
+__device__ __forceinline__ uint32_t near_end(const Shape& s, uint32_t first, uint32_t len)
+{
+    const bool bounded = s.window != 0xffffffffu && (first >= s.sinks || far_apart(s));
+    return bounded && len - first > kOwn - 1 && len - first - (kOwn - 1) > s.window ? first + (kOwn - 1) + s.window : len;
+}
 
 template <typename T, int DIM, bool BIAS, bool DIRECT>
 __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
@@ -271,43 +302,74 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
     __shared__ typename std::conditional<BIAS, BiasLds, int>::type bias;
 
     const Shape& s = a.s;
-    const uint32_t work = die_local(blockIdx.x, gridDim.x), kv_heads = s.heads / s.group;
-    if (work >= a.slots * kv_heads)
+    const uint32_t kv_heads = s.heads / s.group;
+    const uint32_t far_items = a.far_slots * kv_heads, near_items = a.slots * kv_heads * a.splits;
+    uint32_t work = die_local(blockIdx.x, gridDim.x);
+    if (work >= far_items + near_items)
         return;
-    const uint32_t kv = work / a.slots;
+    const bool is_far = work < far_items;
     Piece at;
-    if (!find_piece(s, work - kv * a.slots, &at))  // the first keys have the most queries
-        return;
+    uint32_t kv, part = 0, begin, end, first_key;
+    float* out = nullptr;                          // binary32 sums: dk of the piece's rows, then dv; NULL: dk and dv themselves
+    if (is_far) {
+        kv = work / a.far_slots;
+        const uint32_t slot = work - kv * a.far_slots;
+        if (!find_piece(s, slot, kFar, &at))
+            return;
+        first_key = 0;
+        begin = (near_end(s, 0, at.len) + kTile - 1) / kTile;
+        const uint32_t stop = at.first + kFar < at.len ? at.first + kFar : at.len;
+        begin = begin > at.first / kTile ? begin : at.first / kTile;
+        end = (stop + kTile - 1) / kTile;
+        if (begin >= end)
+            return;
+        out = a.far + uint64_t(work) * (2 * kOwn * DIM);
+    } else {
+        work -= far_items;
+        kv = work / (a.slots * a.splits);
+        const uint32_t rest = work - kv * (a.slots * a.splits), slot = rest / a.splits;
+        part = rest - slot * a.splits;
+        if (!find_piece(s, slot, kOwn, &at))       // the first keys have the most queries
+            return;
+        first_key = at.first;
+        begin = at.first / kTile;
+        end = (near_end(s, at.first, at.len) + kTile - 1) / kTile;
+        if (a.splits > 1)
+            out = a.near + uint64_t(work) * (2 * kOwn * DIM);
+        else if (a.far_slots && at.first == 0)
+            out = a.near + (uint64_t(kv) * s.sequences + at.seq) * (2 * kOwn * DIM);
+    }
     const uint32_t lane = threadIdx.x & 63, c = lane % 32, h = lane / 32;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const uint32_t first = at.first + 32 * wave, mine = first + c;
+    const uint32_t first = first_key + 32 * wave, mine = first + c;
     const uint32_t row = mine < at.len ? mine : at.len - 1;
-    const Places<DIM> places;
+    Places<DIM> places;
     Operand<T, DIM> k, v;
     load_operand<T, DIM>(k, a.k.p + uint64_t(at.start) * a.k.ld + uint64_t(kv) * a.k.hs, a.k.ld, row, s.dim);
     load_operand<T, DIM>(v, a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(kv) * a.v.hs, a.v.ld, row, s.dim);
 
-    // the tiles of queries that see one of the keys, for each query head in turn
-    uint32_t last = at.len;                        // queries below this
-    if (at.first >= s.sinks && s.window != 0xffffffffu && at.len - at.first > kOwn - 1 && at.len - at.first - (kOwn - 1) > s.window)
-        last = at.first + (kOwn - 1) + s.window;
-    const uint32_t begin = at.first / kTile, end = (last + kTile - 1) / kTile;
-    uint32_t head = kv * s.group, t = begin;
-    const uint32_t head_end = head + s.group;
+    const uint32_t tiles = end - begin, steps = tiles * s.group;
+    uint32_t step = is_far ? 0 : uint32_t(uint64_t(steps) * part / a.splits);
+    const uint32_t step_end = is_far ? steps : uint32_t(uint64_t(steps) * (part + 1) / a.splits);
+    uint32_t head = step / tiles, t = begin + step - head * tiles;
+    head += kv * s.group;
 
     Carrier<T, DIM, DIRECT> nq, ndo;
-    float nstat[3] = {};
+    f32x2 nstat = {};
+    float nunit = 0.0f, tile_unit = 0.0f;
+    // the sequence's first slot among the dq kernel's, which wrote the units
+    const uint32_t unit_slots = s.offsets ? at.start / kOwn + at.seq : at.seq * ((s.length + kOwn - 1) / kOwn);
     auto ask = [&](int buf, uint32_t hd, uint32_t tile) {
-        nq.fetch(queries[buf], a.q.p + uint64_t(at.start) * a.q.ld + uint64_t(hd) * a.q.hs, a.q.ld, tile * kTile, at.len, s.dim);
-        ndo.fetch(douts[buf], a.dout.p + uint64_t(at.start) * a.dout.ld + uint64_t(hd) * a.dout.hs, a.dout.ld, tile * kTile, at.len, s.dim);
         if (threadIdx.x < kTile) {
             const uint32_t i = tile * kTile + threadIdx.x;
-            const uint64_t stat = uint64_t(hd) * s.tokens + at.start + (i < at.len ? i : at.len - 1);
-            nstat[0] = a.lse[stat];
-            nstat[1] = a.delta[stat];
-            if (kUnits<T>)
-                nstat[2] = a.unit[stat];
+            nstat = a.stats[uint64_t(hd) * s.tokens + at.start + (i < at.len ? i : at.len - 1)];
         }
+        if (kUnits<T>) {
+            const float* u = a.units + (uint64_t(hd) * a.slots + unit_slots) * kWaves + 2 * tile;
+            nunit = fminf(u[0], u[1]);
+        }
+        nq.fetch(queries[buf], a.q.p + uint64_t(at.start) * a.q.ld + uint64_t(hd) * a.q.hs, a.q.ld, tile * kTile, at.len, s.dim);
+        ndo.fetch(douts[buf], a.dout.p + uint64_t(at.start) * a.dout.ld + uint64_t(hd) * a.dout.hs, a.dout.ld, tile * kTile, at.len, s.dim);
     };
     auto load_bias = [&](uint32_t hd) {
         if constexpr (BIAS)
@@ -318,14 +380,13 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
         nq.put(queries[buf]);
         ndo.put(douts[buf]);
         if (threadIdx.x < kTile) {
-            stats[buf].lse[threadIdx.x] = nstat[0] * kLog2e - (kUnits<T> ? kWeightShift : 0.0f);
+            stats[buf].lse[threadIdx.x] = nstat[0];
             stats[buf].delta[threadIdx.x] = nstat[1];
-            if (kUnits<T>)
-                stats[buf].unit[threadIdx.x] = nstat[2];
         }
+        tile_unit = nunit;
         if constexpr (BIAS)
             if (threadIdx.x < kOwn + kTile - 1) {
-                const int d = int(tile * kTile) - int(at.first + kOwn - 1) + int(threadIdx.x);
+                const int d = int(tile * kTile) - int(first_key + kOwn - 1) + int(threadIdx.x);
                 bias.line[buf][threadIdx.x] = bias.value[bucket_of(bias.starts, a.b.count, d > 0 ? d : 0)];
             }
     };
@@ -335,18 +396,20 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
         load_bias(head);
         __syncthreads();
     }
-    ask(0, head, t);
-    place(0, t);
     f32x16 dk[DIM / 32] = {}, dv[DIM / 32] = {};
     float unit = 0x1p60f;                          // of dk's sums
     int buf = 0;
-    while (true) {
+    if (step < step_end) {
+        ask(0, head, t);
+        place(0, t);
+    }
+    while (step < step_end) {
         uint32_t next = t + 1, next_head = head;
         if (next >= end) {
             next = begin;
             ++next_head;
         }
-        const bool more = next_head < head_end;
+        const bool more = ++step < step_end;
         tiles_there<DIRECT>();
         if (more)
             ask(buf ^ 1, next_head, next);
@@ -355,24 +418,20 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
         if (see != kNone) {
             const bool whole = see == kAll && i0 + kTile <= at.len;
             const QueryLimits limits(s, mine, i0 + 4 * h, at.len);
-            if (kUnits<T>) {
-                float least = stats[buf].unit[lane];               // kTile lanes
+            if (kUnits<T> && tile_unit < unit) {   // the same for every lane
+                const float by = tile_unit / unit;
+                unit = tile_unit;
 #pragma unroll
-                for (int step = 32; step; step >>= 1)
-                    least = fminf(least, __shfl_xor(least, step));
-                if (least < unit) {                // the same for every lane
-                    const float by = least / unit;
-                    unit = least;
+                for (int n = 0; n < DIM / 32; ++n)
 #pragma unroll
-                    for (int n = 0; n < DIM / 32; ++n)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            dk[n][r] *= by;
-                }
+                    for (int r = 0; r < 16; ++r)
+                        dk[n][r] *= by;
             }
-            const float ds_unit = kUnits<T> ? unit * (1.0f / kWeightUnits) : 1.0f;
+            const float ds_unit = unit * (1.0f / kWeightUnits);
 #pragma unroll DIM == 64 ? 2 : 1
             for (int sub = 0; sub < 2; ++sub) {
+                if (DIM == 128)
+                    places.anew();
                 const f32x16 x = rows_times<T, DIM>(queries[buf], places, sub, k);
                 const f32x16 dp = rows_times<T, DIM>(douts[buf], places, sub, v);
                 if (DIM == 128) __builtin_amdgcn_sched_barrier(0);
@@ -424,10 +483,67 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
         place(buf, t);
     }
     const bool live = mine < at.len;
-    store_columns<T, DIM>(a.dk.p + uint64_t(at.start) * a.dk.ld + uint64_t(kv) * a.dk.hs, a.dk.ld, mine, live, s.dim, dk,
-                          kUnits<T> ? s.scale / unit : s.scale);
-    store_columns<T, DIM>(a.dv.p + uint64_t(at.start) * a.dv.ld + uint64_t(kv) * a.dv.hs, a.dv.ld, mine, live, s.dim, dv,
-                          kUnits<T> ? 1.0f / kWeightUnits : 1.0f);
+    const float k_unit = kUnits<T> ? s.scale / unit : s.scale, v_unit = kUnits<T> ? 1.0f / kWeightUnits : 1.0f;
+    if (!out) {
+        store_columns<T, DIM>(a.dk.p + uint64_t(at.start) * a.dk.ld + uint64_t(kv) * a.dk.hs, a.dk.ld, mine, live, s.dim, dk, k_unit);
+        store_columns<T, DIM>(a.dv.p + uint64_t(at.start) * a.dv.ld + uint64_t(kv) * a.dv.hs, a.dv.ld, mine, live, s.dim, dv, v_unit);
+        return;
+    }
+    float* mine_out = out + (32 * wave + c) * DIM + 4 * h;
+#pragma unroll
+    for (int n = 0; n < DIM / 32; ++n)
+#pragma unroll
+        for (int quad = 0; quad < 4; ++quad) {
+            f32x4 x, y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] = dk[n][4 * quad + e] * k_unit;
+                y[e] = dv[n][4 * quad + e] * v_unit;
+            }
+            *reinterpret_cast<f32x4*>(mine_out + 32 * n + 8 * quad) = x;
+            *reinterpret_cast<f32x4*>(mine_out + kOwn * DIM + 32 * n + 8 * quad) = y;
+        }
+}
+
+// dk and dv of a piece of keys from its parts, in their order.  16 rows a workgroup.
+constexpr int kSumRows = 16;
+
+template <typename T, int DIM>
+__global__ __launch_bounds__(kSumRows* DIM / 8) void dkv_sum_kernel(BwdArgs<T> a)
+{
+    typedef typename Vec8<T>::type V;
+    typedef V __attribute__((aligned(sizeof(T)))) VU;
+    const Shape& s = a.s;
+    const uint32_t kv = blockIdx.y;
+    Piece at;
+    if (!find_piece(s, blockIdx.x / (kOwn / kSumRows), kOwn, &at) || (a.splits == 1 && at.first))
+        return;
+    const uint32_t local = blockIdx.x % (kOwn / kSumRows) * kSumRows + threadIdx.x / (DIM / 8), col = threadIdx.x % (DIM / 8) * 8;
+    const uint32_t row = at.first + local;
+    if (row >= at.len || col >= s.dim)
+        return;
+    constexpr uint64_t kPart = 2 * kOwn * DIM;
+    const float* near = a.near + (a.splits > 1 ? (uint64_t(kv) * a.slots + blockIdx.x / (kOwn / kSumRows)) * a.splits : uint64_t(kv) * s.sequences + at.seq) * kPart;
+    uint32_t far_begin = 0, far_end = 0;
+    if (a.far_slots && at.first == 0) {
+        const uint32_t slots = s.offsets ? at.start / kFar + at.seq : at.seq * ((s.length + kFar - 1) / kFar);
+        const uint32_t behind = (near_end(s, 0, at.len) + kTile - 1) / kTile * kTile;
+        if (behind < at.len) {
+            far_begin = slots + behind / kFar;
+            far_end = slots + (at.len + kFar - 1) / kFar;
+        }
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const uint64_t place = (which * kOwn + local) * DIM + col;
+        layer::f32x8 sum = {};
+        for (uint32_t p = 0; p < a.splits; ++p)
+            sum += *reinterpret_cast<const layer::f32x8*>(near + p * kPart + place);
+        for (uint32_t p = far_begin; p < far_end; ++p)
+            sum += *reinterpret_cast<const layer::f32x8*>(a.far + (uint64_t(kv) * a.far_slots + p) * kPart + place);
+        const Heads<T>& to = which ? a.dv : a.dk;
+        *reinterpret_cast<VU*>(to.p + (uint64_t(at.start) + row) * to.ld + uint64_t(kv) * to.hs + col) = __builtin_convertvector(sum, V);
+    }
 }
 
 // A head's bias gradient: its partials added up in their order.
@@ -457,39 +573,91 @@ __global__ __launch_bounds__(kBlock) void fold_bias_kernel(void* dst, bool f32, 
 }
 
 // ---- host side --------------------------------------------------------------------------
-// The workspace: delta and (binary16) the units, a value each for every row,
-// then the bias' partials.  Its size takes the larger form of either choice.
-uint64_t rows_bytes(const zero_attention_t& p, uint64_t tokens) { return (uint64_t(p.heads) * tokens * 4 + 255) / 256 * 256; }
+// How the work on dk and dv is dealt out (see attention_dkv_kernel).
+struct Deal {
+    uint64_t slots, splits, far_slots;
+};
 
-uint64_t workspace_need(const zero_attention_t& p, uint64_t tokens, uint64_t sequences)
+Deal deal(const Shape& s, bool ragged)
 {
-    const uint64_t ragged = slots_of(uint32_t(tokens), uint32_t(sequences), true);
-    return 2 * rows_bytes(p, tokens) + uint64_t(p.heads) * ragged * p.buckets * 4;
+    Deal d{slots_of(s.tokens, s.sequences, ragged, kOwn), 1, 0};
+    if (far_apart(s) && s.tokens > s.window)
+        d.far_slots = slots_of(s.tokens, s.sequences, ragged, kFar);
+    // enough parts for two workgroups a CU, but none with fewer than four steps where a sequence has the mean length
+    const uint64_t items = d.slots * (s.heads / s.group), length = s.tokens / s.sequences + 1;
+    const uint64_t keys = s.window < length / 2 ? s.window : length / 2, steps = s.group * (keys / kTile + 2);
+    const uint64_t wanted = (512 + items - 1) / items;
+    d.splits = wanted < steps / 4 ? wanted : steps / 4;
+    if (d.splits < 1)
+        d.splits = 1;
+    return d;
+}
+
+// The workspace, each part from a multiple of 256 bytes: the rows' statistics,
+// the units, the bias' partial sums, the parts of dk and dv.
+struct Space {
+    uint64_t stats, units, partials, near, far, bytes;
+};
+
+Space space(const Shape& s, const Deal& d, uint32_t buckets, int dim)
+{
+    const uint64_t kv = s.heads / s.group, part = 2 * kOwn * uint64_t(dim) * 4;
+    uint64_t at = 0;
+    auto take = [&](uint64_t bytes) {
+        const uint64_t from = at;
+        at = (at + bytes + 255) / 256 * 256;
+        return from;
+    };
+    Space p;
+    p.stats = take(uint64_t(s.heads) * s.tokens * 8);
+    p.units = take(uint64_t(s.heads) * d.slots * kWaves * 4);
+    p.partials = take(uint64_t(s.heads) * d.slots * buckets * 4);
+    p.near = take(d.splits > 1 ? kv * d.slots * d.splits * part : d.far_slots ? kv * s.sequences * part : 0);
+    p.far = take(kv * d.far_slots * part);
+    p.bytes = at;
+    return p;
+}
+
+// Of the two forms of a call, with offsets and without.
+uint64_t workspace_need(const Shape& s, uint32_t buckets)
+{
+    const int dim = s.dim <= 64 ? 64 : 128;
+    const uint64_t a = space(s, deal(s, true), buckets, dim).bytes;
+    const uint64_t b = s.tokens % s.sequences ? 0 : space(s, deal(s, false), buckets, dim).bytes;
+    return a > b ? a : b;
 }
 
 template <typename T, int DIM, bool BIAS, bool DIRECT>
 int launch(const BwdArgs<T>& a, hipStream_t stream)
 {
-    auto blocks = [&](uint32_t heads) { return dim3(uint32_t((uint64_t(a.slots) * heads + 7) / 8 * 8)); };
-    hipLaunchKernelGGL((attention_dq_kernel<T, DIM, BIAS, DIRECT>), blocks(a.s.heads), dim3(kBlock), 0, stream, a);
-    const int rc = launch_status();
+    auto blocks = [](uint64_t items) { return dim3(uint32_t((items + 7) / 8 * 8)); };
+    const uint32_t kv = a.s.heads / a.s.group;
+    hipLaunchKernelGGL((attention_dq_kernel<T, DIM, BIAS, DIRECT>), blocks(uint64_t(a.slots) * a.s.heads), dim3(kBlock), 0, stream, a);
+    int rc = launch_status();
     if (rc)
         return rc;
-    hipLaunchKernelGGL((attention_dkv_kernel<T, DIM, BIAS, DIRECT>), blocks(a.s.heads / a.s.group), dim3(kBlock), 0, stream, a);
+    hipLaunchKernelGGL((attention_dkv_kernel<T, DIM, BIAS, DIRECT>), blocks((uint64_t(a.slots) * a.splits + a.far_slots) * kv), dim3(kBlock), 0,
+                       stream, a);
+    rc = launch_status();
+    if (rc || (a.splits == 1 && !a.far_slots))
+        return rc;
+    hipLaunchKernelGGL((dkv_sum_kernel<T, DIM>), dim3(a.slots * (kOwn / kSumRows), kv), dim3(kSumRows * DIM / 8), 0, stream, a);
     return launch_status();
 }
 
 template <typename T>
 int run(Heads<void> dq, Heads<void> dk, Heads<void> dv, Heads<const void> dout, Heads<const void> o, Heads<const void> q, Heads<const void> k,
         Heads<const void> v, const float* lse, const Shape& s, const Buckets& b, void* dbias, int grad_dtype, bool accumulate,
-        char* workspace, uint64_t rows, hipStream_t stream)
+        char* workspace, hipStream_t stream)
 {
     auto out = [](Heads<void> x) { return Heads<T>{static_cast<T*>(x.p), x.ld, x.hs}; };
     auto in = [](Heads<const void> x) { return Heads<const T>{static_cast<const T*>(x.p), x.ld, x.hs}; };
-    BwdArgs<T> a{out(dq), out(dk), out(dv), in(dout), in(o), in(q), in(k), in(v), lse, reinterpret_cast<float*>(workspace),
-                 reinterpret_cast<float*>(workspace + rows), dbias ? reinterpret_cast<float*>(workspace + 2 * rows) : nullptr, s, b, 0};
-    a.slots = uint32_t(slots_of(s.tokens, s.sequences, s.offsets != nullptr));
-    int rc;
+    const Deal d = deal(s, s.offsets != nullptr);
+    const Space p = space(s, d, b.count, s.dim <= 64 ? 64 : 128);
+    auto part = [&](uint64_t at) { return reinterpret_cast<float*>(workspace + at); };
+    const BwdArgs<T> a{out(dq), out(dk), out(dv), in(dout), in(o), in(q), in(k), in(v), lse, reinterpret_cast<f32x2*>(workspace + p.stats),
+                       part(p.units), dbias ? part(p.partials) : nullptr, part(p.near), part(p.far), s, b, uint32_t(d.slots), uint32_t(d.splits),
+                       uint32_t(d.far_slots)};
     auto go = [&](auto dim, auto way) {
         constexpr int kDim = decltype(dim)::value;
         constexpr bool kDirect = decltype(way)::value;
@@ -497,6 +665,7 @@ int run(Heads<void> dq, Heads<void> dk, Heads<void> dv, Heads<const void> dout, 
     };
     const std::integral_constant<int, 64> d64;
     const std::integral_constant<int, 128> d128;
+    int rc;
     if (direct_dim(s.dim) && direct(q.p, q.ld, q.hs) && direct(k.p, k.ld, k.hs) && direct(v.p, v.ld, v.hs) && direct(dout.p, dout.ld, dout.hs))
         rc = s.dim == 64 ? go(d64, std::true_type{}) : go(d128, std::true_type{});
     else
@@ -517,10 +686,16 @@ using namespace zero::attention;
 
 extern "C" size_t zero_attention_workspace_bytes(const zero_attention_t* params, uint64_t tokens, uint64_t sequences)
 {
-    if (!params || !tokens || !sequences || tokens > kMaxTokens || sequences > kMaxTokens || params->heads > kMaxHeads ||
-        params->buckets > ZERO_MAX_BUCKETS)
+    Shape s;
+    Buckets b;
+    if (!tokens || !sequences || !params)
         return 0;
-    return size_t(workspace_need(*params, tokens, sequences));
+    // the larger of a call with offsets and one without, where there is one; the pointers are only tested for NULL
+    const void* bias = params->buckets ? params : nullptr;
+    const int32_t* offsets = reinterpret_cast<const int32_t*>(params);
+    if (make_shape(params, tokens, offsets, sequences, ZERO_F16, bias, ZERO_F16, &s, &b))
+        return 0;
+    return size_t(workspace_need(s, b.count));
 }
 
 extern "C" int zero_attention_bwd(void* dq, uint64_t ld_dq, uint64_t hs_dq, void* dk, uint64_t ld_dk, uint64_t hs_dk, void* dv,
@@ -570,10 +745,9 @@ extern "C" int zero_attention_bwd(void* dq, uint64_t ld_dq, uint64_t hs_dq, void
         return ZERO_EINVAL;
     if (!is_aligned(workspace, 16))
         return ZERO_EALIGN;
-    if (workspace_bytes < workspace_need(*params, tokens, sequences))
+    if (workspace_bytes < workspace_need(s, b.count))
         return ZERO_ERANGE;
     const auto go = dtype == ZERO_F16 ? run<_Float16> : run<bf16>;
     return go({dq, ld_dq, hs_dq}, {dk, ld_dk, hs_dk}, {dv, ld_dv, hs_dv}, {dout, ld_dout, hs_dout}, {o, ld_o, hs_o}, {q, ld_q, hs_q},
-              {k, ld_k, hs_k}, {v, ld_v, hs_v}, lse, s, b, dbias, grad_dtype, accumulate != 0, static_cast<char*>(workspace),
-              rows_bytes(*params, tokens), st);
+              {k, ld_k, hs_k}, {v, ld_v, hs_v}, lse, s, b, dbias, grad_dtype, accumulate != 0, static_cast<char*>(workspace), st);
 }

@@ -22,24 +22,22 @@ struct FwdArgs {
     Heads<const T> q, k, v;
     Shape s;
     Buckets b;
-    uint32_t slots;
+    Order order;
 };
 
-template <typename T, int DIM, bool BIAS, bool DIRECT>
+template <typename T, int DIM, int BIAS, bool DIRECT>
 __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kernel(FwdArgs<T> a)
 {
     typedef Tile<DIM> L;
     __shared__ alignas(16) T keys[2][L::kElems];
     __shared__ alignas(16) T values[2][L::kElems];
-    __shared__ typename std::conditional<BIAS, BiasLds, int>::type bias;
+    __shared__ typename std::conditional<BIAS == kLine, BiasLine, int>::type bias;
+    extern __shared__ __attribute__((aligned(16))) float table[];               // BIAS == kTable: of table_size() distances
 
     const Shape& s = a.s;
-    const uint32_t work = die_local(blockIdx.x, gridDim.x);
-    if (work >= a.slots * s.heads)
-        return;
-    const uint32_t head = work / a.slots;
+    uint32_t head, slot;
     Piece at;
-    if (!find_piece(s, a.slots - 1 - (work - head * a.slots), kOwn, &at))      // a head's long rows first
+    if (!a.order.template find<true>(s, blockIdx.x, &head, &slot) || !find_piece(s, slot, kOwn, &at))
         return;
     const uint32_t lane = threadIdx.x & 63, c = lane % 32, h = lane / 32;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -56,21 +54,18 @@ __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kerne
     nv.fetch(values[0], vp, a.v.ld, t * kTile, at.len, s.dim);
     Operand<T, DIM> q;
     load_operand<T, DIM>(q, a.q.p + uint64_t(at.start) * a.q.ld + uint64_t(head) * a.q.hs, a.q.ld, row, s.dim);
-    if constexpr (BIAS) {
-        if (threadIdx.x < a.b.count) {
-            bias.value[threadIdx.x] = bias_value<T>(a.b, head, threadIdx.x) * kLog2e;
-            bias.starts[threadIdx.x] = a.b.starts[threadIdx.x];
-        }
+    float beyond = 0.0f;                           // kTable: the bias of the last bucket
+    if constexpr (BIAS == kTable) {
+        draw_table<T>(table, a.b, head);
+        beyond = bias_value<T>(a.b, head, a.b.count - 1) * kLog2e;
+    }
+    if constexpr (BIAS == kLine) {
+        load_line_values<T>(bias, a.b, head);
         __syncthreads();
     }
-
-    // a tile's bias: one value for each distance, from that of the farthest pair down
     auto draw_line = [&](uint32_t tile, int buf) {
-        if constexpr (BIAS)
-            if (threadIdx.x < kOwn + kTile - 1) {
-                const int d = int(at.first + kOwn - 1) - int(tile * kTile) - int(threadIdx.x);
-                bias.line[buf][threadIdx.x] = bias.value[bucket_of(bias.starts, a.b.count, d > 0 ? d : 0)];
-            }
+        if constexpr (BIAS == kLine)
+            bias.draw(buf, a.b.count, int(at.first + kOwn - 1) - int(tile * kTile), -1);
     };
 
     f32x16 acc[DIM / 32] = {};
@@ -94,19 +89,28 @@ __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kerne
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub)
                 x[sub] = rows_times<T, DIM>(keys[buf], places, sub, q);
-            if constexpr (BIAS)
+            // the scores are scores * factor + shift: where the bias is of one bucket it is the shift, else it is in them
+            float factor = s.scale2, shift = beyond;
+            if (BIAS == kLine || (BIAS == kTable && nearest(first, j0, kTile) < a.b.starts[a.b.count - 1])) {
+                const float* line = BIAS == kLine ? &bias_line(bias, buf)[kOwn - 1 - 32 * wave - c + 4 * h]
+                                                  : table + (int(mine) - int(j0) - (kTile - 1) + kTableBefore - 4 * int(h));
 #pragma unroll
                 for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        x[sub][r] = __builtin_fmaf(x[sub][r], s.scale2, bias.line[buf][kOwn - 1 - 32 * wave - c + 32 * sub + row_of(r, h)]);
+                    for (int r = 0; r < 16; ++r) {
+                        const int j = 32 * sub + row_of(r, 0);
+                        x[sub][r] = __builtin_fmaf(x[sub][r], s.scale2, line[BIAS == kLine ? j : kTile - 1 - j]);
+                    }
+                factor = 1.0f;
+                shift = 0.0f;
+            }
             if (see == kSome) {
-                const Limits limits(s, mine, j0 + 4 * h);
+                const Mask mask = Mask::keys(s, mine, j0 + 4 * h);
 #pragma unroll
                 for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        x[sub][r] = limits.sees(32 * sub + row_of(r, 0)) ? x[sub][r] : -INFINITY;
+                        x[sub][r] = mask.seen_or(x[sub][r], 0xff800000u, sub, r);      // -inf
             }
             float top = x[0][0];
 #pragma unroll
@@ -115,8 +119,7 @@ __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kerne
                 for (int r = 0; r < 16; ++r)
                     top = fmaxf(top, x[sub][r]);
             top = halves_max(top);
-            if constexpr (!BIAS)
-                top *= s.scale2;
+            top = __builtin_fmaf(top, factor, shift);
             // the sums go by the maximum so far until it has been passed by a factor of 2^8: they have the room, and most tiles
             // need not touch them
             if (__any(top > m + 8.0f)) {
@@ -129,12 +132,12 @@ __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kerne
                     for (int r = 0; r < 16; ++r)
                         acc[n][r] *= fall;
             }
-            const float base = m == -INFINITY ? 0.0f : m;
+            const float base = (m == -INFINITY ? 0.0f : m) - shift;
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    x[sub][r] = __builtin_amdgcn_exp2f(BIAS ? x[sub][r] - base : __builtin_fmaf(x[sub][r], s.scale2, -base));
+                    x[sub][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[sub][r], factor, -base));
                     sum += x[sub][r];
                 }
             // the weights are rounded to the element type, as the matrix instruction takes them: half a step of each, where the
@@ -161,11 +164,13 @@ __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kerne
 template <typename T, int DIM, bool DIRECT>
 int launch(const FwdArgs<T>& a, hipStream_t stream)
 {
-    const uint32_t blocks = uint32_t((uint64_t(a.slots) * a.s.heads + 7) / 8 * 8);
-    if (a.b.table)
-        hipLaunchKernelGGL((attention_fwd_kernel<T, DIM, true, DIRECT>), dim3(blocks), dim3(kBlock), 0, stream, a);
+    const uint32_t blocks = uint32_t(a.order.blocks(a.s));
+    if (!a.b.count)
+        hipLaunchKernelGGL((attention_fwd_kernel<T, DIM, kNoBias, DIRECT>), dim3(blocks), dim3(kBlock), 0, stream, a);
+    else if (table_fits(a.b))
+        hipLaunchKernelGGL((attention_fwd_kernel<T, DIM, kTable, DIRECT>), dim3(blocks), dim3(kBlock), table_size(a.b) * 4, stream, a);
     else
-        hipLaunchKernelGGL((attention_fwd_kernel<T, DIM, false, DIRECT>), dim3(blocks), dim3(kBlock), 0, stream, a);
+        hipLaunchKernelGGL((attention_fwd_kernel<T, DIM, kLine, DIRECT>), dim3(blocks), dim3(kBlock), 0, stream, a);
     return launch_status();
 }
 
@@ -223,7 +228,7 @@ int run_fwd(void* o, uint64_t ld_o, uint64_t hs_o, float* lse, const void* q, ui
             uint64_t hs_k, const void* v, uint64_t ld_v, uint64_t hs_v, const Shape& s, const Buckets& b, hipStream_t stream)
 {
     const FwdArgs<T> a{{static_cast<T*>(o), ld_o, hs_o}, lse, {static_cast<const T*>(q), ld_q, hs_q}, {static_cast<const T*>(k), ld_k, hs_k},
-                       {static_cast<const T*>(v), ld_v, hs_v}, s, b, uint32_t(slots_of(s.tokens, s.sequences, s.offsets != nullptr, kOwn))};
+                       {static_cast<const T*>(v), ld_v, hs_v}, s, b, Order(s, s.heads, slots_of(s.tokens, s.sequences, s.offsets != nullptr, kOwn))};
     if (direct_dim(s.dim) && direct(k, ld_k, hs_k) && direct(v, ld_v, hs_v))
         return s.dim == 64 ? launch<T, 64, true>(a, stream) : launch<T, 128, true>(a, stream);
     return s.dim <= 64 ? launch<T, 64, false>(a, stream) : launch<T, 128, false>(a, stream);

@@ -135,10 +135,44 @@ __device__ __forceinline__ bool find_piece(const Shape& s, uint32_t slot, uint32
     return slot >= out->slots && uint64_t(slot - out->slots) * own < out->len;
 }
 
-// Blocks go to the eight dies in turn; neighbours that share a head's keys
-// belong on one, whose L2 then holds them: the blocks of a die take a
-// contiguous part of the work.
-__device__ __forceinline__ uint32_t die_local(uint32_t block, uint32_t blocks) { return block % 8 * (blocks / 8) + block / 8; }
+// Which head and piece a block takes.  Blocks go to the eight dies in turn;
+// neighbours that share a head's keys belong on one, whose L2 then holds them.
+// Sequences of equal length: each die has its own (sequence, head) pairs and
+// takes all of their heaviest pieces first, so that light ones are left for
+// the end; with fewer than 64 pairs that are no multiple of 8 some dies would
+// have less to do.  Else a die takes a contiguous part of the list of heads and
+// slots.
+struct Order {
+    uint32_t heads, slots, pairs;                  // pairs: of a die, or 0
+
+    __host__ Order(const Shape& s, uint32_t h, uint64_t n) : heads(h), slots(uint32_t(n)), pairs(0)
+    {
+        const uint64_t all = uint64_t(h) * s.sequences;
+        if (!s.offsets && (all >= 64 || all % 8 == 0))
+            pairs = uint32_t((all + 7) / 8);
+    }
+    __host__ uint64_t blocks(const Shape& s) const
+    {
+        return pairs ? uint64_t(pairs) * 8 * (slots / s.sequences) : (uint64_t(heads) * slots + 7) / 8 * 8;
+    }
+    // LATE: the last rows of a sequence have the most work, else the first
+    template <bool LATE>
+    __device__ __forceinline__ bool find(const Shape& s, uint32_t block, uint32_t* head, uint32_t* slot) const
+    {
+        const uint32_t die = block % 8, i = block / 8;
+        if (pairs) {
+            const uint32_t per = (s.length + kOwn - 1) / kOwn, rank = i / pairs, pair = die * pairs + (i - rank * pairs), seq = pair / heads;
+            *head = pair - seq * heads;
+            *slot = seq * per + (LATE ? per - 1 - rank : rank);
+            return rank < per && seq < s.sequences;
+        }
+        const uint32_t work = die * ((heads * slots + 7) / 8) + i;
+        *head = work / slots;
+        const uint32_t rest = work - *head * slots;
+        *slot = LATE ? slots - 1 - rest : rest;
+        return i < (heads * slots + 7) / 8 && work < heads * slots;
+    }
+};
 
 // ---- visibility ------------------------------------------------------------------------
 // Position j is visible to i where j <= i and (i - j < window or j < sinks).
@@ -157,31 +191,47 @@ __device__ __forceinline__ Seen seen(const Shape& s, uint32_t i, uint32_t nq, ui
     return kSome;
 }
 
-// The same for single pairs, against one number a lane: of the keys j0 + j of a
-// tile, the lane's query sees those with j <= near, and j > far or j < first.
-struct Limits {
-    int near, far, first;
+// The same for single pairs: a bit for each of a lane's rows of a tile, two
+// words of 32 rows.  A select by one is two vector instructions and takes no
+// scalar registers, of which 32 comparisons would need 64.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 
-    __device__ __forceinline__ Limits(const Shape& s, uint32_t i, uint32_t j0)
+struct Mask {
+    uint32_t word[2];
+
+    // of the keys j0 + 4 h + row_of(r, 0), those that the query i sees
+    static __device__ __forceinline__ Mask keys(const Shape& s, uint32_t i, uint32_t j0)
     {
-        near = int(i) - int(j0);
-        far = s.window > i ? -1 - int(j0) : int(i - s.window) - int(j0);
-        first = s.sinks > j0 ? int(s.sinks - j0 < uint32_t(kTile) ? s.sinks - j0 : uint32_t(kTile)) : 0;
+        const int end = int(i) - int(j0) + 1;                      // keys below this are not behind the query
+        const int far = s.window > i ? -int(j0) : int(i - s.window) + 1 - int(j0);         // keys from this on are in the window
+        const int first = s.sinks > j0 ? int(s.sinks - j0 < uint32_t(kTile) ? s.sinks - j0 : uint32_t(kTile)) : 0;
+        Mask m;
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+            m.word[sub] = below(end - 32 * sub) & (~below(far - 32 * sub) | below(first - 32 * sub));
+        return m;
     }
-    __device__ __forceinline__ bool sees(int j) const { return (j <= near) & ((j > far) | (j < first)); }
-};
-
-// The other way round: of the queries i0 + i of a tile, those that see the lane's key j have i >= near and i < end.
-struct QueryLimits {
-    int near, end;
-
-    __device__ __forceinline__ QueryLimits(const Shape& s, uint32_t j, uint32_t i0, uint32_t len)
+    // of the queries i0 + 4 h + row_of(r, 0), those that see the key j
+    static __device__ __forceinline__ Mask queries(const Shape& s, uint32_t j, uint32_t i0, uint32_t len)
     {
-        near = int(j) - int(i0);
         const uint32_t last = j < s.sinks || s.window > len || j + s.window > len ? len : j + s.window;
-        end = int(last) - int(i0);
+        Mask m;
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+            m.word[sub] = below(int(last) - int(i0) - 32 * sub) & ~below(int(j) - int(i0) - 32 * sub);
+        return m;
     }
-    __device__ __forceinline__ bool sees(int i) const { return (i >= near) & (i < end); }
+    // all ones where register r of the product `sub` is seen
+    __device__ __forceinline__ uint32_t bits(int sub, int r) const { return uint32_t(__builtin_amdgcn_sbfe(int(sub ? word[1] : word[0]), row_of(r, 0), 1)); }
+    __device__ __forceinline__ float seen_or(float x, uint32_t other, int sub, int r) const
+    {
+        const uint32_t m = bits(sub, r);
+        return __builtin_bit_cast(float, (m & __builtin_bit_cast(uint32_t, x)) | (~m & other));
+    }
+    __device__ __forceinline__ float seen_or_0(float x, int sub, int r) const
+    {
+        return __builtin_bit_cast(float, bits(sub, r) & __builtin_bit_cast(uint32_t, x));
+    }
 };
 
 // The key tiles that some query of [i, i + nq) sees, in order: those of the
@@ -204,16 +254,16 @@ struct KeyTiles {
 };
 
 // ---- tiles in LDS ---------------------------------------------------------------------
-// kTile rows of DIM elements in 16-byte pieces.  The pieces of a row are
+// ROWS rows of DIM elements in 16-byte pieces.  The pieces of a row are
 // permuted by the row, so that both ways to read a tile spread over the 64
 // banks: 16 bytes of one column place in consecutive rows (operand A as rows),
 // and 8-byte parts of 4 rows that the transposing read turns (operand A as
 // columns).
-template <int DIM>
+template <int DIM, int ROWS = kTile>
 struct Tile {
     static constexpr int kPieces = DIM / 8;        // a row
-    static constexpr int kPerThread = kTile * kPieces / kBlock;
-    static constexpr int kElems = kTile * DIM;
+    static constexpr int kPerThread = ROWS * kPieces / kBlock;
+    static constexpr int kElems = ROWS * DIM;
 
     static __device__ __forceinline__ uint32_t twist(uint32_t row)
     {
@@ -230,14 +280,14 @@ struct Tile {
 // it needs 16-byte aligned rows of DIM elements.  Else through registers.
 // Rows past the sequence's end repeat its last one (what they give is masked);
 // columns past `dim` are 0.
-template <typename T, int DIM, bool DIRECT>
+template <typename T, int DIM, bool DIRECT, int ROWS = kTile>
 class Carrier;
 
-template <typename T, int DIM>
-class Carrier<T, DIM, false> {
+template <typename T, int DIM, int ROWS>
+class Carrier<T, DIM, false, ROWS> {
     typedef typename Vec8<T>::type V;
     typedef V __attribute__((aligned(sizeof(T)))) VU;
-    typedef Tile<DIM> L;
+    typedef Tile<DIM, ROWS> L;
     V v[L::kPerThread];
 
 public:
@@ -264,9 +314,9 @@ public:
     }
 };
 
-template <typename T, int DIM>
-class Carrier<T, DIM, true> {
-    typedef Tile<DIM> L;
+template <typename T, int DIM, int ROWS>
+class Carrier<T, DIM, true, ROWS> {
+    typedef Tile<DIM, ROWS> L;
     static constexpr uint32_t kRows = kBlock / L::kPieces;         // of one round; the permutation of a row repeats after it
     static_assert(kRows % 16 == 0, "rows of a round");
 
@@ -280,7 +330,7 @@ public:
         const uint32_t to = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) T*)tile)) + wave * 1024;
         const T* from = head + row0 * ld;
         const uint32_t step = uint32_t(ld) * sizeof(T), last = len - 1 - row0;      // ld is below 2^24
-        if (last >= uint32_t(kTile) - 1) {
+        if (last >= uint32_t(ROWS) - 1) {
             const uint32_t at = row * step + col * uint32_t(sizeof(T));
 #pragma unroll
             for (int i = 0; i < L::kPerThread; ++i)
@@ -367,6 +417,18 @@ __device__ __forceinline__ f32x16 rows_times(const T* tile, const Places<DIM>& a
     return c;
 }
 
+// The same with 32 rows of another tile as the operand.
+template <typename T, int DIM>
+__device__ __forceinline__ f32x16 rows_times_rows(const T* tile, const T* other, const Places<DIM>& at)
+{
+    typedef typename Vec8<T>::type V;
+    f32x16 c = {};
+#pragma unroll
+    for (int k = 0; k < DIM / 16; ++k)
+        c = Vec8<T>::mfma(*reinterpret_cast<const V*>(tile + (at.row ^ (16 * k))), *reinterpret_cast<const V*>(other + (at.row ^ (16 * k))), c);
+    return c;
+}
+
 template <typename T>
 __device__ __forceinline__ typename Vec8<T>::type column_pair(const T* a, const T* b)
 {
@@ -376,16 +438,39 @@ __device__ __forceinline__ typename Vec8<T>::type column_pair(const T* a, const 
     return __builtin_bit_cast(typename Vec8<T>::type, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// acc[n] += (rows 16 step .. 16 step + 15 of the tile, columns 32 n .. 32 n + 31)^T x p, where p holds
-// 16 rows in the order that a score's registers give.
+// Operands A for 16 rows of the tile (from 16 step on) as columns: their
+// elements 32 n .. 32 n + 31 each, the rows in the order that a score's
+// registers give them as an operand B.
 template <typename T, int DIM>
-__device__ __forceinline__ void columns_times(f32x16 (&acc)[DIM / 32], const T* tile, const Places<DIM>& at, int step,
-                                              typename Vec8<T>::type p)
+struct Columns {
+    typename Vec8<T>::type v[DIM / 32];
+};
+
+template <typename T, int DIM>
+__device__ __forceinline__ void read_columns(Columns<T, DIM>& a, const T* tile, const Places<DIM>& at, int step)
 {
     const T* rows = tile + 16 * DIM * step;
 #pragma unroll
     for (int n = 0; n < DIM / 32; ++n)
-        acc[n] = Vec8<T>::mfma(column_pair<T>(rows + (at.col ^ (32 * n)), rows + (at.col8 ^ (32 * n))), p, acc[n]);
+        a.v[n] = column_pair<T>(rows + (at.col ^ (32 * n)), rows + (at.col8 ^ (32 * n)));
+}
+
+// acc[n] += (columns of those rows)^T x p
+template <typename T, int DIM>
+__device__ __forceinline__ void columns_times(f32x16 (&acc)[DIM / 32], const Columns<T, DIM>& a, typename Vec8<T>::type p)
+{
+#pragma unroll
+    for (int n = 0; n < DIM / 32; ++n)
+        acc[n] = Vec8<T>::mfma(a.v[n], p, acc[n]);
+}
+
+template <typename T, int DIM>
+__device__ __forceinline__ void columns_times(f32x16 (&acc)[DIM / 32], const T* tile, const Places<DIM>& at, int step,
+                                              typename Vec8<T>::type p)
+{
+    Columns<T, DIM> a;
+    read_columns<T, DIM>(a, tile, at, step);
+    columns_times<T, DIM>(acc, a, p);
 }
 
 // Registers 8 half .. 8 half + 7, rounded to nearest even.
@@ -474,13 +559,57 @@ __device__ __forceinline__ float bias_value(const Buckets& b, uint32_t head, uin
     return b.f32 ? static_cast<const float*>(b.table)[at] : float(static_cast<const T*>(b.table)[at]);
 }
 
-// The bias in LDS: the head's table times log2(e), the buckets' borders, and of
-// the present tile one value for each distance between its rows and keys.
-struct BiasLds {
-    float value[ZERO_MAX_BUCKETS];
+// How a kernel has the bias (template parameter).  kTable: a value for each
+// distance in LDS, up to where every pair of a tile is in the last bucket, whose
+// bias is then one number.  kLine: where the last bucket begins too far out for
+// that, a line of values for each tile, searched for in the buckets.
+enum { kNoBias, kTable, kLine };
+
+// The table: the distance d at d + kTableBefore.  A tile that is not wholly in
+// the last bucket reaches from 94 before distance 0 to 190 past where that begins.
+constexpr int kTableBefore = 96, kTableBeyond = 192;
+constexpr uint32_t kTableMost = 1024;              // LDS for two workgroups a CU beside tiles of 64 columns, one of 128
+
+__host__ __device__ inline bool table_fits(const Buckets& b) { return b.starts[b.count - 1] <= kTableMost; }
+__host__ __device__ inline uint32_t table_size(const Buckets& b) { return b.starts[b.count - 1] + kTableBefore + kTableBeyond; }
+
+// The least distance between the rows from i on and nk keys from j on.
+__device__ __forceinline__ uint32_t nearest(uint32_t i, uint32_t j, uint32_t nk) { return i > j + nk - 1 ? i - (j + nk - 1) : 0; }
+
+template <typename T>
+__device__ __forceinline__ void draw_table(float* table, const Buckets& b, uint32_t head)
+{
+    for (uint32_t x = threadIdx.x; x < table_size(b); x += kBlock) {
+        const int d = int(x) - kTableBefore;
+        table[x] = bias_value<T>(b, head, bucket_of(b.starts, b.count, d > 0 ? d : 0)) * kLog2e;
+    }
+}
+
+struct BiasLine {
+    float value[ZERO_MAX_BUCKETS];                 // the head's bias times log2(e)
     uint32_t starts[ZERO_MAX_BUCKETS];
-    float line[2][kOwn + kTile];                   // line[x]: the distance far - x
+    float line[2][kOwn + kTile];
+
+    // line[x]: the distance `from` + x step
+    __device__ __forceinline__ void draw(int buf, uint32_t count, int from, int step)
+    {
+        if (threadIdx.x < kOwn + kTile - 1) {
+            const int d = from + step * int(threadIdx.x);
+            line[buf][threadIdx.x] = value[bucket_of(starts, count, d > 0 ? d : 0)];
+        }
+    }
 };
+__device__ __forceinline__ const float* bias_line(const BiasLine& b, int buf) { return b.line[buf]; }
+__device__ __forceinline__ const float* bias_line(int, int) { return nullptr; }
+
+template <typename T>
+__device__ __forceinline__ void load_line_values(BiasLine& line, const Buckets& b, uint32_t head)
+{
+    if (threadIdx.x < b.count) {
+        line.value[threadIdx.x] = bias_value<T>(b, head, threadIdx.x) * kLog2e;
+        line.starts[threadIdx.x] = b.starts[threadIdx.x];
+    }
+}
 
 // ---- host side --------------------------------------------------------------------------
 constexpr uint64_t kMaxTokens = uint64_t(1) << 30;

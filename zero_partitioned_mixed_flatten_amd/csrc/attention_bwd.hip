@@ -39,6 +39,7 @@ struct BwdArgs {
     Shape s;
     Buckets b;
     uint32_t slots, splits, far_slots;
+    Order queries, keys;                           // of the two passes
 };
 
 struct BinsLds {
@@ -50,9 +51,52 @@ __device__ __forceinline__ float lane_value(float v, uint32_t from)
     return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(int(from * 4), __builtin_bit_cast(int, v)));
 }
 
+// The sums by distance of a wave (kTable): the distance d at d + kTableBefore.
+__host__ __device__ inline uint32_t sums_size(const Buckets& b) { return b.starts[b.count - 1] + 2 * kTableBefore; }
+
+// They are formed from kSkewRows rows (keys) of a product at a time, written so
+// that the elements of one distance are neighbours: element (row, c) at
+// (c - row + kSkewRows - 1) * kSkewPitch + row, what no element goes to stays 0.
+// Then a lane takes a distance.  Atomic additions in LDS, a distance a lane,
+// took longer than the products (bias_bwd at 8 x 1024, 25 heads: 313 us against
+// 196 for lane permutes of each register).
+template <int DIM>
+constexpr int kSkewRows = DIM == 64 ? 32 : 8;      // 36 KB a workgroup, or 7.5: LDS for two workgroups a CU
+template <int DIM>
+constexpr int kSkewPitch = kSkewRows<DIM> + 4;
+template <int DIM>
+constexpr int kSkewSize = (31 + kSkewRows<DIM>) * kSkewPitch<DIM>;
+
+// ds[r] of lane (c, h): the pair at distance base + c - row_of(r, h).
+template <int DIM>
+__device__ __forceinline__ void add_distances(float* skew, float* sums, int base, f32x16 ds, float back)
+{
+    constexpr int kR = kSkewRows<DIM>, kP = kSkewPitch<DIM>, kLast = kR - 5;
+    const int lane = threadIdx.x & 63, c = lane % 32, h = lane / 32;
+    float* to = skew + (c + kR - 1) * kP - (kLast + 4 * h) * (kP - 1);
+#pragma unroll
+    for (int pass = 0; pass < 32 / kR; ++pass) {
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int r = 0; r < kR / 2; ++r)
+            to[(kLast - row_of(r, 0)) * (kP - 1)] = ds[kR / 2 * pass + r] * back;
+        // the wave's LDS operations are done in order: its writes are there
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (lane < 31 + kR) {
+            f32x4 v = *reinterpret_cast<const f32x4*>(skew + lane * kP);
+#pragma unroll
+            for (int i = 1; i < kR / 4; ++i)
+                v += *reinterpret_cast<const f32x4*>(skew + lane * kP + 4 * i);
+            sums[base - kR * pass + lane - (kR - 1) + kTableBefore] += (v[0] + v[1]) + (v[2] + v[3]);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
 // bins[bucket] += the sums of ds along the distances of a 32 x 32 product
 // whose rows are keys: ds[r] of lane (c, h) is the pair at distance base + c - row_of(r, h).
-__device__ __forceinline__ void add_diagonals(float* bins, const BiasLds& bias, uint32_t count, int base, const float (&ds)[16])
+__device__ __forceinline__ void add_diagonals(float* bins, const BiasLine& bias, uint32_t count, int base, const float (&ds)[16])
 {
     const uint32_t lane = threadIdx.x & 63;        // takes the distance base + lane - 31
     float sum = 0.0f;
@@ -78,24 +122,29 @@ __device__ __forceinline__ void add_diagonals(float* bins, const BiasLds& bias, 
     if (lane == 63 || after != bucket)
         bins[bucket] += sum;
 }
+__device__ __forceinline__ void add_diagonals_of(const BiasLine& bias, float* bins, uint32_t count, int base, const float (&ds)[16])
+{
+    add_diagonals(bins, bias, count, base, ds);
+}
+__device__ __forceinline__ void add_diagonals_of(int, float*, uint32_t, int, const float (&)[16]) {}
 
-template <typename T, int DIM, bool BIAS, bool DIRECT>
+template <typename T, int DIM, int BIAS, bool DIRECT>
 __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
 {
     typedef Tile<DIM> L;
     __shared__ alignas(16) T keys[2][L::kElems];
     __shared__ alignas(16) T values[2][L::kElems];
-    __shared__ typename std::conditional<BIAS, BiasLds, int>::type bias;
-    __shared__ typename std::conditional<BIAS, BinsLds, int>::type sums;
+    __shared__ typename std::conditional<BIAS == kLine, BiasLine, int>::type bias;
+    __shared__ typename std::conditional<BIAS != kNoBias, BinsLds, int>::type sums;
+    extern __shared__ __attribute__((aligned(16))) float table[];               // BIAS == kTable: the waves' skewed rows, the table, the waves' sums by distance
 
     const Shape& s = a.s;
-    const uint32_t work = die_local(blockIdx.x, gridDim.x);
-    if (work >= a.slots * s.heads)
-        return;
-    const uint32_t head = work / a.slots, slot = a.slots - 1 - (work - head * a.slots);
+    uint32_t head, slot;
     Piece at;
+    if (!a.queries.template find<true>(s, blockIdx.x, &head, &slot))
+        return;
     if (!find_piece(s, slot, kOwn, &at)) {
-        if (BIAS && a.partials && threadIdx.x < a.b.count)
+        if (BIAS != kNoBias && a.partials && threadIdx.x < a.b.count)
             a.partials[(uint64_t(head) * a.slots + slot) * a.b.count + threadIdx.x] = 0.0f;
         return;
     }
@@ -147,32 +196,31 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
         a.stats[stat] = f32x2{lse - (kUnits<T> ? kWeightShift : 0.0f), delta};
     delta *= unit;
 
-    if constexpr (BIAS) {
-        if (threadIdx.x < a.b.count) {
-            bias.value[threadIdx.x] = bias_value<T>(a.b, head, threadIdx.x) * kLog2e;
-            bias.starts[threadIdx.x] = a.b.starts[threadIdx.x];
-        }
+    float beyond = 0.0f;                           // kTable: the bias of the last bucket
+    float* const skew = table + wave * kSkewSize<DIM>;                     // the wave's
+    float* const line = table + kWaves * kSkewSize<DIM>;
+    float* const by_distance = line + (BIAS == kTable ? table_size(a.b) + wave * sums_size(a.b) : 0);
+    const uint32_t last_start = BIAS == kTable ? a.b.starts[a.b.count - 1] : 0;
+    if constexpr (BIAS == kTable) {
+        draw_table<T>(line, a.b, head);
+        beyond = bias_value<T>(a.b, head, a.b.count - 1) * kLog2e;
+        for (uint32_t x = lane; x < sums_size(a.b); x += 64)
+            by_distance[x] = 0.0f;
+        for (uint32_t x = lane; x < kSkewSize<DIM>; x += 64)
+            skew[x] = 0.0f;
+    }
+    if constexpr (BIAS == kLine) {
+        load_line_values<T>(bias, a.b, head);
         for (uint32_t i = threadIdx.x; i < kWaves * ZERO_MAX_BUCKETS; i += kBlock)
             sums.bins[i / ZERO_MAX_BUCKETS][i % ZERO_MAX_BUCKETS] = 0.0f;
         __syncthreads();
     }
     auto draw_line = [&](uint32_t tile, int buf) {
-        if constexpr (BIAS)
-            if (threadIdx.x < kOwn + kTile - 1) {
-                const int d = int(at.first + kOwn - 1) - int(tile * kTile) - int(threadIdx.x);
-                bias.line[buf][threadIdx.x] = bias.value[bucket_of(bias.starts, a.b.count, d > 0 ? d : 0)];
-            }
+        if constexpr (BIAS == kLine)
+            bias.draw(buf, a.b.count, int(at.first + kOwn - 1) - int(tile * kTile), -1);
     };
-    float even = 0.0f;                             // ds of tiles whose distances share a bucket
-    uint32_t even_bucket = 0;
-    auto settle_even = [&] {
-        if constexpr (BIAS) {
-            const float v = layer::lanes_sum<64>(even);
-            if (lane == 0)
-                sums.bins[wave][even_bucket] += v;
-            even = 0.0f;
-        }
-    };
+    float far_sum = 0.0f;                          // ds of tiles whose distances are all in the last bucket
+    const float back = live ? 1.0f / unit : 0.0f;  // a power of two: exact
 
     f32x16 acc[DIM / 32] = {};
     nk.put(keys[0]);
@@ -190,18 +238,9 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
         const uint32_t j0 = t * kTile;
         const Seen see = seen(s, first, 32, j0, kTile);
         if (see != kNone) {
-            const Limits limits(s, mine, j0 + 4 * h);
-            bool one_bucket = false;
-            if constexpr (BIAS)
-                if (a.partials) {
-                    const uint32_t near = first > j0 + kTile - 1 ? first - (j0 + kTile - 1) : 0, far = first + 31 - j0;
-                    const uint32_t b0 = __builtin_amdgcn_readfirstlane(bucket_of(bias.starts, a.b.count, near));
-                    one_bucket = b0 == uint32_t(__builtin_amdgcn_readfirstlane(bucket_of(bias.starts, a.b.count, far)));
-                    if (one_bucket && b0 != even_bucket) {
-                        settle_even();
-                        even_bucket = b0;
-                    }
-                }
+            const bool apart = BIAS == kLine || (BIAS == kTable && nearest(first, j0, kTile) < last_start);
+            const float row_shift = apart ? lse : lse - beyond;
+            const int line_at = int(mine) - int(j0) - (kTile - 1) + kTableBefore - 4 * int(h);
 #pragma unroll DIM == 64 ? 2 : 1
             for (int sub = 0; sub < 2; ++sub) {
                 if (DIM == 128)
@@ -209,33 +248,42 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
                 const f32x16 x = rows_times<T, DIM>(keys[buf], places, sub, q);
                 const f32x16 dp = rows_times<T, DIM>(values[buf], places, sub, dout);
                 f32x16 ds;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const uint32_t j = 32 * sub + row_of(r, h);
-                    float v = __builtin_fmaf(x[r], s.scale2, -lse);
-                    if constexpr (BIAS)
-                        v += bias.line[buf][kOwn - 1 - 32 * wave - c + j];
-                    ds[r] = __builtin_amdgcn_exp2f(v) * __builtin_fmaf(dp[r], unit, -delta);
-                }
-                if (see == kSome)
+                if (apart) {
+                    const float* b = BIAS == kLine ? &bias_line(bias, buf)[kOwn - 1 - 32 * wave - c + 4 * h + 32 * sub]
+                                                   : line + line_at - 32 * sub;
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        ds[r] = limits.sees(32 * sub + row_of(r, 0)) ? ds[r] : 0.0f;
-                if constexpr (BIAS)
+                        ds[r] = __builtin_fmaf(x[r], s.scale2, b[BIAS == kLine ? row_of(r, 0) : kTile - 1 - row_of(r, 0)] - row_shift);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        ds[r] = __builtin_fmaf(x[r], s.scale2, -row_shift);
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    ds[r] = __builtin_amdgcn_exp2f(ds[r]) * __builtin_fmaf(dp[r], unit, -delta);
+                if (see == kSome) {
+                    const Mask mask = Mask::keys(s, mine, j0 + 4 * h);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        ds[r] = mask.seen_or_0(ds[r], sub, r);
+                }
+                if constexpr (BIAS != kNoBias)
                     if (a.partials) {
-                        const float back = live ? 1.0f / unit : 0.0f;        // a power of two: exact
-                        if (one_bucket) {
+                        if (BIAS == kLine) {
+                            float w[16];
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                w[r] = ds[r] * back;
+                            add_diagonals_of(bias, sums.bins[wave], a.b.count, int(first) - int(j0) - 32 * sub, w);
+                        } else if (apart) {
+                            add_distances<DIM>(skew, by_distance, int(first) - int(j0) - 32 * sub, ds, back);
+                        } else {
                             float v = 0.0f;
 #pragma unroll
                             for (int r = 0; r < 16; ++r)
                                 v += ds[r];
-                            even += live ? v * back : 0.0f;
-                        } else {
-                            float w[16];
-#pragma unroll
-                            for (int r = 0; r < 16; ++r)
-                                w[r] = live ? ds[r] * back : 0.0f;
-                            add_diagonals(sums.bins[wave], bias, a.b.count, int(first) - int(j0) - 32 * sub, w);
+                            far_sum = __builtin_fmaf(v, back, far_sum);
                         }
                     }
 #pragma unroll
@@ -253,15 +301,43 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
     }
     store_columns<T, DIM>(a.dq.p + uint64_t(at.start) * a.dq.ld + uint64_t(head) * a.dq.hs, a.dq.ld, mine, live, s.dim, acc,
                           s.scale / unit);
-    if constexpr (BIAS)
+    if constexpr (BIAS == kLine)
         if (a.partials) {
-            settle_even();
             __syncthreads();
             if (threadIdx.x < a.b.count) {
                 float v = 0.0f;
                 for (int w = 0; w < kWaves; ++w)
                     v += sums.bins[w][threadIdx.x];
                 a.partials[(uint64_t(head) * a.slots + slot) * a.b.count + threadIdx.x] = v;
+            }
+        }
+    if constexpr (BIAS == kTable)
+        if (a.partials) {
+            far_sum = layer::lanes_sum<64>(far_sum);
+            if (lane == 0)
+                sums.bins[wave][0] = far_sum;
+            __syncthreads();
+            // the waves' sums of each distance, then each bucket's distances: a wave a bucket
+            const uint32_t size = sums_size(a.b);
+            float* all = line + table_size(a.b);
+            for (uint32_t x = threadIdx.x; x < size; x += kBlock) {
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w)
+                    v += all[w * size + x];
+                all[x] = v;
+            }
+            __syncthreads();
+            for (uint32_t b = wave; b < a.b.count; b += kWaves) {
+                const uint32_t from = a.b.starts[b] + kTableBefore, to = b + 1 < a.b.count ? a.b.starts[b + 1] + kTableBefore : size;
+                float v = 0.0f;
+                for (uint32_t x = from + lane; x < to; x += 64)
+                    v += all[x];
+                v = layer::lanes_sum<64>(v);
+                if (b + 1 == a.b.count)
+                    v += (sums.bins[0][0] + sums.bins[1][0]) + (sums.bins[2][0] + sums.bins[3][0]);
+                if (lane == 0)
+                    a.partials[(uint64_t(head) * a.slots + slot) * a.b.count + b] = v;
             }
         }
 }
@@ -278,8 +354,15 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
 //     their own, whose sums are added likewise.
 constexpr uint32_t kFar = 1024;
 
+// Rows of the tiles of queries.  A wave has its keys, and 64 columns take 32
+// registers of each of dk and dv, 128 columns 64: then the values are read from
+// LDS instead (two workgroups a CU have 80 KB each, so tiles are half as long).
+template <int DIM>
+constexpr int kRows = DIM == 64 ? kTile : 32;
+
+template <int DIM>
 struct RowStats {
-    float lse[kTile], delta[kTile];
+    float lse[kRows<DIM>], delta[kRows<DIM>];
 };
 
 // Whether the queries behind the window are taken apart: where the first tokens are in one piece.
@@ -292,50 +375,54 @@ __device__ __forceinline__ uint32_t near_end(const Shape& s, uint32_t first, uin
     return bounded && len - first > kOwn - 1 && len - first - (kOwn - 1) > s.window ? first + (kOwn - 1) + s.window : len;
 }
 
-template <typename T, int DIM, bool BIAS, bool DIRECT>
+template <typename T, int DIM, int BIAS, bool DIRECT>
 __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
 {
-    typedef Tile<DIM> L;
+    constexpr int kQ = kRows<DIM>;
+    constexpr bool kValuesInLds = DIM == 128;
+    typedef Tile<DIM, kQ> L;
     __shared__ alignas(16) T queries[2][L::kElems];
     __shared__ alignas(16) T douts[2][L::kElems];
-    __shared__ alignas(16) RowStats stats[2];
-    __shared__ typename std::conditional<BIAS, BiasLds, int>::type bias;
+    __shared__ alignas(16) T values[kValuesInLds ? Tile<DIM, kOwn>::kElems : 8];
+    __shared__ alignas(16) RowStats<DIM> stats[2];
+    __shared__ typename std::conditional<BIAS == kLine, BiasLine, int>::type bias;
+    extern __shared__ __attribute__((aligned(16))) float table[];               // BIAS == kTable: of table_size() distances
 
     const Shape& s = a.s;
     const uint32_t kv_heads = s.heads / s.group;
-    const uint32_t far_items = a.far_slots * kv_heads, near_items = a.slots * kv_heads * a.splits;
-    uint32_t work = die_local(blockIdx.x, gridDim.x);
-    if (work >= far_items + near_items)
-        return;
-    const bool is_far = work < far_items;
+    // the far items first, then the pieces' lists (of one part), or their parts
+    const uint32_t far_items = a.far_slots * kv_heads, block = blockIdx.x - far_items;
+    const bool is_far = blockIdx.x < far_items;
     Piece at;
-    uint32_t kv, part = 0, begin, end, first_key;
+    uint32_t kv, slot, part = 0, begin, end, first_key;
     float* out = nullptr;                          // binary32 sums: dk of the piece's rows, then dv; NULL: dk and dv themselves
     if (is_far) {
-        kv = work / a.far_slots;
-        const uint32_t slot = work - kv * a.far_slots;
-        if (!find_piece(s, slot, kFar, &at))
+        kv = blockIdx.x / a.far_slots;
+        if (!find_piece(s, blockIdx.x - kv * a.far_slots, kFar, &at))
             return;
         first_key = 0;
-        begin = (near_end(s, 0, at.len) + kTile - 1) / kTile;
+        begin = (near_end(s, 0, at.len) + kQ - 1) / kQ;
         const uint32_t stop = at.first + kFar < at.len ? at.first + kFar : at.len;
-        begin = begin > at.first / kTile ? begin : at.first / kTile;
-        end = (stop + kTile - 1) / kTile;
+        begin = begin > at.first / kQ ? begin : at.first / kQ;
+        end = (stop + kQ - 1) / kQ;
         if (begin >= end)
             return;
-        out = a.far + uint64_t(work) * (2 * kOwn * DIM);
+        out = a.far + uint64_t(blockIdx.x) * (2 * kOwn * DIM);
     } else {
-        work -= far_items;
-        kv = work / (a.slots * a.splits);
-        const uint32_t rest = work - kv * (a.slots * a.splits), slot = rest / a.splits;
-        part = rest - slot * a.splits;
-        if (!find_piece(s, slot, kOwn, &at))       // the first keys have the most queries
+        if (a.splits > 1) {
+            part = block % a.splits;
+            kv = block / a.splits / a.slots;
+            slot = block / a.splits - kv * a.slots;
+        } else if (!a.keys.template find<false>(s, block, &kv, &slot)) {
+            return;
+        }
+        if (!find_piece(s, slot, kOwn, &at))
             return;
         first_key = at.first;
-        begin = at.first / kTile;
-        end = (near_end(s, at.first, at.len) + kTile - 1) / kTile;
+        begin = at.first / kQ;
+        end = (near_end(s, at.first, at.len) + kQ - 1) / kQ;
         if (a.splits > 1)
-            out = a.near + uint64_t(work) * (2 * kOwn * DIM);
+            out = a.near + uint64_t(block) * (2 * kOwn * DIM);
         else if (a.far_slots && at.first == 0)
             out = a.near + (uint64_t(kv) * s.sequences + at.seq) * (2 * kOwn * DIM);
     }
@@ -346,7 +433,14 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
     Places<DIM> places;
     Operand<T, DIM> k, v;
     load_operand<T, DIM>(k, a.k.p + uint64_t(at.start) * a.k.ld + uint64_t(kv) * a.k.hs, a.k.ld, row, s.dim);
-    load_operand<T, DIM>(v, a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(kv) * a.v.hs, a.v.ld, row, s.dim);
+    const T* vp = a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(kv) * a.v.hs;
+    if (kValuesInLds) {
+        Carrier<T, DIM, DIRECT, kOwn> nv;
+        nv.fetch(values, vp, a.v.ld, first_key, at.len, s.dim);
+        nv.put(values);
+    } else {
+        load_operand<T, DIM>(v, vp, a.v.ld, row, s.dim);
+    }
 
     const uint32_t tiles = end - begin, steps = tiles * s.group;
     uint32_t step = is_far ? 0 : uint32_t(uint64_t(steps) * part / a.splits);
@@ -354,45 +448,46 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
     uint32_t head = step / tiles, t = begin + step - head * tiles;
     head += kv * s.group;
 
-    Carrier<T, DIM, DIRECT> nq, ndo;
+    Carrier<T, DIM, DIRECT, kQ> nq, ndo;
     f32x2 nstat = {};
     float nunit = 0.0f, tile_unit = 0.0f;
     // the sequence's first slot among the dq kernel's, which wrote the units
     const uint32_t unit_slots = s.offsets ? at.start / kOwn + at.seq : at.seq * ((s.length + kOwn - 1) / kOwn);
     auto ask = [&](int buf, uint32_t hd, uint32_t tile) {
-        if (threadIdx.x < kTile) {
-            const uint32_t i = tile * kTile + threadIdx.x;
+        if (threadIdx.x < kQ) {
+            const uint32_t i = tile * kQ + threadIdx.x;
             nstat = a.stats[uint64_t(hd) * s.tokens + at.start + (i < at.len ? i : at.len - 1)];
         }
         if (kUnits<T>) {
-            const float* u = a.units + (uint64_t(hd) * a.slots + unit_slots) * kWaves + 2 * tile;
-            nunit = fminf(u[0], u[1]);
+            const float* u = a.units + (uint64_t(hd) * a.slots + unit_slots) * kWaves + kQ / 32 * tile;
+            nunit = kQ == 64 ? fminf(u[0], u[1]) : u[0];
         }
-        nq.fetch(queries[buf], a.q.p + uint64_t(at.start) * a.q.ld + uint64_t(hd) * a.q.hs, a.q.ld, tile * kTile, at.len, s.dim);
-        ndo.fetch(douts[buf], a.dout.p + uint64_t(at.start) * a.dout.ld + uint64_t(hd) * a.dout.hs, a.dout.ld, tile * kTile, at.len, s.dim);
+        nq.fetch(queries[buf], a.q.p + uint64_t(at.start) * a.q.ld + uint64_t(hd) * a.q.hs, a.q.ld, tile * kQ, at.len, s.dim);
+        ndo.fetch(douts[buf], a.dout.p + uint64_t(at.start) * a.dout.ld + uint64_t(hd) * a.dout.hs, a.dout.ld, tile * kQ, at.len, s.dim);
     };
+    float beyond = 0.0f;                           // kTable: the bias of the last bucket
     auto load_bias = [&](uint32_t hd) {
-        if constexpr (BIAS)
-            if (threadIdx.x < a.b.count)
-                bias.value[threadIdx.x] = bias_value<T>(a.b, hd, threadIdx.x) * kLog2e;
+        if constexpr (BIAS == kLine)
+            load_line_values<T>(bias, a.b, hd);
+        if constexpr (BIAS == kTable) {
+            draw_table<T>(table, a.b, hd);
+            beyond = bias_value<T>(a.b, hd, a.b.count - 1) * kLog2e;
+        }
     };
+    // whether every pair of the piece's keys and a tile's queries is in the last bucket
+    auto all_beyond = [&](uint32_t tile) { return BIAS == kTable && nearest(tile * kQ, first_key, kOwn) >= a.b.starts[a.b.count - 1]; };
     auto place = [&](int buf, uint32_t tile) {
         nq.put(queries[buf]);
         ndo.put(douts[buf]);
-        if (threadIdx.x < kTile) {
-            stats[buf].lse[threadIdx.x] = nstat[0];
+        if (threadIdx.x < kQ) {
+            stats[buf].lse[threadIdx.x] = all_beyond(tile) ? nstat[0] - beyond : nstat[0];
             stats[buf].delta[threadIdx.x] = nstat[1];
         }
         tile_unit = nunit;
-        if constexpr (BIAS)
-            if (threadIdx.x < kOwn + kTile - 1) {
-                const int d = int(tile * kTile) - int(first_key + kOwn - 1) + int(threadIdx.x);
-                bias.line[buf][threadIdx.x] = bias.value[bucket_of(bias.starts, a.b.count, d > 0 ? d : 0)];
-            }
+        if constexpr (BIAS == kLine)
+            bias.draw(buf, a.b.count, int(tile * kQ) - int(first_key + kOwn - 1), 1);
     };
-    if constexpr (BIAS) {
-        if (threadIdx.x < a.b.count)
-            bias.starts[threadIdx.x] = a.b.starts[threadIdx.x];
+    if constexpr (BIAS != kNoBias) {
         load_bias(head);
         __syncthreads();
     }
@@ -413,11 +508,10 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
         tiles_there<DIRECT>();
         if (more)
             ask(buf ^ 1, next_head, next);
-        const uint32_t i0 = t * kTile;
-        const Seen see = seen(s, i0, kTile, first, 32);
+        const uint32_t i0 = t * kQ;
+        const Seen see = seen(s, i0, kQ, first, 32);
         if (see != kNone) {
-            const bool whole = see == kAll && i0 + kTile <= at.len;
-            const QueryLimits limits(s, mine, i0 + 4 * h, at.len);
+            const bool whole = see == kAll && i0 + kQ <= at.len;
             if (kUnits<T> && tile_unit < unit) {   // the same for every lane
                 const float by = tile_unit / unit;
                 unit = tile_unit;
@@ -428,14 +522,28 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
                         dk[n][r] *= by;
             }
             const float ds_unit = unit * (1.0f / kWeightUnits);
-#pragma unroll DIM == 64 ? 2 : 1
-            for (int sub = 0; sub < 2; ++sub) {
+            const bool apart = BIAS == kLine || (BIAS == kTable && !all_beyond(t));
+            const float* line = BIAS == kLine ? bias_line(bias, buf) + kOwn - 1 - 32 * wave - c + 4 * h
+                                              : table + (int(i0) - int(mine) + kTableBefore + 4 * int(h));
+#pragma unroll
+            for (int sub = 0; sub < kQ / 32; ++sub) {
                 if (DIM == 128)
                     places.anew();
                 const f32x16 x = rows_times<T, DIM>(queries[buf], places, sub, k);
-                const f32x16 dp = rows_times<T, DIM>(douts[buf], places, sub, v);
-                if (DIM == 128) __builtin_amdgcn_sched_barrier(0);
+                const f32x16 dp = kValuesInLds ? rows_times_rows<T, DIM>(douts[buf], values + 32 * DIM * wave, places)
+                                               : rows_times<T, DIM>(douts[buf], places, sub, v);
+                if (DIM == 128 && BIAS == kTable)
+                    __builtin_amdgcn_sched_barrier(0);             // no loads ahead: the registers are full
                 f32x16 p, ds;
+                if (apart) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        p[r] = line[32 * sub + row_of(r, 0)];
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        p[r] = 0.0f;
+                }
 #pragma unroll
                 for (int quad = 0; quad < 4; ++quad) {
                     const uint32_t i = 32 * sub + 8 * quad + 4 * h;
@@ -444,24 +552,21 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int r = 4 * quad + e;
-                        float y = __builtin_fmaf(x[r], s.scale2, -lse[e]);
-                        if constexpr (BIAS)
-                            y += bias.line[buf][kOwn - 1 - 32 * wave - c + i + e];
-                        p[r] = __builtin_amdgcn_exp2f(y);
+                        p[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], s.scale2, BIAS == kNoBias ? -lse[e] : p[r] - lse[e]));
                         ds[r] = dp[r] - delta[e];
                         if (kUnits<T>)
                             ds[r] *= ds_unit;
                         ds[r] *= p[r];
                     }
                 }
-                if (!whole)
+                if (!whole) {
+                    const Mask mask = Mask::queries(s, mine, i0 + 4 * h, at.len);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        const bool in = limits.sees(32 * sub + row_of(r, 0));
-                        p[r] = in ? p[r] : 0.0f;
-                        ds[r] = in ? ds[r] : 0.0f;
+                        p[r] = mask.seen_or_0(p[r], sub, r);
+                        ds[r] = mask.seen_or_0(ds[r], sub, r);
                     }
-                if (DIM == 128) __builtin_amdgcn_sched_barrier(0);
+                }
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     columns_times<T, DIM>(dv, douts[buf], places, 2 * sub + half, rounded<T>(p, half));
@@ -471,9 +576,9 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
         }
         if (!more)
             break;
-        if constexpr (BIAS)
+        if constexpr (BIAS != kNoBias)
             if (next_head != head) {
-                __syncthreads();                   // the line before is read no more
+                __syncthreads();                   // the bias before is read no more
                 load_bias(next_head);
                 __syncthreads();
             }
@@ -527,7 +632,8 @@ __global__ __launch_bounds__(kSumRows* DIM / 8) void dkv_sum_kernel(BwdArgs<T> a
     uint32_t far_begin = 0, far_end = 0;
     if (a.far_slots && at.first == 0) {
         const uint32_t slots = s.offsets ? at.start / kFar + at.seq : at.seq * ((s.length + kFar - 1) / kFar);
-        const uint32_t behind = (near_end(s, 0, at.len) + kTile - 1) / kTile * kTile;
+        constexpr uint32_t kQ = kRows<DIM>;
+        const uint32_t behind = (near_end(s, 0, at.len) + kQ - 1) / kQ * kQ;
         if (behind < at.len) {
             far_begin = slots + behind / kFar;
             far_end = slots + (at.len + kFar - 1) / kFar;
@@ -627,17 +733,18 @@ uint64_t workspace_need(const Shape& s, uint32_t buckets)
     return a > b ? a : b;
 }
 
-template <typename T, int DIM, bool BIAS, bool DIRECT>
+template <typename T, int DIM, int BIAS, bool DIRECT>
 int launch(const BwdArgs<T>& a, hipStream_t stream)
 {
-    auto blocks = [](uint64_t items) { return dim3(uint32_t((items + 7) / 8 * 8)); };
-    const uint32_t kv = a.s.heads / a.s.group;
-    hipLaunchKernelGGL((attention_dq_kernel<T, DIM, BIAS, DIRECT>), blocks(uint64_t(a.slots) * a.s.heads), dim3(kBlock), 0, stream, a);
+    const uint64_t near = a.splits > 1 ? uint64_t(a.slots) * a.splits * (a.s.heads / a.s.group) : a.keys.blocks(a.s);
+    const uint32_t kv = a.s.heads / a.s.group, table = BIAS == kTable ? table_size(a.b) * 4 : 0;
+    hipLaunchKernelGGL((attention_dq_kernel<T, DIM, BIAS, DIRECT>), dim3(uint32_t(a.queries.blocks(a.s))), dim3(kBlock),
+                       table + (BIAS == kTable ? kWaves * (sums_size(a.b) + kSkewSize<DIM>) * 4 : 0), stream, a);
     int rc = launch_status();
     if (rc)
         return rc;
-    hipLaunchKernelGGL((attention_dkv_kernel<T, DIM, BIAS, DIRECT>), blocks((uint64_t(a.slots) * a.splits + a.far_slots) * kv), dim3(kBlock), 0,
-                       stream, a);
+    hipLaunchKernelGGL((attention_dkv_kernel<T, DIM, BIAS, DIRECT>), dim3(uint32_t(near + uint64_t(a.far_slots) * kv)), dim3(kBlock),
+                       table, stream, a);
     rc = launch_status();
     if (rc || (a.splits == 1 && !a.far_slots))
         return rc;
@@ -657,11 +764,13 @@ int run(Heads<void> dq, Heads<void> dk, Heads<void> dv, Heads<const void> dout, 
     auto part = [&](uint64_t at) { return reinterpret_cast<float*>(workspace + at); };
     const BwdArgs<T> a{out(dq), out(dk), out(dv), in(dout), in(o), in(q), in(k), in(v), lse, reinterpret_cast<f32x2*>(workspace + p.stats),
                        part(p.units), dbias ? part(p.partials) : nullptr, part(p.near), part(p.far), s, b, uint32_t(d.slots), uint32_t(d.splits),
-                       uint32_t(d.far_slots)};
+                       uint32_t(d.far_slots), Order(s, s.heads, d.slots), Order(s, s.heads / s.group, d.slots)};
     auto go = [&](auto dim, auto way) {
         constexpr int kDim = decltype(dim)::value;
         constexpr bool kDirect = decltype(way)::value;
-        return b.table ? launch<T, kDim, true, kDirect>(a, stream) : launch<T, kDim, false, kDirect>(a, stream);
+        if (!b.count)
+            return launch<T, kDim, kNoBias, kDirect>(a, stream);
+        return table_fits(b) ? launch<T, kDim, kTable, kDirect>(a, stream) : launch<T, kDim, kLine, kDirect>(a, stream);
     };
     const std::integral_constant<int, 64> d64;
     const std::integral_constant<int, 128> d128;

@@ -50,6 +50,9 @@ __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kerne
     const Places<DIM> places;
     Carrier<T, DIM, DIRECT> nk, nv;
     uint32_t t = tiles.begin();
+    clear<T, DIM, DIRECT>(keys[0], 2 * L::kElems, s.dim);
+    clear<T, DIM, DIRECT>(values[0], 2 * L::kElems, s.dim);
+    cleared<DIRECT, DIM>(s.dim);
     nk.fetch(keys[0], kp, a.k.ld, t * kTile, at.len, s.dim);
     nv.fetch(values[0], vp, a.v.ld, t * kTile, at.len, s.dim);
     Operand<T, DIM> q;
@@ -229,8 +232,8 @@ int run_fwd(void* o, uint64_t ld_o, uint64_t hs_o, float* lse, const void* q, ui
 {
     const FwdArgs<T> a{{static_cast<T*>(o), ld_o, hs_o}, lse, {static_cast<const T*>(q), ld_q, hs_q}, {static_cast<const T*>(k), ld_k, hs_k},
                        {static_cast<const T*>(v), ld_v, hs_v}, s, b, Order(s, s.heads, slots_of(s.tokens, s.sequences, s.offsets != nullptr, kOwn))};
-    if (direct_dim(s.dim) && direct(k, ld_k, hs_k) && direct(v, ld_v, hs_v))
-        return s.dim == 64 ? launch<T, 64, true>(a, stream) : launch<T, 128, true>(a, stream);
+    if (direct(k, ld_k, hs_k) && direct(v, ld_v, hs_v))
+        return s.dim <= 64 ? launch<T, 64, true>(a, stream) : launch<T, 128, true>(a, stream);
     return s.dim <= 64 ? launch<T, 64, false>(a, stream) : launch<T, 128, false>(a, stream);
 }
 

@@ -277,9 +277,9 @@ struct Tile {
 
 // A tile's way there.  DIRECT: straight into LDS, 16 bytes a lane to consecutive
 // addresses of a wave, so a lane takes the piece that belongs at its address;
-// it needs 16-byte aligned rows of DIM elements.  Else through registers.
-// Rows past the sequence's end repeat its last one (what they give is masked);
-// columns past `dim` are 0.
+// it needs rows at 16-byte aligned places.  Else through registers.  Rows past
+// the sequence's end repeat its last one (what they give is masked); columns
+// past `dim` are 0 (DIRECT: left as clear() made them).
 template <typename T, int DIM, bool DIRECT, int ROWS = kTile>
 class Carrier;
 
@@ -323,12 +323,14 @@ class Carrier<T, DIM, true, ROWS> {
 public:
     // The compiler waits for such a load before any read of LDS that it cannot tell apart from it, the other buffer's too: in
     // assembly it does not, and tiles_there() waits.
-    __device__ __forceinline__ void fetch(T* tile, const T* head, uint64_t ld, uint32_t row0, uint32_t len, uint32_t)
+    __device__ __forceinline__ void fetch(T* tile, const T* head, uint64_t ld, uint32_t row0, uint32_t len, uint32_t dim)
     {
         const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
         const uint32_t row = threadIdx.x / L::kPieces, col = (threadIdx.x % L::kPieces ^ L::twist(row)) * 8;
         const uint32_t to = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) T*)tile)) + wave * 1024;
         const T* from = head + row0 * ld;
+        if (col >= dim)
+            return;
         const uint32_t step = uint32_t(ld) * sizeof(T), last = len - 1 - row0;      // ld is below 2^24
         if (last >= uint32_t(ROWS) - 1) {
             const uint32_t at = row * step + col * uint32_t(sizeof(T));
@@ -355,6 +357,23 @@ private:
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(to), "v"(at), "s"(from) : "memory");
     }
 };
+
+// Before the first fetch into `elems` elements of LDS: 0 in the columns that no fetch writes.
+template <typename T, int DIM, bool DIRECT>
+__device__ __forceinline__ void clear(T* tiles, uint32_t elems, uint32_t dim)
+{
+    if (!DIRECT || dim == DIM)
+        return;
+    typename Vec8<T>::type zero = {};
+    for (uint32_t i = threadIdx.x * 8; i < elems; i += kBlock * 8)
+        *reinterpret_cast<typename Vec8<T>::type*>(tiles + i) = zero;
+}
+template <bool DIRECT, int DIM>
+__device__ __forceinline__ void cleared(uint32_t dim)
+{
+    if (DIRECT && dim != DIM)
+        __syncthreads();
+}
 
 // What was fetched is in LDS for every wave, and what the waves read before may be written over.
 template <bool DIRECT>
@@ -616,12 +635,11 @@ constexpr uint64_t kMaxTokens = uint64_t(1) << 30;
 constexpr uint32_t kMaxHeads = 65535;
 constexpr uint64_t kMaxPieces = uint64_t(1) << 27;
 
-// Rows that go straight into LDS: 16-byte aligned, of a whole tile's width.
+// Rows that go straight into LDS: at 16-byte aligned places.
 inline bool direct(const void* p, uint64_t ld, uint64_t hs)
 {
     return is_aligned(p, 16) && ld % 8 == 0 && hs % 8 == 0 && ld < (1u << 24);
 }
-inline bool direct_dim(uint32_t dim) { return dim == 64 || dim == 128; }
 
 inline int check_heads(const void* p, uint64_t ld, uint64_t hs, uint64_t tokens, uint32_t heads, uint32_t dim, int dtype)
 {

@@ -42,8 +42,9 @@ struct BwdArgs {
     Order queries, keys;                           // of the two passes
 };
 
+template <int BIAS>
 struct BinsLds {
-    float bins[kWaves][ZERO_MAX_BUCKETS];
+    float bins[kWaves][BIAS == kLine ? ZERO_MAX_BUCKETS : 1];      // kTable: of the last bucket
 };
 
 __device__ __forceinline__ float lane_value(float v, uint32_t from)
@@ -51,9 +52,7 @@ __device__ __forceinline__ float lane_value(float v, uint32_t from)
     return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(int(from * 4), __builtin_bit_cast(int, v)));
 }
 
-// The sums by distance of a wave (kTable): the distance d at d + kTableBefore.
-__host__ __device__ inline uint32_t sums_size(const Buckets& b) { return b.starts[b.count - 1] + 2 * kTableBefore; }
-
+// The sums by distance of a wave (kTable), up to where the last bucket begins.
 // They are formed from kSkewRows rows (keys) of a product at a time, written so
 // that the elements of one distance are neighbours: element (row, c) at
 // (c - row + kSkewRows - 1) * kSkewPitch + row, what no element goes to stays 0.
@@ -67,10 +66,12 @@ constexpr int kSkewPitch = kSkewRows<DIM> + 4;
 template <int DIM>
 constexpr int kSkewSize = (31 + kSkewRows<DIM>) * kSkewPitch<DIM>;
 
-// ds[r] of lane (c, h): the pair at distance base + c - row_of(r, h).
+// ds[r] of lane (c, h): the pair at distance base + c - row_of(r, h).  Returns
+// the lane's part of the sum over the distances from `last` on.
 template <int DIM>
-__device__ __forceinline__ void add_distances(float* skew, float* sums, int base, f32x16 ds, float back)
+__device__ __forceinline__ float add_distances(float* skew, float* sums, int last, int base, f32x16 ds, float back)
 {
+    float beyond = 0.0f;
     constexpr int kR = kSkewRows<DIM>, kP = kSkewPitch<DIM>, kLast = kR - 5;
     const int lane = threadIdx.x & 63, c = lane % 32, h = lane / 32;
     float* to = skew + (c + kR - 1) * kP - (kLast + 4 * h) * (kP - 1);
@@ -88,10 +89,16 @@ __device__ __forceinline__ void add_distances(float* skew, float* sums, int base
 #pragma unroll
             for (int i = 1; i < kR / 4; ++i)
                 v += *reinterpret_cast<const f32x4*>(skew + lane * kP + 4 * i);
-            sums[base - kR * pass + lane - (kR - 1) + kTableBefore] += (v[0] + v[1]) + (v[2] + v[3]);
+            const float sum = (v[0] + v[1]) + (v[2] + v[3]);
+            const int d = base - kR * pass + lane - (kR - 1);      // below 0 there is nothing
+            if (d >= last)
+                beyond += sum;
+            else if (d >= 0)
+                sums[d] += sum;
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
+    return beyond;
 }
 
 // bins[bucket] += the sums of ds along the distances of a 32 x 32 product
@@ -135,7 +142,7 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
     __shared__ alignas(16) T keys[2][L::kElems];
     __shared__ alignas(16) T values[2][L::kElems];
     __shared__ typename std::conditional<BIAS == kLine, BiasLine, int>::type bias;
-    __shared__ typename std::conditional<BIAS != kNoBias, BinsLds, int>::type sums;
+    __shared__ typename std::conditional<BIAS != kNoBias, BinsLds<BIAS>, int>::type sums;
     extern __shared__ __attribute__((aligned(16))) float table[];               // BIAS == kTable: the waves' skewed rows, the table, the waves' sums by distance
 
     const Shape& s = a.s;
@@ -160,6 +167,9 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
     Places<DIM> places;
     Carrier<T, DIM, DIRECT> nk, nv;
     uint32_t t = tiles.begin();
+    clear<T, DIM, DIRECT>(keys[0], 2 * L::kElems, s.dim);
+    clear<T, DIM, DIRECT>(values[0], 2 * L::kElems, s.dim);
+    cleared<DIRECT, DIM>(s.dim);
     nk.fetch(keys[0], kp, a.k.ld, t * kTile, at.len, s.dim);
     nv.fetch(values[0], vp, a.v.ld, t * kTile, at.len, s.dim);
     Operand<T, DIM> q, dout;
@@ -199,12 +209,12 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
     float beyond = 0.0f;                           // kTable: the bias of the last bucket
     float* const skew = table + wave * kSkewSize<DIM>;                     // the wave's
     float* const line = table + kWaves * kSkewSize<DIM>;
-    float* const by_distance = line + (BIAS == kTable ? table_size(a.b) + wave * sums_size(a.b) : 0);
     const uint32_t last_start = BIAS == kTable ? a.b.starts[a.b.count - 1] : 0;
+    float* const by_distance = line + (BIAS == kTable ? table_size(a.b) + wave * last_start : 0);
     if constexpr (BIAS == kTable) {
         draw_table<T>(line, a.b, head);
         beyond = bias_value<T>(a.b, head, a.b.count - 1) * kLog2e;
-        for (uint32_t x = lane; x < sums_size(a.b); x += 64)
+        for (uint32_t x = lane; x < last_start; x += 64)
             by_distance[x] = 0.0f;
         for (uint32_t x = lane; x < kSkewSize<DIM>; x += 64)
             skew[x] = 0.0f;
@@ -277,7 +287,7 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
                                 w[r] = ds[r] * back;
                             add_diagonals_of(bias, sums.bins[wave], a.b.count, int(first) - int(j0) - 32 * sub, w);
                         } else if (apart) {
-                            add_distances<DIM>(skew, by_distance, int(first) - int(j0) - 32 * sub, ds, back);
+                            far_sum += add_distances<DIM>(skew, by_distance, int(last_start), int(first) - int(j0) - 32 * sub, ds, back);
                         } else {
                             float v = 0.0f;
 #pragma unroll
@@ -318,24 +328,23 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
                 sums.bins[wave][0] = far_sum;
             __syncthreads();
             // the waves' sums of each distance, then each bucket's distances: a wave a bucket
-            const uint32_t size = sums_size(a.b);
             float* all = line + table_size(a.b);
-            for (uint32_t x = threadIdx.x; x < size; x += kBlock) {
+            for (uint32_t x = threadIdx.x; x < last_start; x += kBlock) {
                 float v = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWaves; ++w)
-                    v += all[w * size + x];
+                    v += all[w * last_start + x];
                 all[x] = v;
             }
             __syncthreads();
             for (uint32_t b = wave; b < a.b.count; b += kWaves) {
-                const uint32_t from = a.b.starts[b] + kTableBefore, to = b + 1 < a.b.count ? a.b.starts[b + 1] + kTableBefore : size;
                 float v = 0.0f;
-                for (uint32_t x = from + lane; x < to; x += 64)
-                    v += all[x];
-                v = layer::lanes_sum<64>(v);
-                if (b + 1 == a.b.count)
-                    v += (sums.bins[0][0] + sums.bins[1][0]) + (sums.bins[2][0] + sums.bins[3][0]);
+                if (b + 1 < a.b.count) {
+                    for (uint32_t x = a.b.starts[b] + lane; x < a.b.starts[b + 1]; x += 64)
+                        v += all[x];
+                    v = layer::lanes_sum<64>(v);
+                } else
+                    v = (sums.bins[0][0] + sums.bins[1][0]) + (sums.bins[2][0] + sums.bins[3][0]);
                 if (lane == 0)
                     a.partials[(uint64_t(head) * a.slots + slot) * a.b.count + b] = v;
             }
@@ -434,6 +443,11 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
     Operand<T, DIM> k, v;
     load_operand<T, DIM>(k, a.k.p + uint64_t(at.start) * a.k.ld + uint64_t(kv) * a.k.hs, a.k.ld, row, s.dim);
     const T* vp = a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(kv) * a.v.hs;
+    clear<T, DIM, DIRECT>(queries[0], 2 * L::kElems, s.dim);
+    clear<T, DIM, DIRECT>(douts[0], 2 * L::kElems, s.dim);
+    if (kValuesInLds)
+        clear<T, DIM, DIRECT>(values, Tile<DIM, kOwn>::kElems, s.dim);
+    cleared<DIRECT, DIM>(s.dim);
     if (kValuesInLds) {
         Carrier<T, DIM, DIRECT, kOwn> nv;
         nv.fetch(values, vp, a.v.ld, first_key, at.len, s.dim);
@@ -739,7 +753,7 @@ int launch(const BwdArgs<T>& a, hipStream_t stream)
     const uint64_t near = a.splits > 1 ? uint64_t(a.slots) * a.splits * (a.s.heads / a.s.group) : a.keys.blocks(a.s);
     const uint32_t kv = a.s.heads / a.s.group, table = BIAS == kTable ? table_size(a.b) * 4 : 0;
     hipLaunchKernelGGL((attention_dq_kernel<T, DIM, BIAS, DIRECT>), dim3(uint32_t(a.queries.blocks(a.s))), dim3(kBlock),
-                       table + (BIAS == kTable ? kWaves * (sums_size(a.b) + kSkewSize<DIM>) * 4 : 0), stream, a);
+                       table + (BIAS == kTable ? kWaves * (a.b.starts[a.b.count - 1] + kSkewSize<DIM>) * 4 : 0), stream, a);
     int rc = launch_status();
     if (rc)
         return rc;
@@ -775,8 +789,8 @@ int run(Heads<void> dq, Heads<void> dk, Heads<void> dv, Heads<const void> dout, 
     const std::integral_constant<int, 64> d64;
     const std::integral_constant<int, 128> d128;
     int rc;
-    if (direct_dim(s.dim) && direct(q.p, q.ld, q.hs) && direct(k.p, k.ld, k.hs) && direct(v.p, v.ld, v.hs) && direct(dout.p, dout.ld, dout.hs))
-        rc = s.dim == 64 ? go(d64, std::true_type{}) : go(d128, std::true_type{});
+    if (direct(q.p, q.ld, q.hs) && direct(k.p, k.ld, k.hs) && direct(v.p, v.ld, v.hs) && direct(dout.p, dout.ld, dout.hs))
+        rc = s.dim <= 64 ? go(d64, std::true_type{}) : go(d128, std::true_type{});
     else
         rc = s.dim <= 64 ? go(d64, std::false_type{}) : go(d128, std::false_type{});
     if (rc || !dbias)

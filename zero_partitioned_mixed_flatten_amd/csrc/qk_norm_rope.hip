@@ -10,6 +10,8 @@
 //
 // Bound by memory: one read and one write of everything, with both tensors in
 // one launch.
+#include <type_traits>
+
 #include "attention.hpp"
 
 namespace zero {
@@ -39,10 +41,246 @@ struct QkArgs {
     const float* table;                            // table_rows x rot / 2 x (cos, sin)
     uint64_t table_rows, period;
     const int32_t* positions;
-    float* partials;                               // backward: blocks of q, then of k, x dim
+    float* partials;                               // backward: blocks x dim (qk_token_kernel: for each q, then k)
     uint32_t blocks[2];
+    uint32_t split;
 };
 
+template <typename T>
+__device__ __forceinline__ const float* turn_row(const QkArgs<T>& a, uint64_t token, bool& known)
+{
+    uint64_t pos;
+    if (a.positions) {
+        const int32_t p = a.positions[token];
+        pos = p < 0 ? ~uint64_t(0) : uint64_t(p);
+    } else {
+        pos = a.period ? token % a.period : token;
+    }
+    known = pos < a.table_rows;
+    return a.table + (known ? pos : 0) * a.rot;
+}
+
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v)
+{
+    if (LANES >= 2) v += layer::dpp<0xB1>(v);      // lane ^ 1
+    if (LANES >= 4) v += layer::dpp<0x4E>(v);      // lane ^ 2
+    if (LANES >= 8) v += layer::dpp<0x141>(v);     // the other quad of 8
+    if (LANES >= 16) v += layer::dpp<0x140>(v);    // the other 8 of 16
+    if (LANES >= 32) v += __shfl_xor(v, 16);
+    return v;
+}
+
+// 1 / sqrt(v), one step off at most; v below the normal numbers (a tiny eps and a head of zeros) by the long way.
+__device__ __forceinline__ float inverse_root(float v)
+{
+    return v >= 0x1p-126f ? __builtin_amdgcn_rsqf(v) : 1.0f / sqrtf(v);
+}
+
+// ---- heads that turn wholly or not at all --------------------------------------------
+// A wave has a token (or one of `split` parts of its heads): its angles are in
+// registers for all heads, and addresses are a scalar base plus a lane's
+// constant.  LANES lanes have a head, 16 bytes each, so that an access takes
+// whole 128-byte lines.  The halves of a pair of a half-split head are then in
+// different lanes: the upper half's pieces are taken in reverse, so that a
+// piece's partner is in the mirrored lane, and the product with the partner is
+// one instruction (DPP).  What it is against is vector instructions: 275 for 16
+// binary16 elements of a lane with both halves of a head in a thread (an access
+// of which leaves half of each line to the next), 23 us forward and 43 backward
+// at 8192 tokens of 2 x 25 heads of 64.
+template <typename T>
+struct Piece16 {
+    static constexpr int kPer = 16 / sizeof(T);
+    typedef T V __attribute__((ext_vector_type(kPer)));
+    typedef V VU __attribute__((aligned(sizeof(T))));
+};
+
+template <int LANES>
+__device__ __forceinline__ float mirrored(float v)
+{
+    if (LANES == 2) return layer::dpp<0xB1>(v);
+    if (LANES == 4) return layer::dpp<0x1B>(v);
+    if (LANES == 8) return layer::dpp<0x141>(v);
+    return layer::dpp<0x140>(v);
+}
+
+// STYLE 0: not turned, 1: pairs of halves, 2: neighbours.
+template <typename T, int LANES, int STYLE, bool PAST, bool BWD>
+__global__ __launch_bounds__(kQkBlock) void qk_token_kernel(QkArgs<T> a)
+{
+    typedef Piece16<T> P;
+    typedef typename P::V V;
+    typedef typename P::VU VU;
+    constexpr int kPer = P::kPer, kHeads = 64 / LANES;             // heads of an access
+    constexpr int kBatch = BWD ? 2 : 4;
+    __shared__ float sums[BWD ? kQkBlock / 64 : 1][2][BWD ? LANES * kPer : 1];
+    const uint32_t lane = threadIdx.x % 64, i = lane % LANES, sub = lane / LANES;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const bool high = STYLE == 1 && i >= LANES / 2;
+    const uint32_t piece = high ? 3 * LANES / 2 - 1 - i : i;
+    float w[2][kPer], dw[2][kPer] = {};
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const void* p = a.side[n].w;
+        if (p && a.vec_f32) {
+            typedef float F __attribute__((ext_vector_type(kPer)));
+            typedef F FU __attribute__((aligned(4)));
+            const F r = *reinterpret_cast<const FU*>(static_cast<const float*>(p) + piece * kPer);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                w[n][j] = r[j];
+        } else if (p) {
+            const V r = *reinterpret_cast<const VU*>(static_cast<const T*>(p) + piece * kPer);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                w[n][j] = float(r[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                w[n][j] = 1.0f;
+        }
+    }
+    const float inv = 1.0f / float(LANES * kPer);
+    const uint64_t units = a.tokens * a.split;
+    for (uint64_t u = uint64_t(blockIdx.x) * (kQkBlock / 64) + wave; u < units; u += uint64_t(gridDim.x) * (kQkBlock / 64)) {
+        const uint64_t token = a.split == 1 ? u : u / a.split;
+        const uint32_t part = uint32_t(u - token * a.split);
+        float c[kPer], s[kPer];                    // of each element's pair, the sine as it comes with the partner
+        if (STYLE != 0) {
+            bool known;
+            const float* row = turn_row(a, token, known);
+            if (STYLE == 1) {
+                const uint32_t first = (high ? piece - LANES / 2 : piece) * kPer;
+#pragma unroll
+                for (int j = 0; j < kPer; j += 2) {
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(row + 2 * (first + j));
+                    c[j] = v[0];
+                    s[j] = high != BWD ? v[1] : -v[1];
+                    c[j + 1] = v[2];
+                    s[j + 1] = high != BWD ? v[3] : -v[3];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPer; j += 4) {
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(row + piece * kPer + j);
+                    c[j] = c[j + 1] = v[0];
+                    s[j] = BWD ? v[1] : -v[1];
+                    s[j + 1] = -s[j];
+                    c[j + 2] = c[j + 3] = v[2];
+                    s[j + 2] = BWD ? v[3] : -v[3];
+                    s[j + 3] = -s[j + 2];
+                }
+            }
+            if (!known)
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    c[j] = __builtin_nanf("");
+        }
+        auto turned = [&](float (&v)[kPer]) {
+            if (STYLE == 0)
+                return;
+            float p[kPer];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                p[j] = (STYLE == 1 ? mirrored<LANES>(v[j]) : v[j ^ 1]) * s[j];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                v[j] = __builtin_fmaf(v[j], c[j], p[j]);
+        };
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const QkSide<T>& side = a.side[n];
+            const uint32_t accesses = (side.heads + kHeads - 1) / kHeads;
+            uint32_t k = a.split == 1 ? 0 : accesses * part / a.split;
+            const uint32_t end = a.split == 1 ? accesses : accesses * (part + 1) / a.split;
+            auto at = [&](uint64_t hs, uint32_t access) {          // the lane's element, from the token's; heads past the last read that
+                const uint32_t head = access * kHeads + sub;
+                return (head < side.heads ? head : side.heads - 1) * uint32_t(hs) + piece * kPer;
+            };
+            auto read = [&](const T* p, uint64_t ld, uint64_t hs, uint32_t access) {
+                const VU* from = reinterpret_cast<const VU*>(p + token * ld + at(hs, access));
+                return PAST ? V(__builtin_nontemporal_load(from)) : V(*from);
+            };
+            for (; k < end; k += kBatch) {
+                V raw[kBatch], grad[kBatch];       // a batch of accesses in flight together
+#pragma unroll
+                for (int e = 0; e < kBatch; ++e) {
+                    raw[e] = read(side.x, side.ld_x, side.hs_x, k + e < end ? k + e : end - 1);
+                    if (BWD)
+                        grad[e] = read(side.dy, side.ld_dy, side.hs_dy, k + e < end ? k + e : end - 1);
+                }
+#pragma unroll
+                for (int e = 0; e < kBatch; ++e) {
+                    if (k + e >= end)
+                        break;
+                    const V rx = raw[e], rg = BWD ? grad[e] : raw[e];
+                    const bool live = (k + e) * kHeads + sub < side.heads;
+                    float x[kPer], g[kPer], q = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) {
+                        x[j] = float(rx[j]);
+                        q = __builtin_fmaf(x[j], x[j], q);
+                    }
+                    const float rstd = inverse_root(__builtin_fmaf(group_sum<LANES>(q), inv, a.eps));
+                    if (!BWD) {
+#pragma unroll
+                        for (int j = 0; j < kPer; ++j)
+                            x[j] = x[j] * rstd * w[n][j];
+                        turned(x);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kPer; ++j)
+                            g[j] = float(rg[j]);
+                        turned(g);
+                        float mean = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < kPer; ++j) {
+                            x[j] = live ? x[j] * rstd : 0.0f;
+                            dw[n][j] = live ? __builtin_fmaf(g[j], x[j], dw[n][j]) : dw[n][j];
+                            g[j] *= w[n][j];
+                            mean = __builtin_fmaf(g[j], x[j], mean);
+                        }
+                        mean = group_sum<LANES>(mean) * inv;
+#pragma unroll
+                        for (int j = 0; j < kPer; ++j)
+                            x[j] = rstd * __builtin_fmaf(-x[j], mean, g[j]);
+                    }
+                    V out;
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j)
+                        out[j] = T(x[j]);
+                    if (live)
+                        __builtin_nontemporal_store(out, reinterpret_cast<VU*>(side.out + token * side.ld_out + at(side.hs_out, k + e)));
+                }
+            }
+        }
+    }
+    if (!BWD || !a.partials)
+        return;
+    // the wave's heads, then the waves
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            float v = dw[n][j];
+#pragma unroll
+            for (int d = LANES; d < 64; d <<= 1)
+                v += __shfl_xor(v, d);
+            if (lane < LANES)
+                sums[wave][n][piece * kPer + j] = v;
+        }
+    __syncthreads();
+    constexpr int kWavesOf = BWD ? kQkBlock / 64 : 1;
+    for (uint32_t x = threadIdx.x; x < 2 * LANES * kPer; x += kQkBlock) {
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWavesOf; ++k)
+            v += sums[k][x / (LANES * kPer)][x % (LANES * kPer)];
+        a.partials[uint64_t(blockIdx.x) * (2 * LANES * kPer) + x] = v;
+    }
+}
+
+// ---- other forms -------------------------------------------------------------------------
 // A thread holds 16 bytes at each of two places of a head, so that it has
 // whole pairs: of a turned half-split head the same part of both halves.
 // Elements past `rot` are taken alike, as two halves of what is left.
@@ -112,20 +350,6 @@ struct Part2 {
     }
 };
 
-template <typename T>
-__device__ __forceinline__ const float* turn_row(const QkArgs<T>& a, uint64_t token, bool& known)
-{
-    uint64_t pos;
-    if (a.positions) {
-        const int32_t p = a.positions[token];
-        pos = p < 0 ? ~uint64_t(0) : uint64_t(p);
-    } else {
-        pos = a.period ? token % a.period : token;
-    }
-    known = pos < a.table_rows;
-    return a.table + (known ? pos : 0) * a.rot;
-}
-
 // Turns v by the row's angles, or back.
 template <typename T, int PER>
 __device__ __forceinline__ void turn(float (&v)[2][PER], const float* row, bool known, const Part2<T>& at, bool interleaved, bool back)
@@ -159,17 +383,6 @@ __device__ __forceinline__ void turn(float (&v)[2][PER], const float* row, bool 
         x = __builtin_fmaf(p, c, -(q * s));
         y = __builtin_fmaf(q, c, p * s);
     }
-}
-
-template <int LANES>
-__device__ __forceinline__ float group_sum(float v)
-{
-    if (LANES >= 2) v += layer::dpp<0xB1>(v);      // lane ^ 1
-    if (LANES >= 4) v += layer::dpp<0x4E>(v);      // lane ^ 2
-    if (LANES >= 8) v += layer::dpp<0x141>(v);     // the other quad of 8
-    if (LANES >= 16) v += layer::dpp<0x140>(v);    // the other 8 of 16
-    if (LANES >= 32) v += __shfl_xor(v, 16);
-    return v;
 }
 
 template <int PER>
@@ -419,18 +632,19 @@ constexpr int kQkFoldCols = 8, kQkFoldRows = 128;
 template <typename T>
 __global__ __launch_bounds__(kQkFoldCols* kQkFoldRows) void qk_fold_kernel(void* dwq, void* dwk, bool f32, bool accumulate,
                                                                          const float* partials, uint32_t blocks_q, uint32_t blocks_k,
-                                                                         uint32_t dim)
+                                                                         uint32_t dim, bool both)
 {
     __shared__ float part[kQkFoldRows][kQkFoldCols];
     void* dst = blockIdx.y ? dwk : dwq;
     if (!dst)
         return;
     const uint32_t c = threadIdx.x % kQkFoldCols, r = threadIdx.x / kQkFoldCols, col = blockIdx.x * kQkFoldCols + c;
-    const uint32_t first = blockIdx.y ? blocks_q : 0, n = blockIdx.y ? blocks_k : blocks_q;
+    // both: each workgroup has a partial for q, then one for k
+    const uint32_t first = !blockIdx.y ? 0 : both ? 1 : blocks_q, n = blockIdx.y ? blocks_k : blocks_q, apart = both ? 2 : 1;
     float v = 0.0f;
     if (col < dim)
         for (uint32_t i = r; i < n; i += kQkFoldRows)
-            v += partials[uint64_t(first + i) * dim + col];
+            v += partials[(uint64_t(first) + uint64_t(i) * apart) * dim + col];
     part[r][c] = v;
     for (int rows = kQkFoldRows / 2; rows; rows >>= 1) {
         __syncthreads();
@@ -508,11 +722,68 @@ uint32_t bwd_blocks(uint64_t tokens, uint32_t heads, uint32_t all, uint32_t item
     return uint32_t(need < most ? need : most);
 }
 
+// Of qk_token_kernel: a wave a token, or where that leaves most of the card idle a part of its heads, and no more
+// workgroups than are resident, which go on to further tokens: a wave's start (its weights, the position, then the
+// angles) is a chain of loads.  8192 tokens of 2 x 25 heads of 64, forward: 24 us with 1024 workgroups, 26 with 1536 or
+// 2048, 29 in two parts a token; backward 40, 45, 47 and 42.
+constexpr uint64_t kTokenWaves = 4096, kTokenBlocks = 1024;
+
+uint32_t token_split(uint64_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t each)
+{
+    const uint64_t accesses = (heads + each - 1) / each, more = (kv_heads + each - 1) / each, most = accesses > more ? accesses : more;
+    uint64_t n = tokens ? (kTokenWaves + tokens - 1) / tokens : 1;
+    return uint32_t(n < most ? n : most);
+}
+
+uint64_t token_blocks(uint64_t tokens, uint32_t split, bool bwd)
+{
+    const uint64_t n = (tokens * split + kQkBlock / 64 - 1) / (kQkBlock / 64);
+    return n > kTokenBlocks ? kTokenBlocks : n;
+}
+
 uint64_t qk_workspace(uint64_t tokens, uint32_t heads, uint32_t kv_heads, uint32_t dim)
 {
     // the fewest heads that any form gives a workgroup
     const uint64_t q = bwd_blocks(tokens, heads, heads + kv_heads, kQkBlock / 32), k = bwd_blocks(tokens, kv_heads, heads + kv_heads, kQkBlock / 32);
-    return (q + k) * dim * 4;
+    const uint64_t by_token = 2 * token_blocks(tokens, token_split(tokens, heads, kv_heads, 1), true);
+    return (q + k > by_token ? q + k : by_token) * dim * 4;
+}
+
+// Lanes a head of qk_token_kernel, or 0 where it does not take the call.
+template <typename T>
+uint32_t token_lanes(const QkCall& c)
+{
+    constexpr uint32_t kPer = 16 / sizeof(T);
+    const uint32_t lanes = c.dim / kPer;
+    if (c.dim % kPer || (c.rot && c.rot != c.dim) || lanes < 2 || lanes > 16 || (lanes & (lanes - 1)))
+        return 0;
+    // a lane's place in a token is 32 bits
+    for (const QkTensor& t : c.side)
+        for (uint64_t hs : {t.hs_out, t.hs_x, t.hs_dy})
+            if (t.heads && hs * t.heads >= (uint64_t(1) << 30))
+                return 0;
+    return lanes;
+}
+
+template <typename T, bool BWD>
+void launch_token(const QkArgs<T>& a, uint32_t lanes, uint64_t blocks, bool past, hipStream_t s)
+{
+    auto go = [&](auto n, auto style, auto p) {
+        hipLaunchKernelGGL((qk_token_kernel<T, decltype(n)::value, decltype(style)::value, decltype(p)::value, BWD>), dim3(uint32_t(blocks)),
+                           dim3(kQkBlock), 0, s, a);
+    };
+    auto with_past = [&](auto n, auto style) { past ? go(n, style, std::true_type{}) : go(n, style, std::false_type{}); };
+    auto with_style = [&](auto n) {
+        if (!a.rot) with_past(n, std::integral_constant<int, 0>{});
+        else if (!a.interleaved) with_past(n, std::integral_constant<int, 1>{});
+        else with_past(n, std::integral_constant<int, 2>{});
+    };
+    switch (lanes) {
+    case 2: with_style(std::integral_constant<int, 2>{}); break;
+    case 4: with_style(std::integral_constant<int, 4>{}); break;
+    case 8: with_style(std::integral_constant<int, 8>{}); break;
+    default: with_style(std::integral_constant<int, 16>{}); break;
+    }
 }
 
 template <typename T, bool BWD, int LANES, int STYLE>
@@ -569,7 +840,18 @@ int run_qk(const QkCall& c, hipStream_t s)
     }
     // what is read once goes past the caches where it does not fit them anyway
     const bool past = c.tokens * all * c.dim * sizeof(T) * (BWD ? 3 : 2) > layer::kStreamBytes;
-    if (c.tokens) {
+    const uint32_t token_way = token_lanes<T>(c);
+    const bool by_token = token_way != 0;
+    if (c.tokens && by_token) {
+        a.split = token_split(c.tokens, c.side[0].heads, c.side[1].heads, 64 / token_way);
+        const uint64_t n = token_blocks(c.tokens, a.split, BWD);
+        a.blocks[0] = uint32_t(n);
+        a.blocks[1] = uint32_t(n);
+        launch_token<T, BWD>(a, token_way, n, past, s);
+        const int rc = launch_status();
+        if (rc)
+            return rc;
+    } else if (c.tokens) {
         if (!parts) {
             hipLaunchKernelGGL((qk_any_kernel<T, BWD>), dim3(uint32_t(blocks)), dim3(kQkBlock), 0, s, a);
         } else {
@@ -596,7 +878,7 @@ int run_qk(const QkCall& c, hipStream_t s)
     if (!BWD || !(c.dw[0] || c.dw[1]))
         return ZERO_OK;
     hipLaunchKernelGGL(qk_fold_kernel<T>, dim3((c.dim + kQkFoldCols - 1) / kQkFoldCols, 2), dim3(kQkFoldCols * kQkFoldRows), 0, s, c.dw[0],
-                       c.dw[1], c.grad_dtype == ZERO_F32, c.accumulate, a.partials, a.blocks[0], a.blocks[1], c.dim);
+                       c.dw[1], c.grad_dtype == ZERO_F32, c.accumulate, a.partials, a.blocks[0], a.blocks[1], c.dim, by_token);
     return launch_status();
 }
 

@@ -363,3 +363,48 @@ def test_binding_qk(Z, bound):
         with pytest.raises((ValueError, TypeError)):
             Z.zero_rope_table(t)
     assert len(bound) == 4
+
+
+# ---- WindowAttention ------------------------------------------------------------------------------
+
+def _place(Z, **kw):
+    return Z.WindowAttention(16, 4, 2, 8, dtype=torch.float32, device="cpu", **kw)
+
+
+def test_place_refusals(Z):
+    q, k = torch.zeros(6, 4, 8), torch.zeros(6, 2, 8)
+    for kw in (dict(bias=torch.zeros(4, 2)), dict(starts=[0])):
+        with pytest.raises(ValueError, match="go together"):
+            _place(Z, **kw)
+    with pytest.raises(ValueError):
+        Z.WindowAttention(-1, 4, 2, 8, device="cpu")
+    with pytest.raises(ValueError):
+        Z.WindowAttention(1, 4, 2, 8, max_sequences=0, device="cpu")
+    p = _place(Z, table=torch.zeros(6, 4, 2))
+    with pytest.raises(ValueError, match="made for"):
+        p.forward(torch.zeros(17, 4, 8), torch.zeros(17, 2, 8), torch.zeros(17, 2, 8))
+    with pytest.raises(ValueError, match="made for"):
+        p.forward(q, k, k, sequences=2)
+    with pytest.raises(ValueError, match="made for"):
+        p.forward(q, k, k, offsets=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError, match="positions"):
+        p.forward(q, k, k, offsets=torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="no forward pass"):
+        p.backward(q)
+    p = Z.WindowAttention(16, 4, 2, 8, max_sequences=4, device="cpu")
+    with pytest.raises(ValueError, match="equal length"):
+        p.forward(q, k, k, sequences=4)
+    with pytest.raises(ValueError, match="equal length"):
+        p.forward(q, k, k, sequences=0)
+
+
+def test_a_refused_forward_leaves_the_last_one(Z):
+    """Refusals before anything is enqueued; one that comes later leaves no pass to go back over."""
+    p = _place(Z)
+    last = p._last = object()
+    with pytest.raises(ValueError, match="made for"):
+        p.forward(torch.zeros(17, 4, 8), torch.zeros(17, 2, 8), torch.zeros(17, 2, 8))
+    assert p._last is last
+    with pytest.raises(ValueError, match="device tensor"):
+        p.forward(torch.zeros(6, 4, 8), torch.zeros(6, 2, 8), torch.zeros(6, 2, 8))
+    assert p._last is None

@@ -1,5 +1,6 @@
 """MI355X-native ZeRO partitioned mixed-precision Adam shard step, and the
-layer operators of a block's residual stream that produce gradients for it.
+layer operators of a block's residual stream and the attention operators that
+produce gradients for it.
 
 The computation is HIP kernels for gfx950 behind the C ABI declared in
 include/zero_mi355x.h (libzero_mi355x.so, built in-tree); this package is the
@@ -23,6 +24,7 @@ from ._lib import (EXPORTS, NORM_PARTIAL_BYTES, ONEBIT_STATE_BYTES, RNG_BYTES, S
                    zero_status_string, zero_step_state_init,
                    zero_stream_copy, zero_host_create, zero_host_destroy, zero_host_threads, zero_host_state_init,
                    zero_host_norm_overflow, zero_host_adam_step, zero_offload_step, zero_host_stream_copy)
+from .attention import WindowAttention
 from .layers import LayerRng, ResidualNorm
 from .stepper import AccumStep, HostContext, OffloadStep, OneBitStep, ShardStep, hparams
 
@@ -44,4 +46,4 @@ __all__ = ["EXPORTS", "NORM_PARTIAL_BYTES", "STATE_BYTES", "ZERO_BF16", "ZERO_F1
            "zero_dropout_layernorm_fwd", "zero_dropout_layernorm_bwd", "zero_layer_workspace_bytes", "LayerRng",
            "ResidualNorm", "ZERO_MAX_BUCKETS", "AttentionParams", "attention_params", "zero_rope_table",
            "zero_qk_norm_rope_fwd", "zero_qk_workspace_bytes", "zero_qk_norm_rope_bwd", "zero_attention_buckets",
-           "zero_attention_fwd", "zero_attention_workspace_bytes", "zero_attention_bwd"]
+           "zero_attention_fwd", "zero_attention_workspace_bytes", "zero_attention_bwd", "WindowAttention"]

@@ -25,6 +25,47 @@ struct FwdArgs {
     Order order;
 };
 
+// The output of one row by a wave, from its maximum and sum, over the keys that
+// it sees and no others: 64 keys a time, a lane a key for their weights, then a
+// lane a column.  Slow (a row of 1024 keys some 50 us); for rows of a tile
+// beside an inf or NaN value that they do not see.
+template <typename T, int DIM, int BIAS>
+__device__ __forceinline__ void sum_row(const FwdArgs<T>& a, const Piece& at, uint32_t head, uint32_t i, float m, float sum)
+{
+    const Shape& s = a.s;
+    const uint32_t lane = threadIdx.x & 63;
+    const T* q = a.q.p + (uint64_t(at.start) + i) * a.q.ld + uint64_t(head) * a.q.hs;
+    const T* kp = a.k.p + uint64_t(at.start) * a.k.ld + uint64_t(head / s.group) * a.k.hs;
+    const T* vp = a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(head / s.group) * a.v.hs;
+    const float base = m == -INFINITY ? 0.0f : m;
+    float acc[DIM / 64] = {};
+    for (uint32_t j0 = 0; j0 <= i; j0 += 64) {
+        const uint32_t j = j0 + lane;
+        const bool in = j <= i && (i - j < s.window || j < s.sinks);
+        float p = 0.0f;
+        if (in) {
+            for (uint32_t d = 0; d < s.dim; ++d)
+                p = __builtin_fmaf(float(q[d]), float(kp[j * a.k.ld + d]), p);
+            p *= s.scale2;
+            if (BIAS != kNoBias)
+                p += bias_value<T>(a.b, head, bucket_of(a.b.starts, a.b.count, i - j)) * kLog2e;
+            p = __builtin_amdgcn_exp2f(p - base);
+        }
+        for (uint64_t left = __ballot(in); left; left &= left - 1) {
+            const uint32_t k = __builtin_ctzll(left);
+            const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, p), k));
+#pragma unroll
+            for (int n = 0; n < DIM / 64; ++n)
+                if (lane + 64 * n < s.dim)
+                    acc[n] = __builtin_fmaf(w, float(vp[(j0 + k) * a.v.ld + lane + 64 * n]), acc[n]);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < DIM / 64; ++n)
+        if (lane + 64 * n < s.dim)
+            a.o.p[(uint64_t(at.start) + i) * a.o.ld + uint64_t(head) * a.o.hs + lane + 64 * n] = T(acc[n] / sum);
+}
+
 template <typename T, int DIM, int BIAS, bool DIRECT>
 __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kernel(FwdArgs<T> a)
 {
@@ -159,9 +200,24 @@ __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kerne
     }
     sum = halves_sum(sum);
     const bool live = mine < at.len;
-    store_columns<T, DIM>(a.o.p + uint64_t(at.start) * a.o.ld + uint64_t(head) * a.o.hs, a.o.ld, mine, live, s.dim, acc, 1.0f / sum);
+    // a weight of 0 times an inf or NaN value is a NaN: rows with one are summed again over the keys that they see
+    float probe = 0.0f;
+#pragma unroll
+    for (int n = 0; n < DIM / 32; ++n)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            probe = __builtin_fmaf(acc[n][r], 0.0f, probe);
+    const uint64_t marked = __ballot(probe != probe);
+    uint32_t again = uint32_t(marked) | uint32_t(marked >> 32);
+    store_columns<T, DIM>(a.o.p + uint64_t(at.start) * a.o.ld + uint64_t(head) * a.o.hs, a.o.ld, mine, live && !(again >> c & 1), s.dim, acc, 1.0f / sum);
     if (a.lse && live && h == 0)
         a.lse[uint64_t(head) * s.tokens + at.start + mine] = (m + __builtin_amdgcn_logf(sum)) * kLn2;
+    for (; again; again &= again - 1) {
+        const uint32_t i = __builtin_ctz(again);
+        if (first + i < at.len)
+            sum_row<T, DIM, BIAS>(a, at, head, first + i, __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, m), i)),
+                                  __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sum), i)));
+    }
 }
 
 template <typename T, int DIM, bool DIRECT>

@@ -391,6 +391,8 @@ def test_place_refusals(Z):
         p.forward(q, k, k, offsets=torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError, match="no forward pass"):
         p.backward(q)
+    with pytest.raises(ValueError, match="angles of 6"):
+        p.forward(torch.zeros(7, 4, 8), torch.zeros(7, 2, 8), torch.zeros(7, 2, 8))
     p = Z.WindowAttention(16, 4, 2, 8, max_sequences=4, device="cpu")
     with pytest.raises(ValueError, match="equal length"):
         p.forward(q, k, k, sequences=4)

@@ -74,6 +74,8 @@ class WindowAttention:
             raise ValueError("WindowAttention.forward: packed sequences with a rotation need their positions")
         if offsets is None and (n < 1 or tokens % n):
             raise ValueError(f"WindowAttention.forward: {tokens} tokens are not {n} sequences of equal length")
+        if self.table is not None and positions is None and tokens // n > self.table.shape[0]:
+            raise ValueError(f"WindowAttention.forward: sequences of {tokens // n} tokens, angles of {self.table.shape[0]}")
         nq, nk = self._q[:tokens], self._k[:tokens]
         o = self._o[:tokens] if o is None else o
         lse = self._lse[:self.params.heads * tokens].view(self.params.heads, tokens)

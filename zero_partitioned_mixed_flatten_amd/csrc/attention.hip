@@ -207,7 +207,7 @@ __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kerne
 #pragma unroll
         for (int r = 0; r < 16; ++r)
             probe = __builtin_fmaf(acc[n][r], 0.0f, probe);
-    const uint64_t marked = __ballot(probe != probe);
+    const uint64_t marked = __ballot(probe != probe && sum < INFINITY);          // a NaN or inf among the scores stays what it is
     uint32_t again = uint32_t(marked) | uint32_t(marked >> 32);
     store_columns<T, DIM>(a.o.p + uint64_t(at.start) * a.o.ld + uint64_t(head) * a.o.hs, a.o.ld, mine, live && !(again >> c & 1), s.dim, acc, 1.0f / sum);
     if (a.lse && live && h == 0)

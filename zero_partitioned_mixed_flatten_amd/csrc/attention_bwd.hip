@@ -253,6 +253,9 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
             const int line_at = int(mine) - int(j0) - (kTile - 1) + kTableBefore - 4 * int(h);
 #pragma unroll DIM == 64 ? 2 : 1
             for (int sub = 0; sub < 2; ++sub) {
+                // half a tile beyond the window's edge: 2% of dq, dk and dv of 2 x 4096 positions, 64 heads of 128; none of heads of 64
+                if (DIM == 128 && see == kSome && seen(s, first, 32, j0 + 32 * sub, 32) == kNone)
+                    continue;
                 if (DIM == 128)
                     places.anew();
                 const f32x16 x = rows_times<T, DIM>(keys[buf], places, sub, q);

@@ -85,6 +85,24 @@ def test_rows_behind_the_window_are_not_seen():
     assert bool(o[10:149].isnan().flatten(1).any(1).all())
 
 
+def test_rows_long_behind_first_tokens_and_window():
+    """The same with keys between the first tokens and the window's, whole tiles of them, and one such value that is seen."""
+    for value in (math.nan, math.inf):
+        c = Call([700], 2, 1, 128, BF16, window=50, sinks=70)
+        (want, _), (e, _) = c.want_fwd()
+        c.d["k"][400:460] = value
+        c.d["v"][400:460] = value
+        c.d["v"][600, 0, 5] = value
+        o, _ = c.fwd()
+        keep = torch.ones(700, dtype=torch.bool)
+        keep[400:509] = False                        # 509 sees 460 on
+        keep[600:650] = False
+        close(o[keep.cuda()], want[keep], A.stored(e, want, BF16)[keep], "o")
+        bad = o[600:650]
+        assert bool(bad[:, :, 5].isfinite().logical_not().all()) and bool(bad[:, :, :5].isfinite().all())
+        assert bool(bad[:, :, 6:].isfinite().all())
+
+
 def test_other_sequences_do_not_matter():
     """Whatever one sequence and the rows behind the last hold, the others' results and gradients are the same bits."""
     c = Call([130, 70, 200], 4, 2, 64, F16, window=90, sinks=3, after=9)

@@ -39,7 +39,8 @@ __device__ __forceinline__ void sum_row(const FwdArgs<T>& a, const Piece& at, ui
     const T* vp = a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(head / s.group) * a.v.hs;
     const float base = m == -INFINITY ? 0.0f : m;
     float acc[DIM / 64] = {};
-    for (uint32_t j0 = 0; j0 <= i; j0 += 64) {
+    const uint32_t near = i >= s.window ? (i - s.window + 1) & ~63u : 0;         // where the window's keys start
+    for (uint32_t j0 = 0; j0 <= i; j0 = j0 + 64 >= s.sinks && j0 + 64 < near ? near : j0 + 64) {
         const uint32_t j = j0 + lane;
         const bool in = j <= i && (i - j < s.window || j < s.sinks);
         float p = 0.0f;
@@ -59,6 +60,12 @@ __device__ __forceinline__ void sum_row(const FwdArgs<T>& a, const Piece& at, ui
                 if (lane + 64 * n < s.dim)
                     acc[n] = __builtin_fmaf(w, float(vp[(j0 + k) * a.v.ld + lane + 64 * n]), acc[n]);
         }
+        bool open = false;
+#pragma unroll
+        for (int n = 0; n < DIM / 64; ++n)
+            open |= lane + 64 * n < s.dim && acc[n] == acc[n];
+        if (!__ballot(open))
+            break;
     }
 #pragma unroll
     for (int n = 0; n < DIM / 64; ++n)

@@ -32,6 +32,7 @@ struct FwdArgs {
 template <typename T, int DIM, int BIAS>
 __device__ __forceinline__ void sum_row(const FwdArgs<T>& a, const Piece& at, uint32_t head, uint32_t i, float m, float sum)
 {
+    typedef typename Vec8<T>::type VU __attribute__((aligned(sizeof(T))));
     const Shape& s = a.s;
     const uint32_t lane = threadIdx.x & 63;
     const T* q = a.q.p + (uint64_t(at.start) + i) * a.q.ld + uint64_t(head) * a.q.hs;
@@ -45,21 +46,32 @@ __device__ __forceinline__ void sum_row(const FwdArgs<T>& a, const Piece& at, ui
         const bool in = j <= i && (i - j < s.window || j < s.sinks);
         float p = 0.0f;
         if (in) {
-            for (uint32_t d = 0; d < s.dim; ++d)
-                p = __builtin_fmaf(float(q[d]), float(kp[j * a.k.ld + d]), p);
+            for (uint32_t d = 0; d < s.dim; d += 8) {
+                const VU x = *reinterpret_cast<const VU*>(q + d), y = *reinterpret_cast<const VU*>(kp + j * a.k.ld + d);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    p = __builtin_fmaf(float(x[e]), float(y[e]), p);
+            }
             p *= s.scale2;
             if (BIAS != kNoBias)
                 p += bias_value<T>(a.b, head, bucket_of(a.b.starts, a.b.count, i - j)) * kLog2e;
             p = __builtin_amdgcn_exp2f(p - base);
         }
-        for (uint64_t left = __ballot(in); left; left &= left - 1) {
-            const uint32_t k = __builtin_ctzll(left);
+        auto add = [&](uint32_t k) {
             const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, p), k));
 #pragma unroll
             for (int n = 0; n < DIM / 64; ++n)
                 if (lane + 64 * n < s.dim)
                     acc[n] = __builtin_fmaf(w, float(vp[(j0 + k) * a.v.ld + lane + 64 * n]), acc[n]);
-        }
+        };
+        uint64_t left = __ballot(in);
+        if (left == ~0ull)                         // loads ahead of the sums
+#pragma unroll 16
+            for (uint32_t k = 0; k < 64; ++k)
+                add(k);
+        else
+            for (; left; left &= left - 1)
+                add(__builtin_ctzll(left));
         bool open = false;
 #pragma unroll
         for (int n = 0; n < DIM / 64; ++n)

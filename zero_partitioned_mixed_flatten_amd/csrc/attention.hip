@@ -5,7 +5,22 @@
 //   s_ij = scale q_i.k_j + bias[h][bucket(i - j)]   for visible (i, j)
 //   o_i = sum_j exp(s_ij - lse_i) v_j,   lse_i = log sum_j exp(s_ij)
 //
-// One pass over the visible keys with a running maximum and sum of each row.
+// One pass over the visible keys with a running maximum and sum of each row.  A
+// workgroup owns 128 queries of a head, 32 a wave, and goes over tiles of 64 keys,
+// two in LDS: one is fetched under the other's products.  Of a wave's 32 x 32
+// scores each lane owns a query (attention.hpp), so a row's maximum and sum are
+// the lane's own but for one exchange, and the weights go from the first product's
+// registers to the second's operand.
+//
+// Bound by issue: the exponentials, masks and roundings of 32 x 32 scores (108
+// vector instructions at 64 columns, 150 at 128) and the products follow one
+// another in a wave, and waves overlap little of them.  Left out in trials at
+// 8 x 1024 positions: both products, 60% of the time stays; the tiles' fetches,
+// 85%.  8 x 1024 positions, 25 heads of 64: 46-49 us, 549-582 TFLOP/s of the visible
+// pairs.  2 x 4096 positions, 64 heads of 128 on 8 of keys, window 512: 204-217 us,
+// 599-637 TFLOP/s.  Operands read further ahead, two tiles a turn of the loop and
+// wave priorities gave nothing; four waves a SIMD spill; no bank conflicts are
+// counted.
 #include <type_traits>
 #include <vector>
 
@@ -27,8 +42,10 @@ struct FwdArgs {
 
 // The output of one row by a wave, from its maximum and sum, over the keys that
 // it sees and no others: 64 keys a time, a lane a key for their weights, then a
-// lane a column.  Slow (a row of 1024 keys some 50 us); for rows of a tile
-// beside an inf or NaN value that they do not see.
+// lane a column.  Slow, a row after the other (all rows of 2 x 4096 positions, 64
+// heads of 128, window 512: 38 ms for 0.2); for rows of a tile beside an inf or
+// NaN value that they do not see.  Rows that do see one come this way too, unless
+// their scores have one as well, and end where all their columns are NaN.
 template <typename T, int DIM, int BIAS>
 __device__ __forceinline__ void sum_row(const FwdArgs<T>& a, const Piece& at, uint32_t head, uint32_t i, float m, float sum)
 {

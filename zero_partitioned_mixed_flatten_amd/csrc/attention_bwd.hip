@@ -10,6 +10,19 @@
 // whose waves own keys (dk and dv).  That is 7 products a pair of tiles where
 // one pass would take 5, and no atomic sums, whose order would change the
 // results, nor a binary32 copy of dq.
+//
+// p and ds are rounded to the element type as operands of the products, half a
+// step each; the sums stay in binary32.  Where the keys share a common part, as
+// keys with a mean other than 0 do, the exact sum of ds over a row is 0 and takes it
+// out of dq, the roundings' is not: dq is then 1.5 times as far off as from unrounded
+// ds (2-norm, relative: 2.5e-3 to 1.7e-3 in bfloat16, 3.1e-4 to 2.1e-4 in binary16).
+//
+// Bound by issue, as the forward pass, with more products a pair of tiles.
+// 8 x 1024 positions, 25 heads of 64: dq 63-65 us, dk and dv 95-99, 408-427 TFLOP/s
+// of the formula's five products; 8191 packed positions, 64 heads of 128 on 8 of
+// keys, window 1024: 464-490 and 701-737 us under the profiler, 1062-1110 together
+// without, 509-532 TFLOP/s.  The bias adds 15 us to dk and dv, and its gradient's
+// sums by distance 48 to dq at 25 heads of 64.
 #include <type_traits>
 
 #include "attention.hpp"
@@ -58,7 +71,7 @@ __device__ __forceinline__ float lane_value(float v, uint32_t from)
 // (c - row + kSkewRows - 1) * kSkewPitch + row, what no element goes to stays 0.
 // Then a lane takes a distance.  Atomic additions in LDS, a distance a lane,
 // took longer than the products (bias_bwd at 8 x 1024, 25 heads: 313 us against
-// 196 for lane permutes of each register).
+// 196 for lane permutes of each register; so 111 for the pass, 64 without a bias).
 template <int DIM>
 constexpr int kSkewRows = DIM == 64 ? 32 : 8;      // 36 KB a workgroup, or 7.5: LDS for two workgroups a CU
 template <int DIM>
@@ -706,7 +719,9 @@ Deal deal(const Shape& s, bool ragged)
     Deal d{slots_of(s.tokens, s.sequences, ragged, kOwn), 1, 0};
     if (far_apart(s) && s.tokens > s.window)
         d.far_slots = slots_of(s.tokens, s.sequences, ragged, kFar);
-    // enough parts for two workgroups a CU, but none with fewer than four steps where a sequence has the mean length
+    // enough parts for two workgroups a CU, but none with fewer than four steps where a sequence has the mean length:
+    // a part costs a workgroup's start and 128 rows of binary32 sums written and read.  4099 positions, 3 key heads of
+    // 80, window 700: 105 items, five parts each: 74 us and 12 for the sums
     const uint64_t items = d.slots * (s.heads / s.group), length = s.tokens / s.sequences + 1;
     const uint64_t keys = s.window < length / 2 ? s.window : length / 2, steps = s.group * (keys / kTile + 2);
     const uint64_t wanted = (512 + items - 1) / items;

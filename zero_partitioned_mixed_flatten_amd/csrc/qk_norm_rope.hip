@@ -8,8 +8,13 @@
 // cosines and sines come from a table.  The backward pass takes rstd from x
 // again: a head's sum of squares is there before dy is.
 //
-// Bound by memory: one read and one write of everything, with both tensors in
-// one launch.
+// One read and one write of everything, with both tensors in one launch.  8192
+// tokens of 2 x 25 heads of 64, binary16: 22.6 us forward, 38.2 backward with the
+// fold of the weights' gradients (34 and 4), 4.7 and 4.2 TB/s; a plain copy of
+// the forward pass's bytes takes 17-19.  What is above the copy is a wave's
+// start (weights, position, angles: loads that wait for one another) and vector
+// instructions, 60% of the issue slots.  16384 tokens of 72 heads of 128, bfloat16,
+// backward: 168-172 us, 5.3 TB/s.
 #include <type_traits>
 
 #include "attention.hpp"

@@ -805,6 +805,8 @@ int zero_attention_buckets(uint32_t* starts, uint32_t buckets, uint32_t max_dist
  * of o and lse outside all sequences stay as they are.  NULL: sequences of
  * equal length, tokens / sequences.  (Indices out of order or range are
  * clamped to the tensors; which rows are then computed is undefined.)
+ * What rows hold that a token does not see, inf and NaN too, changes its result by
+ * roundings at most; an inf or NaN that it sees gives what its sums of products give.
  * The unnormalised weights are rounded to dtype for the product with v.
  * o must not overlap an input.
  * Errors: ZERO_EINVAL (NULL, a type, heads, dim or scale out of the above,
@@ -818,8 +820,8 @@ int zero_attention_fwd(void* o, uint64_t ld_o, uint64_t hs_o, float* lse, const 
                        const void* bias, int vec_dtype, const zero_attention_t* params, uint64_t tokens,
                        const int32_t* dev_offsets, uint64_t sequences, int dtype, void* stream);
 
-/* Bytes of device workspace zero_attention_bwd needs; 0 for no tokens or a
- * refused shape. */
+/* Bytes of device workspace zero_attention_bwd needs for these or fewer tokens
+ * in these or fewer sequences; 0 for no tokens or a refused shape. */
 size_t zero_attention_workspace_bytes(const zero_attention_t* params, uint64_t tokens, uint64_t sequences);
 
 /* The backward pass of zero_attention_fwd, from the o and lse it stored:
@@ -830,7 +832,9 @@ size_t zero_attention_workspace_bytes(const zero_attention_t* params, uint64_t t
  * ds are rounded to dtype for the products (ds for binary16 in units that go
  * by the size of do); dbias is a sum of the unrounded ds.  dbias (NULL: not
  * wanted): heads x buckets of grad_dtype, dtype or ZERO_F32, stored, or with
- * accumulate added to what is there, then rounded once.
+ * accumulate added to what is there, then rounded once.  An inf or NaN anywhere
+ * in a sequence may reach all gradients of that sequence, and dbias, as an
+ * overflowed backward pass does; other sequences' rows take nothing from it.
  * dq, dk and dv must not overlap an input or each other.  Rows outside all
  * sequences stay as they are.  workspace: device, 16-byte aligned, >=
  * zero_attention_workspace_bytes(params, tokens, sequences); contents need no

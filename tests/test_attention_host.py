@@ -6,6 +6,7 @@ import math
 import os
 from fractions import Fraction
 
+import numpy as np
 import pytest
 import torch
 
@@ -410,3 +411,20 @@ def test_a_refused_forward_leaves_the_last_one(Z):
     with pytest.raises(ValueError, match="device tensor"):
         p.forward(torch.zeros(6, 4, 8), torch.zeros(6, 2, 8), torch.zeros(6, 2, 8))
     assert p._last is None
+
+
+def test_workspace_holds_smaller_batches(Z):
+    """The workspace of a batch is enough for every smaller one: no more tokens in no more sequences."""
+    rng = np.random.default_rng(5)
+    for heads, kv, dim, window, sinks, buckets in [(64, 8, 128, 1024, 16, 0), (25, 25, 64, 0, 0, 32), (12, 3, 80, 700, 1, 24),
+                                                   (1, 1, 8, 0, 0, 0), (8, 1, 128, 0, 0, 4), (600, 600, 64, 100, 200, 0)]:
+        p = Z.attention_params(heads, kv, dim, window=window, sinks=sinks, starts=list(range(buckets)) or None)
+        for most_tokens, most_n in [(8192, 1), (8192, 8), (20000, 3), (129, 2), (70, 70)]:
+            whole = Z.zero_attention_workspace_bytes(p, most_tokens, most_n)
+            assert whole > 0
+            sizes = set(range(1, min(most_tokens, 300), 7)) | {int(t) for t in rng.integers(1, most_tokens + 1, 200)} | {most_tokens}
+            for tokens in sizes:
+                for n in range(1, most_n + 1):
+                    assert Z.zero_attention_workspace_bytes(p, tokens, n) <= whole, (heads, kv, tokens, n)
+        assert (Z.zero_qk_workspace_bytes(8192, heads, kv, dim) >=
+                max(Z.zero_qk_workspace_bytes(t, heads, kv, dim) for t in range(1, 8193)))

@@ -387,3 +387,17 @@ def test_gradients_into_a_partition():
         # a backward pass without the parameters' gradients gives the same at the inputs
         assert same(net.backward(x[3], grads=(None, None, None)), net.backward(x[3]))
     assert same(grads, total) and bool((part[:3] == 0).all())
+
+
+def test_place_takes_smaller_batches():
+    """A place made for a batch that needs no parts of dk and dv, with batches that do."""
+    place = Z.WindowAttention(8192, 64, 8, 128, window=256, sinks=4, max_sequences=4, dtype=BF16)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    for tokens, n in ((8192, 4), (1024, 1), (384, 3), (1, 1), (2048, 2)):
+        log("smaller", tokens, n)
+        q, k, v, do = (torch.randn(tokens, h, 128, generator=g, device="cuda").to(BF16) for h in (64, 8, 8, 64))
+        o = place.forward(q, k, v, sequences=n).clone()
+        got = place.backward(do)
+        alone = Z.WindowAttention(tokens, 64, 8, 128, window=256, sinks=4, max_sequences=n, dtype=BF16)
+        assert torch.equal(alone.forward(q, k, v, sequences=n), o)
+        assert same(alone.backward(do), got)

@@ -47,7 +47,7 @@ class WindowAttention:
         new = lambda h: torch.empty(self.max_tokens, h, dim, dtype=self.dtype, device=self.device)
         self._q, self._k, self._o = new(heads), new(kv_heads), new(heads)
         self._lse = torch.empty(heads * self.max_tokens, dtype=torch.float32, device=self.device)
-        # no fewer tokens or sequences ever need more; a call of other lengths checks its own need
+        # enough for fewer tokens or sequences, too
         need = max(16, Z.zero_qk_workspace_bytes(self.max_tokens, heads, kv_heads, dim),
                    Z.zero_attention_workspace_bytes(self.params, self.max_tokens, self.max_sequences))
         self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)

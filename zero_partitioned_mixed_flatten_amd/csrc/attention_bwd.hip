@@ -711,23 +711,30 @@ __global__ __launch_bounds__(kBlock) void fold_bias_kernel(void* dst, bool f32, 
 // ---- host side --------------------------------------------------------------------------
 // How the work on dk and dv is dealt out (see attention_dkv_kernel).
 struct Deal {
-    uint64_t slots, splits, far_slots;
+    uint64_t slots, splits, far_slots, parts;      // parts: of dk and dv, of 128 keys, that go to the workspace
 };
+
+constexpr uint64_t kItems = 512;
+
+// Parts with the fewest steps that one may have, where a sequence has `length` positions.
+uint64_t most_splits(const Shape& s, uint64_t length)
+{
+    const uint64_t keys = s.window < length / 2 ? s.window : length / 2, splits = s.group * (keys / kTile + 2) / 4;
+    return splits ? splits : 1;
+}
 
 Deal deal(const Shape& s, bool ragged)
 {
-    Deal d{slots_of(s.tokens, s.sequences, ragged, kOwn), 1, 0};
+    Deal d{slots_of(s.tokens, s.sequences, ragged, kOwn), 1, 0, 0};
     if (far_apart(s) && s.tokens > s.window)
         d.far_slots = slots_of(s.tokens, s.sequences, ragged, kFar);
     // enough parts for two workgroups a CU, but none with fewer than four steps where a sequence has the mean length:
     // a part costs a workgroup's start and 128 rows of binary32 sums written and read.  4099 positions, 3 key heads of
     // 80, window 700: 105 items, five parts each: 74 us and 12 for the sums
-    const uint64_t items = d.slots * (s.heads / s.group), length = s.tokens / s.sequences + 1;
-    const uint64_t keys = s.window < length / 2 ? s.window : length / 2, steps = s.group * (keys / kTile + 2);
-    const uint64_t wanted = (512 + items - 1) / items;
-    d.splits = wanted < steps / 4 ? wanted : steps / 4;
-    if (d.splits < 1)
-        d.splits = 1;
+    const uint64_t kv = s.heads / s.group, items = d.slots * kv;
+    const uint64_t wanted = (kItems + items - 1) / items, most = most_splits(s, s.tokens / s.sequences + 1);
+    d.splits = wanted < most ? wanted : most;
+    d.parts = d.splits > 1 ? items * d.splits : d.far_slots ? kv * s.sequences : 0;
     return d;
 }
 
@@ -750,19 +757,28 @@ Space space(const Shape& s, const Deal& d, uint32_t buckets, int dim)
     p.stats = take(uint64_t(s.heads) * s.tokens * 8);
     p.units = take(uint64_t(s.heads) * d.slots * kWaves * 4);
     p.partials = take(uint64_t(s.heads) * d.slots * buckets * 4);
-    p.near = take(d.splits > 1 ? kv * d.slots * d.splits * part : d.far_slots ? kv * s.sequences * part : 0);
+    p.near = take(d.parts * part);
     p.far = take(kv * d.far_slots * part);
     p.bytes = at;
     return p;
 }
 
-// Of the two forms of a call, with offsets and without.
+// Of a call with or without offsets, and of every smaller one: no more tokens in
+// no more sequences.  The slots of sequences of equal length are no more than
+// those with offsets; fewer items may be cut into more parts, of which i items
+// have at most i + kItems - 1, and i times what the longest sequence allows.
 uint64_t workspace_need(const Shape& s, uint32_t buckets)
 {
-    const int dim = s.dim <= 64 ? 64 : 128;
-    const uint64_t a = space(s, deal(s, true), buckets, dim).bytes;
-    const uint64_t b = s.tokens % s.sequences ? 0 : space(s, deal(s, false), buckets, dim).bytes;
-    return a > b ? a : b;
+    Deal d = deal(s, true);
+    const uint64_t kv = s.heads / s.group, items = d.slots * kv, cut = items < kItems ? items : kItems - 1;
+    const uint64_t most = most_splits(s, s.tokens + 1);
+    if (most > 1) {
+        const uint64_t parts = cut * most < cut + kItems - 1 ? cut * most : cut + kItems - 1;
+        d.parts = parts > d.parts ? parts : d.parts;
+    }
+    if (d.far_slots && kv * s.sequences > d.parts)
+        d.parts = kv * s.sequences;
+    return space(s, d, buckets, s.dim <= 64 ? 64 : 128).bytes;
 }
 
 template <typename T, int DIM, int BIAS, bool DIRECT>

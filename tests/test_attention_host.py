@@ -428,3 +428,12 @@ def test_workspace_holds_smaller_batches(Z):
                     assert Z.zero_attention_workspace_bytes(p, tokens, n) <= whole, (heads, kv, tokens, n)
         assert (Z.zero_qk_workspace_bytes(8192, heads, kv, dim) >=
                 max(Z.zero_qk_workspace_bytes(t, heads, kv, dim) for t in range(1, 8193)))
+
+
+def test_place_refuses_gradients_over_what_it_reads(Z):
+    p = Z.WindowAttention(16, 4, 2, 8, device="cpu")
+    q, k, v, o, do = (torch.zeros(7, h, 8, dtype=torch.float16) for h in (4, 2, 2, 4, 4))
+    p._last = (q, k, v, q.clone(), k.clone(), o, None, {}, dict(offsets=None, sequences=1))
+    for kw in (dict(dq=q), dict(dk=k), dict(dv=v), dict(dq=do), dict(dq=o)):
+        with pytest.raises(ValueError, match="still read"):
+            p.backward(do, **kw)

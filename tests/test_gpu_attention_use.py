@@ -401,3 +401,37 @@ def test_place_takes_smaller_batches():
         alone = Z.WindowAttention(tokens, 64, 8, 128, window=256, sinks=4, max_sequences=n, dtype=BF16)
         assert torch.equal(alone.forward(q, k, v, sequences=n), o)
         assert same(alone.backward(do), got)
+
+
+def test_place_with_rows_behind_the_last_sequence():
+    """Rows in no sequence add nothing to the weights' gradients, whatever the gradients' memory held, and get 0."""
+    heads, kv, dim, total, after = 6, 2, 64, 300, 37
+    g = torch.Generator(device="cuda").manual_seed(3)
+    wq, wk = (1 + 0.1 * torch.randn(dim, generator=g, device="cuda") for _ in range(2))
+    table = torch.empty(512, dim // 2, 2, device="cuda")
+    Z.zero_rope_table(table)
+    q, k, v, do = (torch.randn(total + after, h, dim, generator=g, device="cuda").half() for h in (heads, kv, kv, heads))
+    offsets = torch.tensor([0, 100, 100, total], dtype=torch.int32, device="cuda")
+    positions = torch.cat([torch.arange(100), torch.arange(200), torch.zeros(after)]).int().cuda()
+    results = []
+    for tokens in (total, total + after):
+        place = Z.WindowAttention(total + after, heads, kv, dim, wq, wk, table, window=64, sinks=2, max_sequences=3, dtype=F16)
+        place.forward(q[:tokens], k[:tokens], v[:tokens], offsets=offsets, positions=positions[:tokens])
+        dq, dk, dv = (torch.full((tokens, h, dim), math.nan, dtype=F16, device="cuda") for h in (heads, kv, kv))
+        dw = [torch.full((dim,), math.nan, device="cuda") for _ in range(2)]
+        place.backward(do[:tokens], dq=dq, dk=dk, dv=dv, grads=(dw[0], dw[1], None))
+        assert bool((dq[total:] == 0).all()) and bool((dk[total:] == 0).all()) and bool(dv[total:].isnan().all())
+        results.append((dq[:total], dk[:total], dv[:total], dw))
+    assert same(results[0][:3], results[1][:3])
+    # The weights' gradients are binary32 sums of the same n addends (and zeros), in orders that may differ: two such sums are
+    # at most 2 n 2^-24 times the sum of the addends' sizes apart.  An addend is an element of the attention's gradient, turned
+    # back (at most its size and its partner's), times one of the normed head.
+    nq, nk, o, lse = place._last[3:7]
+    aq, ak, av = torch.zeros_like(nq), torch.zeros_like(nk), torch.empty_like(nk)
+    Z.zero_attention_bwd(aq, ak, av, None, do, o, lse, nq, nk, v, place.params, offsets=offsets, sequences=3)
+    for a, b, x, g2 in ((results[0][3][0], results[1][3][0], q, aq), (results[0][3][1], results[1][3][1], k, ak)):
+        x, g2 = x[:total].double(), g2[:total].double().abs()
+        h = x * (x.square().mean(-1, keepdim=True) + 1e-6).rsqrt()
+        sizes = ((g2 + g2.roll(dim // 2, -1)) * h.abs()).sum((0, 1))
+        n = total * x.shape[1]
+        assert bool(((a - b).abs().double() <= 2 * n * 2.0 ** -24 * sizes).all()) and bool(b.abs().max() > 0)

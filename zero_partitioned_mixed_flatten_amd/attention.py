@@ -64,7 +64,8 @@ class WindowAttention:
         """The attention's output for q (tokens, heads, dim) and k, v (tokens, kv_heads, dim): slices of a joint
         projection are fine.  offsets: int32 on the device, the sequences' first tokens and the end; None:
         `sequences` of equal length.  positions: of the tokens in their sequences (int32 on the device), needed with
-        offsets and a rotation."""
+        offsets and a rotation.  Rows outside all sequences go through the norms like others, so they need finite values
+        and a position with angles; their rows of o stay as they are, their gradients at q and k are 0."""
         tokens = q.shape[0]
         n = sequences if offsets is None else offsets.numel() - 1
         if tokens > self.max_tokens or n > self.max_sequences:
@@ -98,6 +99,12 @@ class WindowAttention:
         q, k, v, nq, nk, o, lse, turn, where = self._last
         new = lambda t: torch.empty(t.shape, dtype=self.dtype, device=self.device)
         dq, dk, dv = new(q) if dq is None else dq, new(k) if dk is None else dk, new(v) if dv is None else dv
+        for t in (dq, dk, dv):
+            if t.numel() and any(t.data_ptr() == x.data_ptr() for x in (q, k, v, o, dout)):
+                raise ValueError("WindowAttention.backward: a gradient over a tensor that is still read")
+        if where["offsets"] is not None:            # rows outside all sequences: nothing for the norms' gradients
+            dq.zero_()
+            dk.zero_()
         dwq, dwk, dbias = (self.dwq, self.dwk, self.dbias) if grads is None else grads
         Z.zero_attention_bwd(dq, dk, dv, dbias, dout, o, lse, nq, nk, v, self.params, bias=self.bias, accumulate=accumulate,
                              workspace=self.workspace, **where)

@@ -435,3 +435,21 @@ def test_place_with_rows_behind_the_last_sequence():
         sizes = ((g2 + g2.roll(dim // 2, -1)) * h.abs()).sum((0, 1))
         n = total * x.shape[1]
         assert bool(((a - b).abs().double() <= 2 * n * 2.0 ** -24 * sizes).all()) and bool(b.abs().max() > 0)
+
+
+class WithoutBiasGradient(Call):
+    def bwd(self, o, lse, grad_dtype=None, accumulate=False, start=0.0, workspace=None):
+        outs = [self.out(h) for h in (self.hq, self.hk, self.hk)]
+        Z.zero_attention_bwd(outs[0][1], outs[1][1], outs[2][1], None, self.d["do"], o, lse, self.d["q"], self.d["k"], self.d["v"], self.params,
+                             bias=self.dbias, **self.where)
+        return [v for _, v in outs] + [None]
+
+
+@pytest.mark.parametrize("kind", [Call, WithoutBiasGradient])
+@pytest.mark.parametrize("lengths,starts", [([1300], [0, 3, 601]), ([700, 500], [0, 3, 601]), ([300, 90], [0, 1, 5, 250])])
+def test_bias_with_and_without_its_gradient(kind, lengths, starts):
+    """Last buckets far out, in sequences that are long and short against them; the gradient wanted or not."""
+    for dtype, dim in ((F16, 64), (BF16, 128)):
+        log("bias gradient", kind.__name__, lengths, starts, dim)
+        c = kind(lengths, 2, 1, dim, dtype, starts=starts, window=0, bias_dtype=F32)
+        c.check_bwd(*c.check_fwd())

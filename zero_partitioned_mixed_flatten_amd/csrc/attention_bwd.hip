@@ -79,6 +79,9 @@ constexpr int kSkewPitch = kSkewRows<DIM> + 4;
 template <int DIM>
 constexpr int kSkewSize = (31 + kSkewRows<DIM>) * kSkewPitch<DIM>;
 
+// Where the first wave's begin behind the table: 16-byte aligned.
+__host__ __device__ inline uint32_t sums_at(const Buckets& b) { return (table_size(b) + 3) / 4 * 4; }
+
 // ds[r] of lane (c, h): the pair at distance base + c - row_of(r, h).  Returns
 // the lane's part of the sum over the distances from `last` on.
 template <int DIM>
@@ -156,7 +159,7 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
     __shared__ alignas(16) T values[2][L::kElems];
     __shared__ typename std::conditional<BIAS == kLine, BiasLine, int>::type bias;
     __shared__ typename std::conditional<BIAS != kNoBias, BinsLds<BIAS>, int>::type sums;
-    extern __shared__ __attribute__((aligned(16))) float table[];               // BIAS == kTable: the waves' skewed rows, the table, the waves' sums by distance
+    extern __shared__ __attribute__((aligned(16))) float table[];               // BIAS == kTable: the table; with a gradient the waves' skewed rows and sums by distance
 
     const Shape& s = a.s;
     uint32_t head, slot;
@@ -220,17 +223,18 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
     delta *= unit;
 
     float beyond = 0.0f;                           // kTable: the bias of the last bucket
-    float* const skew = table + wave * kSkewSize<DIM>;                     // the wave's
-    float* const line = table + kWaves * kSkewSize<DIM>;
     const uint32_t last_start = BIAS == kTable ? a.b.starts[a.b.count - 1] : 0;
-    float* const by_distance = line + (BIAS == kTable ? table_size(a.b) + wave * last_start : 0);
+    float* const skews = table + (BIAS == kTable ? sums_at(a.b) : 0);           // where a.partials, from here on
+    float* const skew = skews + wave * kSkewSize<DIM>, * const by_distance = skews + kWaves * kSkewSize<DIM> + wave * last_start;
     if constexpr (BIAS == kTable) {
-        draw_table<T>(line, a.b, head);
+        draw_table<T>(table, a.b, head);
         beyond = bias_value<T>(a.b, head, a.b.count - 1) * kLog2e;
-        for (uint32_t x = lane; x < last_start; x += 64)
-            by_distance[x] = 0.0f;
-        for (uint32_t x = lane; x < kSkewSize<DIM>; x += 64)
-            skew[x] = 0.0f;
+        if (a.partials) {
+            for (uint32_t x = lane; x < last_start; x += 64)
+                by_distance[x] = 0.0f;
+            for (uint32_t x = lane; x < kSkewSize<DIM>; x += 64)
+                skew[x] = 0.0f;
+        }
     }
     if constexpr (BIAS == kLine) {
         load_line_values<T>(bias, a.b, head);
@@ -276,7 +280,7 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
                 f32x16 ds;
                 if (apart) {
                     const float* b = BIAS == kLine ? &bias_line(bias, buf)[kOwn - 1 - 32 * wave - c + 4 * h + 32 * sub]
-                                                   : line + line_at - 32 * sub;
+                                                   : table + line_at - 32 * sub;
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
                         ds[r] = __builtin_fmaf(x[r], s.scale2, b[BIAS == kLine ? row_of(r, 0) : kTile - 1 - row_of(r, 0)] - row_shift);
@@ -344,7 +348,7 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
                 sums.bins[wave][0] = far_sum;
             __syncthreads();
             // the waves' sums of each distance, then each bucket's distances: a wave a bucket
-            float* all = line + table_size(a.b);
+            float* all = skews + kWaves * kSkewSize<DIM>;
             for (uint32_t x = threadIdx.x; x < last_start; x += kBlock) {
                 float v = 0.0f;
 #pragma unroll
@@ -786,8 +790,9 @@ int launch(const BwdArgs<T>& a, hipStream_t stream)
 {
     const uint64_t near = a.splits > 1 ? uint64_t(a.slots) * a.splits * (a.s.heads / a.s.group) : a.keys.blocks(a.s);
     const uint32_t kv = a.s.heads / a.s.group, table = BIAS == kTable ? table_size(a.b) * 4 : 0;
+    const uint32_t sums = BIAS == kTable && a.partials ? (sums_at(a.b) + kWaves * (a.b.starts[a.b.count - 1] + kSkewSize<DIM>)) * 4 : 0;
     hipLaunchKernelGGL((attention_dq_kernel<T, DIM, BIAS, DIRECT>), dim3(uint32_t(a.queries.blocks(a.s))), dim3(kBlock),
-                       table + (BIAS == kTable ? kWaves * (a.b.starts[a.b.count - 1] + kSkewSize<DIM>) * 4 : 0), stream, a);
+                       sums ? sums : table, stream, a);
     int rc = launch_status();
     if (rc)
         return rc;
@@ -818,7 +823,12 @@ int run(Heads<void> dq, Heads<void> dk, Heads<void> dv, Heads<const void> dout, 
         constexpr bool kDirect = decltype(way)::value;
         if (!b.count)
             return launch<T, kDim, kNoBias, kDirect>(a, stream);
-        return table_fits(b) ? launch<T, kDim, kTable, kDirect>(a, stream) : launch<T, kDim, kLine, kDirect>(a, stream);
+        // with sums for more than some 512 distances (384 at 128 columns) LDS has one workgroup a CU.  25 heads of 64, the
+        // last bucket from 1000 on: table and line take 328 and 264 us at 8 x 1024 positions, where most tiles need the
+        // table, 919 and 1108 at 2 x 4096.  64 heads of 128 on 8, window 1024: 1863 and 1958
+        const uint32_t last = b.starts[b.count - 1];
+        const bool line = kDim == 64 && dbias && last > 512 && s.tokens / s.sequences < 2 * last;
+        return table_fits(b) && !line ? launch<T, kDim, kTable, kDirect>(a, stream) : launch<T, kDim, kLine, kDirect>(a, stream);
     };
     const std::integral_constant<int, 64> d64;
     const std::integral_constant<int, 128> d128;

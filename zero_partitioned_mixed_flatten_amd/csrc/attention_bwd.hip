@@ -206,7 +206,9 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
         norm = halves_sum(norm);
     }
     const uint64_t stat = uint64_t(head) * s.tokens + at.start + row;
-    const float lse = a.lse[stat] * kLog2e;
+    // Lanes past the sequence's end have its last row, but distances that none of its pairs has, and so any bias: their weights
+    // are 0 (a factor of 0 behind them would not do: exp of a bias far above the row's own scores is inf).
+    const float lse = live ? a.lse[stat] * kLog2e : INFINITY;
     float unit = 1.0f;
     if (kUnits<T>) {
         // a row of zeros gets a large unit, so that it does not set that of the rows beside it
@@ -247,7 +249,7 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
             bias.draw(buf, a.b.count, int(at.first + kOwn - 1) - int(tile * kTile), -1);
     };
     float far_sum = 0.0f;                          // ds of tiles whose distances are all in the last bucket
-    const float back = live ? 1.0f / unit : 0.0f;  // a power of two: exact
+    const float back = 1.0f / unit;                // a power of two: exact
 
     f32x16 acc[DIM / 32] = {};
     nk.put(keys[0]);

@@ -40,6 +40,11 @@ struct FwdArgs {
     Order order;
 };
 
+// binary16 has no numbers below 2^-24, and a row may have many keys whose weights are below that beside the largest: the
+// weights are formed in units of 2^-7, where the largest and the 2^8 that a maximum may lag behind leave room.
+template <typename T>
+constexpr float kLift = __is_same(T, _Float16) ? 7.0f : 0.0f;
+
 // The output of one row by a wave, from its maximum and sum, over the keys that
 // it sees and no others: 64 keys a time, a lane a key for their weights, then a
 // lane a column.  Slow, a row after the other (all rows of 2 x 4096 positions, 64
@@ -55,7 +60,7 @@ __device__ __forceinline__ void sum_row(const FwdArgs<T>& a, const Piece& at, ui
     const T* q = a.q.p + (uint64_t(at.start) + i) * a.q.ld + uint64_t(head) * a.q.hs;
     const T* kp = a.k.p + uint64_t(at.start) * a.k.ld + uint64_t(head / s.group) * a.k.hs;
     const T* vp = a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(head / s.group) * a.v.hs;
-    const float base = m == -INFINITY ? 0.0f : m;
+    const float base = (m == -INFINITY ? 0.0f : m) - kLift<T>;
     float acc[DIM / 64] = {};
     const uint32_t near = i >= s.window ? (i - s.window + 1) & ~63u : 0;         // where the window's keys start
     for (uint32_t j0 = 0; j0 <= i; j0 = j0 + 64 >= s.sinks && j0 + 64 < near ? near : j0 + 64) {
@@ -149,7 +154,7 @@ __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kerne
     };
 
     f32x16 acc[DIM / 32] = {};
-    float m = -INFINITY, sum = 0.0f;               // in units of log2; the sum over this half of the keys
+    float m = -INFINITY, sum = 0.0f;               // in units of log2; the sum over this half of the keys, in the weights' units
     nk.put(keys[0]);
     nv.put(values[0]);
     draw_line(t, 0);
@@ -212,16 +217,19 @@ __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kerne
                     for (int r = 0; r < 16; ++r)
                         acc[n][r] *= fall;
             }
-            const float base = (m == -INFINITY ? 0.0f : m) - shift;
+            const float base = (m == -INFINITY ? 0.0f : m) - shift - kLift<T>;
+            float part = 0.0f;                     // the tile's, so that small weights do not meet a large sum one by one
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     x[sub][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[sub][r], factor, -base));
-                    sum += x[sub][r];
+                    part += x[sub][r];
                 }
-            // the weights are rounded to the element type, as the matrix instruction takes them: half a step of each, where the
-            // binary32 sum they are divided by is of the unrounded ones
+            sum += part;
+            // the weights are rounded to the element type, as the matrix instruction takes them, where the binary32 sum they are
+            // divided by is of the unrounded ones: half a step of each, in binary16 of those above 2^-21 of the row's largest;
+            // below it 2^-32 of the largest at most
 #pragma unroll
             for (int step = 0; step < 4; ++step)
                 columns_times<T, DIM>(acc, values[buf], places, step, rounded<T>(x[step / 2], step % 2));
@@ -247,7 +255,7 @@ __global__ __launch_bounds__(kBlock, DIM == 64 ? 3 : 2) void attention_fwd_kerne
     uint32_t again = uint32_t(marked) | uint32_t(marked >> 32);
     store_columns<T, DIM>(a.o.p + uint64_t(at.start) * a.o.ld + uint64_t(head) * a.o.hs, a.o.ld, mine, live && !(again >> c & 1), s.dim, acc, 1.0f / sum);
     if (a.lse && live && h == 0)
-        a.lse[uint64_t(head) * s.tokens + at.start + mine] = (m + __builtin_amdgcn_logf(sum)) * kLn2;
+        a.lse[uint64_t(head) * s.tokens + at.start + mine] = (m + __builtin_amdgcn_logf(sum * __builtin_ldexpf(1.0f, -int(kLift<T>)))) * kLn2;
     for (; again; again &= again - 1) {
         const uint32_t i = __builtin_ctz(again);
         if (first + i < at.len)

@@ -830,7 +830,7 @@ size_t zero_attention_workspace_bytes(const zero_attention_t* params, uint64_t t
  *   dv_j = sum over i of p do_i,   dbias[h][b] = sum of ds over the pairs of b
  * dk and dv are sums over the query heads that share a key head, too.  p and
  * ds are rounded to dtype for the products (ds for binary16 in units that go
- * by the size of do); dbias is a sum of the unrounded ds.  dbias (NULL: not
+ * by the sizes of do, o and v, so that it does not overflow); dbias is a sum of the unrounded ds.  dbias (NULL: not
  * wanted): heads x buckets of grad_dtype, dtype or ZERO_F32, stored, or with
  * accumulate added to what is there, then rounded once.  An inf or NaN anywhere
  * in a sequence may reach all gradients of that sequence, and dbias, as an

@@ -1,5 +1,6 @@
-"""binary16's exponents in the attention kernels: keys with weights far below
-the row's largest, which are many."""
+"""binary16's exponents in the attention kernels: values as large as binary16
+holds, whose gradients fit, and keys with weights far below the row's largest,
+which are many."""
 import math
 
 import pytest
@@ -9,6 +10,76 @@ import attention_oracle as A
 from test_gpu_attention import BF16, F16, Call, close
 
 pytestmark = pytest.mark.gpu
+
+
+def log(*a):
+    print("[units]", *a, flush=True)
+
+
+class LargeValues(Call):
+    """Rows `at` of v up to binary16's largest values, along dout and against it in turn; dout small enough for gradients that
+    fit."""
+
+    def __init__(self, *args, at=slice(None), size=30000.0, **kw):
+        super().__init__(*args, do_scale=1e-3, **kw)
+        sign = 1.0 - 2.0 * (torch.arange(self.tokens) % 2)[:, None, None]
+        self.v[at] = ((0.5 + self.v.double().abs()) * sign * size).clamp(-65504.0, 65504.0).to(self.dtype)[at]
+        self.do.abs_()
+        self.d["v"].copy_(self.v)
+        self.d["do"].copy_(self.do)
+
+
+@pytest.mark.parametrize("size", [100.0, 1000.0, 30000.0, 1e6])
+def test_large_values(size):
+    """ds may leave binary16 in units of |do|, by up to 2 |v|; what it gives at the queries and keys does not."""
+    for dim in (64, 128):
+        log("large values", size, dim)
+        c = LargeValues([300, 40], 2, 1, dim, F16, size=size)
+        got = c.check_bwd(*c.check_fwd())
+        assert all(bool(t.isfinite().all()) for t in got[:3])
+
+
+@pytest.mark.parametrize("starts", [[0, 1, 20], [0, 3, 601]])
+def test_large_values_with_a_bias(starts):
+    """The gradient of the bias takes each ds once."""
+    for dim in (64, 128):
+        log("large values, bias", starts, dim)
+        c = LargeValues([300, 40], 2, 2, dim, F16, starts=starts, bias_dtype=torch.float32)
+        got = c.check_bwd(*c.check_fwd())
+        assert all(bool(t.isfinite().all()) for t in got)
+
+
+def test_large_values_of_the_first_tokens():
+    """Queries long behind the window, taken apart; many query heads a key head; rows off 16-byte places."""
+    for lengths, heads, kv, dim, layout in (([2500], 2, 1, 64, "plain"), ([1400, 30], 8, 1, 128, "plain"), ([1300], 2, 2, 64, "odd")):
+        log("large values, first tokens", lengths, dim)
+        c = LargeValues(lengths, heads, kv, dim, F16, window=70, sinks=9, layout=layout, at=slice(0, 40))
+        got = c.check_bwd(*c.check_fwd())
+        assert all(bool(t.isfinite().all()) for t in got[:3])
+
+
+def test_large_values_elsewhere():
+    """A sequence's results are the same bits whatever another's values are."""
+    plain = LargeValues([200, 200], 2, 1, 64, F16, at=slice(0, 0))
+    o, lse = plain.fwd()
+    want = plain.bwd(o, lse)
+    c = LargeValues([200, 200], 2, 1, 64, F16, at=slice(0, 200))
+    o2, lse2 = c.check_fwd()
+    got = c.check_bwd(o2, lse2)
+    assert torch.equal(o2[200:], o[200:]) and all(torch.equal(a[200:], b[200:]) for a, b in zip(got[:3], want[:3]))
+
+
+def test_overflow_stays_an_overflow():
+    """Gradients that do not fit binary16 are inf, and NaN goes in and comes out."""
+    c = LargeValues([200], 1, 1, 64, F16)
+    c.do = (c.do.double() * 1e6).to(F16)
+    c.d["do"].copy_(c.do)
+    o, lse = c.fwd()
+    assert bool(c.bwd(o, lse)[0].isinf().any())
+    c = Call([200], 1, 1, 64, F16)
+    c.d["v"][7, 0, 3] = math.nan
+    o, lse = c.fwd()
+    assert bool(c.bwd(o, lse)[0].isnan().any())
 
 
 class Far(Call):

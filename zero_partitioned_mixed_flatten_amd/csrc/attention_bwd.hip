@@ -35,9 +35,41 @@ namespace {
 // 2^-k where 2^k is about |do_i| (its 2-norm, a power of two, so the products
 // are exact), for dk the largest of the rows so far, and p of the dv product in
 // units of 2^-6.  bfloat16 needs neither.
+// In those units |do_i| is below 1 and ds below |v_j| + |o_i|, which may leave
+// binary16 (2^20.6 for 128 columns of its largest values). So the units also go
+// by what of |o_i| is past 2^14, and for dk by what of the wave's largest |v_j|
+// is. The dq pass has the values only as they come: rows whose ds leave binary16
+// there have sums of inf or NaN, and are summed again in binary32 (sum_dq_row).
 template <typename T>
 constexpr bool kUnits = __is_same(T, _Float16);
 constexpr float kWeightUnits = 64.0f, kWeightShift = 6.0f;
+constexpr int kRoom = 14;                          // log2 of what |v_j| and |o_i| may come to each
+
+// The power of two by which a vector of this squared 2-norm is too large, at most 1.
+__device__ __forceinline__ float room(float norm)
+{
+    const int over = ((__builtin_amdgcn_frexp_expf(norm) + 1) >> 1) - kRoom;
+    return __builtin_ldexpf(1.0f, over > 0 ? -over : 0);
+}
+
+// The units by |do_i|, from its square.  A row of zeros gets a large one, so that it does not set that of the rows beside it.
+__device__ __forceinline__ float unit_of(float norm)
+{
+    return norm > 0.0f ? __builtin_ldexpf(1.0f, -((__builtin_amdgcn_frexp_expf(norm) + 1) >> 1)) : 0x1p60f;
+}
+
+// The lane's part of the sum of squares of its operand's column.
+template <typename T, int DIM>
+__device__ __forceinline__ float squares(const Operand<T, DIM>& x)
+{
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < DIM / 16; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            sum = __builtin_fmaf(float(x.v[k][j]), float(x.v[k][j]), sum);
+    return sum;
+}
 
 template <typename T>
 struct BwdArgs {
@@ -45,7 +77,7 @@ struct BwdArgs {
     Heads<const T> dout, o, q, k, v;
     const float* lse;
     f32x2* stats;                                  // heads x tokens: lse in units of log2 (binary16: less the weights' units), delta
-    float* units;                                  // heads x slots x waves: 2^-k of 32 rows' largest (binary16)
+    float* units;                                  // heads x slots x waves: the smallest units of 32 rows (binary16)
     float* partials;                               // heads x slots x buckets
     float* near;                                   // parts of dk and dv (see dkv_items)
     float* far;
@@ -151,8 +183,59 @@ __device__ __forceinline__ void add_diagonals_of(const BiasLine& bias, float* bi
 }
 __device__ __forceinline__ void add_diagonals_of(int, float*, uint32_t, int, const float (&)[16]) {}
 
+// dq of one row by a wave, all in binary32 but the store: 64 keys a time, a lane
+// a key for their ds, then a lane a column.  Slow, as the forward pass's rows
+// beside an inf (attention.hip).  lse is in units of log2.
+template <typename T, int DIM, int BIAS>
+__device__ __forceinline__ void sum_dq_row(const BwdArgs<T>& a, const Piece& at, uint32_t head, uint32_t i, float lse, float delta)
+{
+    typedef typename Vec8<T>::type VU __attribute__((aligned(sizeof(T))));
+    const Shape& s = a.s;
+    const uint32_t lane = threadIdx.x & 63;
+    const T* q = a.q.p + (uint64_t(at.start) + i) * a.q.ld + uint64_t(head) * a.q.hs;
+    const T* dout = a.dout.p + (uint64_t(at.start) + i) * a.dout.ld + uint64_t(head) * a.dout.hs;
+    const T* kp = a.k.p + uint64_t(at.start) * a.k.ld + uint64_t(head / s.group) * a.k.hs;
+    const T* vp = a.v.p + uint64_t(at.start) * a.v.ld + uint64_t(head / s.group) * a.v.hs;
+    float acc[DIM / 64] = {};
+    const uint32_t near = i >= s.window ? (i - s.window + 1) & ~63u : 0;         // where the window's keys start
+    for (uint32_t j0 = 0; j0 <= i; j0 = j0 + 64 >= s.sinks && j0 + 64 < near ? near : j0 + 64) {
+        const uint32_t j = j0 + lane;
+        const bool in = j <= i && (i - j < s.window || j < s.sinks);
+        float ds = 0.0f;
+        if (in) {
+            float x = 0.0f, dp = 0.0f;
+            for (uint32_t d = 0; d < s.dim; d += 8) {
+                const VU qx = *reinterpret_cast<const VU*>(q + d), kx = *reinterpret_cast<const VU*>(kp + j * a.k.ld + d);
+                const VU ox = *reinterpret_cast<const VU*>(dout + d), vx = *reinterpret_cast<const VU*>(vp + j * a.v.ld + d);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x = __builtin_fmaf(float(qx[e]), float(kx[e]), x);
+                    dp = __builtin_fmaf(float(ox[e]), float(vx[e]), dp);
+                }
+            }
+            float shift = -lse;
+            if (BIAS != kNoBias)
+                shift += bias_value<T>(a.b, head, bucket_of(a.b.starts, a.b.count, i - j)) * kLog2e;
+            ds = __builtin_amdgcn_exp2f(__builtin_fmaf(x, s.scale2, shift)) * (dp - delta);
+        }
+        for (uint64_t left = __ballot(in); left; left &= left - 1) {
+            const uint32_t k = __builtin_ctzll(left);
+            const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ds), k));
+#pragma unroll
+            for (int n = 0; n < DIM / 64; ++n)
+                if (lane + 64 * n < s.dim)
+                    acc[n] = __builtin_fmaf(w, float(kp[(j0 + k) * a.k.ld + lane + 64 * n]), acc[n]);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < DIM / 64; ++n)
+        if (lane + 64 * n < s.dim)
+            a.dq.p[(uint64_t(at.start) + i) * a.dq.ld + uint64_t(head) * a.dq.hs + lane + 64 * n] = T(acc[n] * s.scale);
+}
+
+// Without a bias 64 columns leave registers for three waves a SIMD: 63-66 us at 8 x 1024 positions, 25 heads, where two take 79.
 template <typename T, int DIM, int BIAS, bool DIRECT>
-__global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
+__global__ __launch_bounds__(kBlock, DIM == 64 && BIAS == kNoBias ? 3 : 2) void attention_dq_kernel(BwdArgs<T> a)
 {
     typedef Tile<DIM> L;
     __shared__ alignas(16) T keys[2][L::kElems];
@@ -191,28 +274,24 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
     Operand<T, DIM> q, dout;
     load_operand<T, DIM>(q, a.q.p + uint64_t(at.start) * a.q.ld + uint64_t(head) * a.q.hs, a.q.ld, row, s.dim);
     load_operand<T, DIM>(dout, a.dout.p + uint64_t(at.start) * a.dout.ld + uint64_t(head) * a.dout.hs, a.dout.ld, row, s.dim);
-    float delta = 0.0f, norm = 0.0f;
+    float delta = 0.0f, unit = 1.0f;
     {
         Operand<T, DIM> o;
         load_operand<T, DIM>(o, a.o.p + uint64_t(at.start) * a.o.ld + uint64_t(head) * a.o.hs, a.o.ld, row, s.dim);
 #pragma unroll
         for (int k = 0; k < DIM / 16; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 8; ++j)
                 delta = __builtin_fmaf(float(dout.v[k][j]), float(o.v[k][j]), delta);
-                norm = __builtin_fmaf(float(dout.v[k][j]), float(dout.v[k][j]), norm);
-            }
         delta = halves_sum(delta);
-        norm = halves_sum(norm);
+        if (kUnits<T>)
+            unit = unit_of(halves_sum(squares<T, DIM>(dout))) * room(halves_sum(squares<T, DIM>(o)));
     }
     const uint64_t stat = uint64_t(head) * s.tokens + at.start + row;
     // Lanes past the sequence's end have its last row, but distances that none of its pairs has, and so any bias: their weights
     // are 0 (a factor of 0 behind them would not do: exp of a bias far above the row's own scores is inf).
     const float lse = live ? a.lse[stat] * kLog2e : INFINITY;
-    float unit = 1.0f;
     if (kUnits<T>) {
-        // a row of zeros gets a large unit, so that it does not set that of the rows beside it
-        unit = norm > 0.0f ? __builtin_ldexpf(1.0f, -((__builtin_amdgcn_frexp_expf(norm) + 1) >> 1)) : 0x1p60f;
         float least = unit;
 #pragma unroll
         for (int step = 16; step; step >>= 1)
@@ -331,8 +410,27 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dq_kernel(BwdArgs<T> a)
         nv.put(values[buf]);
         draw_line(t, buf);
     }
-    store_columns<T, DIM>(a.dq.p + uint64_t(at.start) * a.dq.ld + uint64_t(head) * a.dq.hs, a.dq.ld, mine, live, s.dim, acc,
-                          s.scale / unit);
+    uint32_t again = 0;                            // rows whose ds were too large for binary16 (not those with an inf or NaN of their own)
+    if (kUnits<T>) {
+        float probe = 0.0f;
+#pragma unroll
+        for (int n = 0; n < DIM / 32; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                probe = __builtin_fmaf(acc[n][r], 0.0f, probe);
+        const uint64_t marked = __ballot(live && probe != probe && fabsf(lse) < INFINITY && fabsf(delta) < INFINITY);
+        again = uint32_t(marked) | uint32_t(marked >> 32);
+    }
+    store_columns<T, DIM>(a.dq.p + uint64_t(at.start) * a.dq.ld + uint64_t(head) * a.dq.hs, a.dq.ld, mine, live && !(again >> c & 1), s.dim,
+                          acc, s.scale / unit);
+    if (kUnits<T>) {
+        delta /= unit;
+        for (; again; again &= again - 1) {
+            const uint32_t i = __builtin_ctz(again);
+            sum_dq_row<T, DIM, BIAS>(a, at, head, first + i, __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, lse), i)),
+                                     __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, delta), i)));
+        }
+    }
     if constexpr (BIAS == kLine)
         if (a.partials) {
             __syncthreads();
@@ -528,11 +626,21 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
         __syncthreads();
     }
     f32x16 dk[DIM / 32] = {}, dv[DIM / 32] = {};
-    float unit = 0x1p60f;                          // of dk's sums
+    float unit = 0x1p60f;                          // of dk's sums, but for v_room
     int buf = 0;
     if (step < step_end) {
         ask(0, head, t);
         place(0, t);
+    }
+    float v_room = 1.0f;                           // the wave's
+    if (kUnits<T>) {
+        if (kValuesInLds)
+            load_operand<T, DIM>(v, vp, a.v.ld, row, s.dim);
+        float norm = halves_sum(squares<T, DIM>(v));
+#pragma unroll
+        for (int step = 16; step; step >>= 1)
+            norm = fmaxf(norm, __shfl_xor(norm, step));
+        v_room = room(norm);
     }
     while (step < step_end) {
         uint32_t next = t + 1, next_head = head;
@@ -557,7 +665,7 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
                     for (int r = 0; r < 16; ++r)
                         dk[n][r] *= by;
             }
-            const float ds_unit = unit * (1.0f / kWeightUnits);
+            const float ds_unit = unit * (v_room / kWeightUnits);
             const bool apart = BIAS == kLine || (BIAS == kTable && !all_beyond(t));
             const float* line = BIAS == kLine ? bias_line(bias, buf) + kOwn - 1 - 32 * wave - c + 4 * h
                                               : table + (int(i0) - int(mine) + kTableBefore + 4 * int(h));
@@ -624,7 +732,7 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
         place(buf, t);
     }
     const bool live = mine < at.len;
-    const float k_unit = kUnits<T> ? s.scale / unit : s.scale, v_unit = kUnits<T> ? 1.0f / kWeightUnits : 1.0f;
+    const float k_unit = kUnits<T> ? s.scale / (unit * v_room) : s.scale, v_unit = kUnits<T> ? 1.0f / kWeightUnits : 1.0f;
     if (!out) {
         store_columns<T, DIM>(a.dk.p + uint64_t(at.start) * a.dk.ld + uint64_t(kv) * a.dk.hs, a.dk.ld, mine, live, s.dim, dk, k_unit);
         store_columns<T, DIM>(a.dv.p + uint64_t(at.start) * a.dv.ld + uint64_t(kv) * a.dv.hs, a.dv.ld, mine, live, s.dim, dv, v_unit);

@@ -122,3 +122,35 @@ def test_many_small_weights(dtype, dim):
         e[:, 1] += i * 2.0 ** -32 * 64.0
     close(o[:, 0], want, A.stored(e, want, dtype), "o")
     close(lse[0], 18.0 + torch.log1p(w), 18.0 * 8 * A.U + 2 * (34 + N / 64) * A.U + 16 * A.U + 0 * w, "lse")
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+def test_gradients_of_many_small_weights(dtype, dim):
+    """Weights of 2^-31, each ds below binary16's smallest number in units of |do|."""
+    g = 1024.0
+    c = Far(N, dim, dtype, 21.5, g)
+    o, lse = c.fwd()
+    dq, dk, dv, _ = c.bwd(o, lse)
+    i = torch.arange(N, dtype=torch.float64)
+    p = torch.exp(-lse[0].cpu().double())                                # of every key but the first, whose score is 21.5
+    delta = g * o[:, 0, 1].cpu().double()
+    ds, ds0 = p * (64.0 * g - delta), -torch.exp(21.5 - lse[0].cpu().double()) * delta
+    # binary32: the score and the difference (21.5, 8 u each) and the exponential, of ds; then half a step; binary16 2^-25 in
+    # units of 2^-4 over twice |do|
+    r = (8 * 2 * 21.5 + 16) * A.U + A.HALF[dtype]
+    lost = 2.0 ** -25 * 2.0 ** -4 * 2.0 * g if dtype == F16 else 0.0
+    depth = 2 * N * A.U
+    want, e = (torch.zeros(N, dim, dtype=torch.float64) for _ in range(2))
+    want[:, 0], want[:, 2] = 0.125 * 32.0 * ds0, 0.125 * 8.0 * i * ds
+    e[:, 0] = 0.125 * 32.0 * (ds0.abs() * (r + depth) + lost)
+    e[:, 2] = 0.125 * 8.0 * i * (ds * (r + depth) + lost)
+    close(dq[:, 0], want, A.stored(e, want, dtype), "dq")
+    after = lambda t: t.flip(0).cumsum(0).flip(0)                        # sums over the queries from the key on
+    q0 = 21.5 / 4.0
+    want, e = (torch.zeros(N, dim, dtype=torch.float64) for _ in range(2))
+    want[:, 0] = 0.125 * q0 * after(ds)
+    e[:, 0] = 0.125 * q0 * after(ds * (r + depth) + lost)
+    want[0, 0] = 0.125 * q0 * ds0.sum()
+    e[0, 0] = 0.125 * q0 * (ds0.abs() * (r + depth) + lost).sum()
+    close(dk[:, 0], want, A.stored(e, want, dtype), "dk")

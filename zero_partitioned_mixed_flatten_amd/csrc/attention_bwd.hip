@@ -32,18 +32,20 @@ namespace attention {
 namespace {
 
 // binary16 has few exponents below a gradient's: ds is formed in units of
-// 2^-k where 2^k is about |do_i| (its 2-norm, a power of two, so the products
-// are exact), for dk the largest of the rows so far, and p of the dv product in
-// units of 2^-6.  bfloat16 needs neither.
-// In those units |do_i| is below 1 and ds below |v_j| + |o_i|, which may leave
-// binary16 (2^20.6 for 128 columns of its largest values). So the units also go
-// by what of |o_i| is past 2^14, and for dk by what of the wave's largest |v_j|
-// is. The dq pass has the values only as they come: rows whose ds leave binary16
-// there have sums of inf or NaN, and are summed again in binary32 (sum_dq_row).
+// 2^-(k + 4) where 2^k is about |do_i| (its 2-norm, a power of two, so the
+// products are exact), for dk the largest of the rows so far, and p of the dv
+// product in units of 2^-6.  bfloat16 needs neither.
+// In units of 2^-k |do_i| is below 1 and ds below |v_j| + |o_i|, which may leave
+// binary16 (2^20.6 for 128 columns of its largest values), and where a few keys
+// have most of a row's weight, the ds of the many others are small beside it:
+// the 4 makes room below, and above it the units also go by what of |o_i| is
+// past 2^10, for dk by what of the wave's largest |v_j| is.  The dq pass has the
+// values only as they come: rows whose ds leave binary16 there have sums of inf
+// or NaN, and are summed again in binary32 (sum_dq_row).
 template <typename T>
 constexpr bool kUnits = __is_same(T, _Float16);
 constexpr float kWeightUnits = 64.0f, kWeightShift = 6.0f;
-constexpr int kRoom = 14;                          // log2 of what |v_j| and |o_i| may come to each
+constexpr int kBelow = 4, kRoom = 14 - kBelow;     // 2^kRoom: what |v_j| and |o_i| may come to each
 
 // The power of two by which a vector of this squared 2-norm is too large, at most 1.
 __device__ __forceinline__ float room(float norm)
@@ -55,7 +57,7 @@ __device__ __forceinline__ float room(float norm)
 // The units by |do_i|, from its square.  A row of zeros gets a large one, so that it does not set that of the rows beside it.
 __device__ __forceinline__ float unit_of(float norm)
 {
-    return norm > 0.0f ? __builtin_ldexpf(1.0f, -((__builtin_amdgcn_frexp_expf(norm) + 1) >> 1)) : 0x1p60f;
+    return norm > 0.0f ? __builtin_ldexpf(1.0f, kBelow - ((__builtin_amdgcn_frexp_expf(norm) + 1) >> 1)) : 0x1p60f;
 }
 
 // The lane's part of the sum of squares of its operand's column.

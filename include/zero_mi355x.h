@@ -820,6 +820,17 @@ int zero_attention_fwd(void* o, uint64_t ld_o, uint64_t hs_o, float* lse, const 
                        const void* bias, int vec_dtype, const zero_attention_t* params, uint64_t tokens,
                        const int32_t* dev_offsets, uint64_t sequences, int dtype, void* stream);
 
+/* Enqueue 0 in the rows of x (tokens x heads x dim elements of dtype, ZERO_F16,
+ * ZERO_BF16 or ZERO_F32) that are in no sequence: those before dev_offsets[0]
+ * and from dev_offsets[sequences] on, which zero_attention_fwd and
+ * zero_attention_bwd leave as they are.
+ * Errors: ZERO_EINVAL (NULL, a type, heads = 0, dim no multiple of 8),
+ *         ZERO_EALIGN, ZERO_ERANGE (dim > 128, more than 65535 heads or 2^30
+ *         tokens or sequences, ld or hs < dim or > 2^50, an extent > 2^56),
+ *         ZERO_EHIP. */
+int zero_attention_clear_rows(void* x, uint64_t ld, uint64_t hs, uint64_t tokens, uint32_t heads, uint32_t dim,
+                              int dtype, const int32_t* dev_offsets, uint64_t sequences, void* stream);
+
 /* Bytes of device workspace zero_attention_bwd needs for these or fewer tokens
  * in these or fewer sequences; 0 for no tokens or a refused shape. */
 size_t zero_attention_workspace_bytes(const zero_attention_t* params, uint64_t tokens, uint64_t sequences);

@@ -15,7 +15,8 @@ from ._lib import (EXPORTS, NORM_PARTIAL_BYTES, ONEBIT_STATE_BYTES, RNG_BYTES, S
                    read_onebit_state, zero_onebit_state_init,
                    zero_onebit_step, zero_onebit_workspace_bytes,
                    zero_rope_table, zero_qk_norm_rope_fwd, zero_qk_workspace_bytes, zero_qk_norm_rope_bwd,
-                   zero_attention_buckets, zero_attention_fwd, zero_attention_workspace_bytes, zero_attention_bwd,
+                   zero_attention_buckets, zero_attention_fwd, zero_attention_clear_rows, zero_attention_workspace_bytes,
+                   zero_attention_bwd,
                    attention_params, ZeroError, lib, make_segments, read_state, zero_bucket_segments, zero_decide_workspace_bytes,
                    zero_flatten_bucket, zero_flatten_buckets, zero_flatten_norm_bucket,
                    zero_flatten_norm_bucket_f32, zero_flatten_norm_partials, zero_norm_workspace_bytes, zero_shard_adam_step,
@@ -46,4 +47,4 @@ __all__ = ["EXPORTS", "NORM_PARTIAL_BYTES", "STATE_BYTES", "ZERO_BF16", "ZERO_F1
            "zero_dropout_layernorm_fwd", "zero_dropout_layernorm_bwd", "zero_layer_workspace_bytes", "LayerRng",
            "ResidualNorm", "ZERO_MAX_BUCKETS", "AttentionParams", "attention_params", "zero_rope_table",
            "zero_qk_norm_rope_fwd", "zero_qk_workspace_bytes", "zero_qk_norm_rope_bwd", "zero_attention_buckets",
-           "zero_attention_fwd", "zero_attention_workspace_bytes", "zero_attention_bwd", "WindowAttention"]
+           "zero_attention_fwd", "zero_attention_clear_rows", "zero_attention_workspace_bytes", "zero_attention_bwd", "WindowAttention"]

@@ -27,7 +27,8 @@ EXPORTS = ("zero_status_string", "zero_state_bytes", "zero_bucket_segments", "ze
            "zero_rng_advance", "zero_dropout_fwd", "zero_dropout_bwd", "zero_layer_workspace_bytes",
            "zero_layernorm_fwd", "zero_layernorm_bwd", "zero_dropout_layernorm_fwd", "zero_dropout_layernorm_bwd",
            "zero_rope_table", "zero_qk_norm_rope_fwd", "zero_qk_workspace_bytes", "zero_qk_norm_rope_bwd",
-           "zero_attention_buckets", "zero_attention_fwd", "zero_attention_workspace_bytes", "zero_attention_bwd")
+           "zero_attention_buckets", "zero_attention_fwd", "zero_attention_clear_rows", "zero_attention_workspace_bytes",
+           "zero_attention_bwd")
 NORM_PARTIAL_BYTES = 16
 
 
@@ -173,6 +174,7 @@ def lib():
         L.zero_attention_buckets.argtypes = [C.POINTER(u32), u32, u32]
         params = C.POINTER(AttentionParams)
         L.zero_attention_fwd.argtypes = heads + [vp] + heads * 3 + [vp, i32, params, u64, vp, u64, i32, vp]
+        L.zero_attention_clear_rows.argtypes = heads + [u64, u32, u32, i32, vp, u64, vp]
         L.zero_attention_workspace_bytes.argtypes = [params, u64, u64]
         L.zero_attention_workspace_bytes.restype = C.c_size_t
         L.zero_attention_bwd.argtypes = heads * 3 + [vp, i32, i32] + heads * 2 + [vp] + heads * 3 + [
@@ -980,6 +982,15 @@ def zero_attention_fwd(o, lse, q, k, v, params: AttentionParams, bias=None, offs
     bias_, btype = c.vector(bias, (hq, params.buckets))
     c.check(lib().zero_attention_fwd(*c.heads(o, hq), _lse(c, lse, hq), *c.heads(q, hq), *c.heads(k, hk), *c.heads(v, hk),
                                      bias_, btype, params, c.rows, *_sequences(c, offsets, sequences), c.code, c.stream))
+
+
+def zero_attention_clear_rows(x, offsets, stream=None) -> None:
+    """0 in the rows of x (tokens, heads, dim) that are in none of the sequences that offsets gives."""
+    c = _HeadsCall("zero_attention_clear_rows", x, stream)
+    if offsets is None:
+        raise ValueError(f"{c.fn}: expected offsets")
+    n = c.shape[1]
+    c.check(lib().zero_attention_clear_rows(*c.heads(x, n), c.rows, n, c.dim, c.code, *_sequences(c, offsets, 0), c.stream))
 
 
 def zero_attention_bwd(dq, dk, dv, dbias, dout, o, lse, q, k, v, params: AttentionParams, bias=None, offsets=None,

@@ -65,7 +65,7 @@ class WindowAttention:
         projection are fine.  offsets: int32 on the device, the sequences' first tokens and the end; None:
         `sequences` of equal length.  positions: of the tokens in their sequences (int32 on the device), needed with
         offsets and a rotation.  Rows outside all sequences go through the norms like others, so they need finite values
-        and a position with angles; their rows of o stay as they are, their gradients at q and k are 0."""
+        and a position with angles; their rows of the place's own output are 0, those of a given o stay as they are."""
         tokens = q.shape[0]
         n = sequences if offsets is None else offsets.numel() - 1
         if tokens > self.max_tokens or n > self.max_sequences:
@@ -78,12 +78,15 @@ class WindowAttention:
         if self.table is not None and positions is None and tokens // n > self.table.shape[0]:
             raise ValueError(f"WindowAttention.forward: sequences of {tokens // n} tokens, angles of {self.table.shape[0]}")
         nq, nk = self._q[:tokens], self._k[:tokens]
-        o = self._o[:tokens] if o is None else o
+        own = o is None
+        o = self._o[:tokens] if own else o
         lse = self._lse[:self.params.heads * tokens].view(self.params.heads, tokens)
         turn = dict(eps=self.eps, positions=positions, period=0 if offsets is not None else tokens // n,
                     interleaved=self.interleaved)
         where = dict(offsets=offsets, sequences=n)
         self._last = None                           # the buffers are the new call's from here on
+        if own and offsets is not None:
+            Z.zero_attention_clear_rows(o, offsets)
         Z.zero_qk_norm_rope_fwd(nq, nk, q, k, self.wq, self.wk, self.table, **turn)
         Z.zero_attention_fwd(o, lse, nq, nk, v, self.params, bias=self.bias, **where)
         self._last = (q, k, v, nq, nk, o, lse, turn, where)
@@ -92,19 +95,21 @@ class WindowAttention:
     def backward(self, dout, dq=None, dk=None, dv=None, grads=None, accumulate: bool = False):
         """(dq, dk, dv): the gradients at the last forward pass's q, k and v from the output's.  The parameters' go to
         self.dwq, self.dwk and self.dbias, or to `grads`, three tensors (None: not wanted) such as slices of a
-        partition; accumulate adds them to what is there."""
+        partition; accumulate adds them to what is there.  In rows outside all sequences dq and dk are 0, and so is dv
+        where it is made here; those of a given dv stay as they are."""
         import torch
         if self._last is None:
             raise ValueError("WindowAttention.backward: no forward pass")
         q, k, v, nq, nk, o, lse, turn, where = self._last
         new = lambda t: torch.empty(t.shape, dtype=self.dtype, device=self.device)
-        dq, dk, dv = new(q) if dq is None else dq, new(k) if dk is None else dk, new(v) if dv is None else dv
+        own_dv = dv is None
+        dq, dk, dv = new(q) if dq is None else dq, new(k) if dk is None else dk, new(v) if own_dv else dv
         for t in (dq, dk, dv):
             if t.numel() and any(t.data_ptr() == x.data_ptr() for x in (q, k, v, o, dout)):
                 raise ValueError("WindowAttention.backward: a gradient over a tensor that is still read")
         if where["offsets"] is not None:            # rows outside all sequences: nothing for the norms' gradients
-            dq.zero_()
-            dk.zero_()
+            for t in (dq, dk, dv) if own_dv else (dq, dk):
+                Z.zero_attention_clear_rows(t, where["offsets"])
         dwq, dwk, dbias = (self.dwq, self.dwk, self.dbias) if grads is None else grads
         Z.zero_attention_bwd(dq, dk, dv, dbias, dout, o, lse, nq, nk, v, self.params, bias=self.bias, accumulate=accumulate,
                              workspace=self.workspace, **where)

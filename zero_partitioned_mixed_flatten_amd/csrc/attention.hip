@@ -337,6 +337,28 @@ int run_fwd(void* o, uint64_t ld_o, uint64_t hs_o, float* lse, const void* q, ui
     return s.dim <= 64 ? launch<T, 64, false>(a, stream) : launch<T, 128, false>(a, stream);
 }
 
+// 0 in the rows before the first sequence and behind the last, 8 elements a
+// thread: bound by the bytes of those rows, or where there are none by the launch.
+template <typename T>
+__global__ __launch_bounds__(kBlock) void clear_rows_kernel(Heads<T> x, uint64_t tokens, uint32_t heads, uint32_t dim, const int32_t* offsets,
+                                                            uint64_t sequences)
+{
+    typedef T V0 __attribute__((ext_vector_type(8)));
+    typedef V0 V __attribute__((aligned(sizeof(T))));
+    auto offset = [&](uint64_t i) {
+        const int32_t o = offsets[i];
+        return o < 0 ? uint64_t(0) : uint64_t(o) < tokens ? uint64_t(o) : tokens;
+    };
+    const uint64_t first = offset(0), end = offset(sequences);
+    const uint32_t pieces = dim / 8;
+    const uint64_t row = uint64_t(heads) * pieces, items = (first + (end < tokens ? tokens - (end > first ? end : first) : 0)) * row;
+    for (uint64_t i = uint64_t(blockIdx.x) * kBlock + threadIdx.x; i < items; i += uint64_t(gridDim.x) * kBlock) {
+        const uint64_t r = i / row, token = r < first ? r : r - first + (end > first ? end : first);
+        const uint32_t rest = uint32_t(i - r * row), head = rest / pieces;
+        *reinterpret_cast<V*>(x.p + token * x.ld + head * x.hs + (rest - head * pieces) * 8) = V0{};
+    }
+}
+
 // A natural number of any size, for comparing powers.
 struct Natural {
     std::vector<uint32_t> d{1};
@@ -405,6 +427,30 @@ extern "C" int zero_attention_buckets(uint32_t* starts, uint32_t buckets, uint32
         return ZERO_ENOMEM;
     }
     return ZERO_OK;
+}
+
+extern "C" int zero_attention_clear_rows(void* x, uint64_t ld, uint64_t hs, uint64_t tokens, uint32_t heads, uint32_t dim, int dtype,
+                                         const int32_t* dev_offsets, uint64_t sequences, void* stream)
+{
+    if (!layer::dtype_ok(dtype) || !heads || !dim || dim % 8 || !dev_offsets)
+        return ZERO_EINVAL;
+    if (!is_aligned(dev_offsets, 4))
+        return ZERO_EALIGN;
+    if (heads > kMaxHeads || dim > 128 || tokens > kMaxTokens || sequences > kMaxTokens)
+        return ZERO_ERANGE;
+    const int rc = check_heads(x, ld, hs, tokens, heads, dim, dtype);
+    if (rc || !tokens)
+        return rc;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const uint64_t most = (tokens * heads * (dim / 8) + kBlock - 1) / kBlock;
+    const dim3 grid(uint32_t(most < 1024 ? most : 1024));
+    if (dtype == ZERO_F32)
+        hipLaunchKernelGGL(clear_rows_kernel<float>, grid, dim3(kBlock), 0, s, Heads<float>{static_cast<float*>(x), ld, hs}, tokens, heads, dim,
+                           dev_offsets, sequences);
+    else                                           // the zeros of both 16-bit types are the same bits
+        hipLaunchKernelGGL(clear_rows_kernel<_Float16>, grid, dim3(kBlock), 0, s, Heads<_Float16>{static_cast<_Float16*>(x), ld, hs}, tokens,
+                           heads, dim, dev_offsets, sequences);
+    return launch_status();
 }
 
 extern "C" int zero_attention_fwd(void* o, uint64_t ld_o, uint64_t hs_o, float* lse, const void* q, uint64_t ld_q, uint64_t hs_q,

@@ -85,6 +85,11 @@ struct Buckets {
 // finds its sequence from the offsets alone, and some slots stay empty.
 // Offsets out of order or out of range are clamped: they give wrong tiles, but
 // none outside the tensors.
+// Where only sequences of at least `apart` tokens matter, they get the slots
+// from offsets[s] / own + offsets[s] / apart on: another such sequence begins at
+// least `apart` tokens later, so these are as many as it has pieces, too, and
+// tokens / own + tokens / apart in all.  A shorter one has slots that the long
+// one after it may share: the last sequence is found that has a slot.
 struct Piece {
     uint32_t seq, start, len;                      // the sequence: its index, first token, tokens
     uint32_t first;                                // the piece's first row in the sequence
@@ -98,7 +103,7 @@ __host__ __device__ inline uint64_t slots_of(uint32_t tokens, uint32_t sequences
     return uint64_t(sequences) * ((tokens / sequences + own - 1) / own);
 }
 
-__device__ __forceinline__ bool find_piece(const Shape& s, uint32_t slot, uint32_t own, Piece* out)
+__device__ __forceinline__ bool find_piece(const Shape& s, uint32_t slot, uint32_t own, Piece* out, uint32_t apart = 0)
 {
     if (!s.offsets) {
         const uint32_t per = (s.length + own - 1) / own;
@@ -117,7 +122,8 @@ __device__ __forceinline__ bool find_piece(const Shape& s, uint32_t slot, uint32
     uint32_t seq = 0;                              // the number of sequences whose slots begin at or before this one
     for (uint32_t base = 0; base < s.sequences; base += 64) {
         const uint32_t i = base + lane;
-        const bool before = i < s.sequences && offset(i < s.sequences ? i : 0) / own + i <= slot;
+        const uint32_t at = offset(i < s.sequences ? i : 0);
+        const bool before = i < s.sequences && at / own + (apart ? at / apart : i) <= slot;
         const uint32_t n = __popcll(__ballot(before));
         seq += n;
         if (n < 64)
@@ -130,7 +136,7 @@ __device__ __forceinline__ bool find_piece(const Shape& s, uint32_t slot, uint32
     out->seq = seq;
     out->start = start;
     out->len = end > start ? end - start : 0;
-    out->slots = start / own + seq;
+    out->slots = start / own + (apart ? start / apart : seq);
     out->first = (slot - out->slots) * own;
     return slot >= out->slots && uint64_t(slot - out->slots) * own < out->len;
 }

@@ -85,7 +85,7 @@ struct BwdArgs {
     float* far;
     Shape s;
     Buckets b;
-    uint32_t slots, splits, far_slots;
+    uint32_t slots, splits, far_slots, near_slots, long_from, apart;             // see Deal
     Order queries, keys;                           // of the two passes
 };
 
@@ -480,9 +480,10 @@ __global__ __launch_bounds__(kBlock, DIM == 64 && BIAS == kNoBias ? 3 : 2) void 
 //   - few keys in all: the list is then cut into `splits` parts, whose binary32
 //     sums go to the workspace and are added up by dkv_sum_kernel;
 //   - a window with first tokens that stay visible: the piece of keys that holds
-//     them is seen by every query of the sequence.  Its list ends with the
-//     window, and the queries behind are taken kFar at a time by workgroups of
-//     their own, whose sums are added likewise.
+//     them is seen by every query of the sequence.  Where there are queries
+//     behind the window, in sequences of at least long_from tokens, its list
+//     ends with the window, and the queries behind are taken kFar at a time by
+//     workgroups of their own, whose sums are added likewise.
 constexpr uint32_t kFar = 1024;
 
 // Rows of the tiles of queries.  A wave has its keys, and 64 columns take 32
@@ -529,7 +530,7 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
     float* out = nullptr;                          // binary32 sums: dk of the piece's rows, then dv; NULL: dk and dv themselves
     if (is_far) {
         kv = blockIdx.x / a.far_slots;
-        if (!find_piece(s, blockIdx.x - kv * a.far_slots, kFar, &at))
+        if (!find_piece(s, blockIdx.x - kv * a.far_slots, kFar, &at, a.apart) || at.len < a.long_from)
             return;
         first_key = 0;
         begin = (near_end(s, 0, at.len) + kQ - 1) / kQ;
@@ -554,8 +555,8 @@ __global__ __launch_bounds__(kBlock, 2) void attention_dkv_kernel(BwdArgs<T> a)
         end = (near_end(s, at.first, at.len) + kQ - 1) / kQ;
         if (a.splits > 1)
             out = a.near + uint64_t(block) * (2 * kOwn * DIM);
-        else if (a.far_slots && at.first == 0)
-            out = a.near + (uint64_t(kv) * s.sequences + at.seq) * (2 * kOwn * DIM);
+        else if (a.far_slots && at.first == 0 && at.len >= a.long_from)
+            out = a.near + (uint64_t(kv) * a.near_slots + (a.apart ? at.start / a.apart : at.seq)) * (2 * kOwn * DIM);
     }
     const uint32_t lane = threadIdx.x & 63, c = lane % 32, h = lane / 32;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -766,18 +767,19 @@ __global__ __launch_bounds__(kSumRows* DIM / 8) void dkv_sum_kernel(BwdArgs<T> a
     typedef V __attribute__((aligned(sizeof(T)))) VU;
     const Shape& s = a.s;
     const uint32_t kv = blockIdx.y;
+    const uint32_t slot = blockIdx.x / (kOwn / kSumRows);          // of the pieces, or of the long sequences' first ones
     Piece at;
-    if (!find_piece(s, blockIdx.x / (kOwn / kSumRows), kOwn, &at) || (a.splits == 1 && at.first))
+    if (a.splits > 1 ? !find_piece(s, slot, kOwn, &at) : !find_piece(s, slot, 1u << 31, &at, a.apart) || at.len < a.long_from)
         return;
     const uint32_t local = blockIdx.x % (kOwn / kSumRows) * kSumRows + threadIdx.x / (DIM / 8), col = threadIdx.x % (DIM / 8) * 8;
     const uint32_t row = at.first + local;
     if (row >= at.len || col >= s.dim)
         return;
     constexpr uint64_t kPart = 2 * kOwn * DIM;
-    const float* near = a.near + (a.splits > 1 ? (uint64_t(kv) * a.slots + blockIdx.x / (kOwn / kSumRows)) * a.splits : uint64_t(kv) * s.sequences + at.seq) * kPart;
+    const float* near = a.near + (a.splits > 1 ? (uint64_t(kv) * a.slots + slot) * a.splits : uint64_t(kv) * a.near_slots + slot) * kPart;
     uint32_t far_begin = 0, far_end = 0;
-    if (a.far_slots && at.first == 0) {
-        const uint32_t slots = s.offsets ? at.start / kFar + at.seq : at.seq * ((s.length + kFar - 1) / kFar);
+    if (a.far_slots && at.first == 0 && at.len >= a.long_from) {
+        const uint32_t slots = s.offsets ? at.start / kFar + (a.apart ? at.start / a.apart : at.seq) : at.seq * ((s.length + kFar - 1) / kFar);
         constexpr uint32_t kQ = kRows<DIM>;
         const uint32_t behind = (near_end(s, 0, at.len) + kQ - 1) / kQ * kQ;
         if (behind < at.len) {
@@ -827,7 +829,11 @@ __global__ __launch_bounds__(kBlock) void fold_bias_kernel(void* dst, bool f32, 
 // ---- host side --------------------------------------------------------------------------
 // How the work on dk and dv is dealt out (see attention_dkv_kernel).
 struct Deal {
-    uint64_t slots, splits, far_slots, parts;      // parts: of dk and dv, of 128 keys, that go to the workspace
+    uint64_t slots, splits;
+    uint64_t far_slots, near_slots, long_from;     // of the queries behind the window, and of the pieces of keys that they see, in
+                                                   // sequences of at least long_from tokens
+    uint64_t apart;                                // of find_piece() for these: long_from where that gives fewer slots, else 0
+    uint64_t parts;                                // of dk and dv, of 128 keys, that go to the workspace
 };
 
 constexpr uint64_t kItems = 512;
@@ -841,16 +847,22 @@ uint64_t most_splits(const Shape& s, uint64_t length)
 
 Deal deal(const Shape& s, bool ragged)
 {
-    Deal d{slots_of(s.tokens, s.sequences, ragged, kOwn), 1, 0, 0};
-    if (far_apart(s) && s.tokens > s.window)
-        d.far_slots = slots_of(s.tokens, s.sequences, ragged, kFar);
+    Deal d{slots_of(s.tokens, s.sequences, ragged, kOwn), 1, 0, 0, 0, 0, 0};
+    const uint64_t behind = uint64_t(s.window) + kOwn;             // near_end() is before the end from here on
+    if (far_apart(s) && (ragged ? s.tokens : s.length) >= behind) {
+        d.long_from = behind;
+        const uint64_t most = s.tokens / behind;                   // such sequences
+        d.apart = ragged && most < s.sequences ? behind : 0;
+        d.far_slots = d.apart ? s.tokens / kFar + most : slots_of(s.tokens, s.sequences, ragged, kFar);
+        d.near_slots = d.apart ? most : s.sequences;
+    }
     // enough parts for two workgroups a CU, but none with fewer than four steps where a sequence has the mean length:
     // a part costs a workgroup's start and 128 rows of binary32 sums written and read.  4099 positions, 3 key heads of
     // 80, window 700: 105 items, five parts each: 74 us and 12 for the sums
     const uint64_t kv = s.heads / s.group, items = d.slots * kv;
     const uint64_t wanted = (kItems + items - 1) / items, most = most_splits(s, s.tokens / s.sequences + 1);
     d.splits = wanted < most ? wanted : most;
-    d.parts = d.splits > 1 ? items * d.splits : d.far_slots ? kv * s.sequences : 0;
+    d.parts = d.splits > 1 ? items * d.splits : kv * d.near_slots;
     return d;
 }
 
@@ -881,7 +893,7 @@ Space space(const Shape& s, const Deal& d, uint32_t buckets, int dim)
 
 // Of a call with or without offsets, and of every smaller one: no more tokens in
 // no more sequences.  The slots of sequences of equal length are no more than
-// those with offsets; fewer items may be cut into more parts, of which i items
+// those with offsets (which hold for any lengths); fewer items may be cut into more parts, of which i items
 // have at most i + kItems - 1, and i times what the longest sequence allows.
 uint64_t workspace_need(const Shape& s, uint32_t buckets)
 {
@@ -892,8 +904,8 @@ uint64_t workspace_need(const Shape& s, uint32_t buckets)
         const uint64_t parts = cut * most < cut + kItems - 1 ? cut * most : cut + kItems - 1;
         d.parts = parts > d.parts ? parts : d.parts;
     }
-    if (d.far_slots && kv * s.sequences > d.parts)
-        d.parts = kv * s.sequences;
+    if (kv * d.near_slots > d.parts)
+        d.parts = kv * d.near_slots;
     return space(s, d, buckets, s.dim <= 64 ? 64 : 128).bytes;
 }
 
@@ -913,7 +925,7 @@ int launch(const BwdArgs<T>& a, hipStream_t stream)
     rc = launch_status();
     if (rc || (a.splits == 1 && !a.far_slots))
         return rc;
-    hipLaunchKernelGGL((dkv_sum_kernel<T, DIM>), dim3(a.slots * (kOwn / kSumRows), kv), dim3(kSumRows * DIM / 8), 0, stream, a);
+    hipLaunchKernelGGL((dkv_sum_kernel<T, DIM>), dim3((a.splits > 1 ? a.slots : a.near_slots) * (kOwn / kSumRows), kv), dim3(kSumRows * DIM / 8), 0, stream, a);
     return launch_status();
 }
 
@@ -929,7 +941,7 @@ int run(Heads<void> dq, Heads<void> dk, Heads<void> dv, Heads<const void> dout, 
     auto part = [&](uint64_t at) { return reinterpret_cast<float*>(workspace + at); };
     const BwdArgs<T> a{out(dq), out(dk), out(dv), in(dout), in(o), in(q), in(k), in(v), lse, reinterpret_cast<f32x2*>(workspace + p.stats),
                        part(p.units), dbias ? part(p.partials) : nullptr, part(p.near), part(p.far), s, b, uint32_t(d.slots), uint32_t(d.splits),
-                       uint32_t(d.far_slots), Order(s, s.heads, d.slots), Order(s, s.heads / s.group, d.slots)};
+                       uint32_t(d.far_slots), uint32_t(d.near_slots), uint32_t(d.long_from), uint32_t(d.apart), Order(s, s.heads, d.slots), Order(s, s.heads / s.group, d.slots)};
     auto go = [&](auto dim, auto way) {
         constexpr int kDim = decltype(dim)::value;
         constexpr bool kDirect = decltype(way)::value;

@@ -65,6 +65,15 @@ __device__ __forceinline__ const float* turn_row(const QkArgs<T>& a, uint64_t to
     return a.table + (known ? pos : 0) * a.rot;
 }
 
+// A dimension of a launch holds fewer than 2^32 threads: more workgroups than
+// 2^22 are dealt out over two.
+dim3 flat_grid(uint64_t blocks)
+{
+    const uint64_t x = blocks < (uint64_t(1) << 22) ? blocks : uint64_t(1) << 22;
+    return dim3(uint32_t(x), uint32_t((blocks + x - 1) / x));
+}
+__device__ __forceinline__ uint64_t flat_block() { return uint64_t(blockIdx.y) * gridDim.x + blockIdx.x; }
+
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v)
 {
@@ -408,7 +417,7 @@ __global__ __launch_bounds__(kQkBlock) void qk_fwd_kernel(QkArgs<T> a)
 {
     constexpr int kPer = Part2<T>::kPer, kItems = kQkBlock / LANES;
     const uint32_t heads = a.side[0].heads + a.side[1].heads;
-    const uint64_t base = uint64_t(blockIdx.x) * kItems, token0 = base / heads;
+    const uint64_t base = flat_block() * kItems, token0 = base / heads;
     const uint32_t local = uint32_t(base - token0 * heads) + threadIdx.x / LANES, skip = local / heads;
     const uint64_t token = token0 + skip;
     uint32_t head = local - skip * heads;
@@ -670,7 +679,7 @@ __global__ __launch_bounds__(kQkFoldCols* kQkFoldRows) void qk_fold_kernel(void*
 
 __global__ __launch_bounds__(256) void rope_table_kernel(float* table, uint64_t entries, uint32_t half, double log2_base)
 {
-    const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x;
+    const uint64_t i = flat_block() * 256 + threadIdx.x;
     if (i >= entries)
         return;
     const uint64_t pos = i / half;
@@ -801,9 +810,9 @@ void launch_part(const QkArgs<T>& a, uint64_t blocks, bool past, hipStream_t s)
             hipLaunchKernelGGL((qk_bwd_kernel<T, LANES, STYLE, false>), dim3(uint32_t(blocks)), dim3(kQkBlock), 0, s, a);
     } else {
         if (past)
-            hipLaunchKernelGGL((qk_fwd_kernel<T, LANES, STYLE, true>), dim3(uint32_t(blocks)), dim3(kQkBlock), 0, s, a);
+            hipLaunchKernelGGL((qk_fwd_kernel<T, LANES, STYLE, true>), flat_grid(blocks), dim3(kQkBlock), 0, s, a);
         else
-            hipLaunchKernelGGL((qk_fwd_kernel<T, LANES, STYLE, false>), dim3(uint32_t(blocks)), dim3(kQkBlock), 0, s, a);
+            hipLaunchKernelGGL((qk_fwd_kernel<T, LANES, STYLE, false>), flat_grid(blocks), dim3(kQkBlock), 0, s, a);
     }
 }
 
@@ -968,7 +977,7 @@ extern "C" int zero_rope_table(float* table, uint64_t positions, uint32_t rot, d
     const uint64_t entries = positions * (rot / 2);
     if (!entries)
         return ZERO_OK;
-    hipLaunchKernelGGL(rope_table_kernel, dim3(uint32_t((entries + 255) / 256)), dim3(256), 0, static_cast<hipStream_t>(stream), table, entries,
+    hipLaunchKernelGGL(rope_table_kernel, flat_grid((entries + 255) / 256), dim3(256), 0, static_cast<hipStream_t>(stream), table, entries,
                        rot / 2, log2(base));
     return launch_status();
 }

@@ -813,8 +813,9 @@ int zero_attention_buckets(uint32_t* starts, uint32_t buckets, uint32_t max_dist
  *         sequences = 0 with tokens, tokens not a multiple of sequences
  *         without offsets, starts not ascending from 0, bias without buckets
  *         or the other way round), ZERO_EALIGN, ZERO_ERANGE (more than 2^30
- *         tokens or sequences, heads * (tokens / 128 + sequences) >= 2^27, ld
- *         or hs < dim or > 2^50, an extent > 2^56, dim > 128), ZERO_EHIP. */
+ *         tokens or sequences, heads * (tokens / 128 + sequences) >= 2^24 - 8
+ *         (without offsets: heads times the sequences' pieces of 128 tokens),
+ *         ld or hs < dim or > 2^50, an extent > 2^56, dim > 128), ZERO_EHIP. */
 int zero_attention_fwd(void* o, uint64_t ld_o, uint64_t hs_o, float* lse, const void* q, uint64_t ld_q, uint64_t hs_q,
                        const void* k, uint64_t ld_k, uint64_t hs_k, const void* v, uint64_t ld_v, uint64_t hs_v,
                        const void* bias, int vec_dtype, const zero_attention_t* params, uint64_t tokens,
@@ -850,7 +851,10 @@ size_t zero_attention_workspace_bytes(const zero_attention_t* params, uint64_t t
  * sequences stay as they are.  workspace: device, 16-byte aligned, >=
  * zero_attention_workspace_bytes(params, tokens, sequences); contents need no
  * initialisation; calls that share it must be ordered.
- * Errors: as for zero_attention_fwd, and ZERO_ERANGE for a workspace too small. */
+ * Errors: as for zero_attention_fwd, and ZERO_ERANGE for a workspace too small,
+ *         or where first tokens are seen by so many queries behind the window
+ *         that kv_heads * (tokens / 128 + tokens / 1024 + 2 * sequences) >=
+ *         2^24 - 8, or 2^21 sequences or more have such queries. */
 int zero_attention_bwd(void* dq, uint64_t ld_dq, uint64_t hs_dq, void* dk, uint64_t ld_dk, uint64_t hs_dk, void* dv,
                        uint64_t ld_dv, uint64_t hs_dv, void* dbias, int grad_dtype, int accumulate, const void* dout,
                        uint64_t ld_dout, uint64_t hs_dout, const void* o, uint64_t ld_o, uint64_t hs_o,

@@ -141,6 +141,9 @@ __device__ __forceinline__ bool find_piece(const Shape& s, uint32_t slot, uint32
     return slot >= out->slots && uint64_t(slot - out->slots) * own < out->len;
 }
 
+// A dimension of a launch holds fewer than 2^32 threads: with kBlock a workgroup fewer workgroups than this.
+constexpr uint64_t kMostBlocks = (uint64_t(1) << 32) / kBlock;
+
 // Which head and piece a block takes.  Blocks go to the eight dies in turn;
 // neighbours that share a head's keys belong on one, whose L2 then holds them.
 // Sequences of equal length: each die has its own (sequence, head) pairs and
@@ -154,7 +157,7 @@ struct Order {
     __host__ Order(const Shape& s, uint32_t h, uint64_t n) : heads(h), slots(uint32_t(n)), pairs(0)
     {
         const uint64_t all = uint64_t(h) * s.sequences;
-        if (!s.offsets && (all >= 64 || all % 8 == 0))
+        if (!s.offsets && (all >= 64 || all % 8 == 0) && (all + 7) / 8 * 8 * (n / s.sequences) < kMostBlocks)
             pairs = uint32_t((all + 7) / 8);
     }
     __host__ uint64_t blocks(const Shape& s) const
@@ -642,7 +645,7 @@ __device__ __forceinline__ void load_line_values(BiasLine& line, const Buckets& 
 // ---- host side --------------------------------------------------------------------------
 constexpr uint64_t kMaxTokens = uint64_t(1) << 30;
 constexpr uint32_t kMaxHeads = 65535;
-constexpr uint64_t kMaxPieces = uint64_t(1) << 27;
+constexpr uint64_t kMaxPieces = kMostBlocks - 8;   // of all heads; Order rounds up to the dies
 
 // Rows that go straight into LDS: at 16-byte aligned places.
 inline bool direct(const void* p, uint64_t ld, uint64_t hs)

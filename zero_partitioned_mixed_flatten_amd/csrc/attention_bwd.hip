@@ -909,10 +909,25 @@ uint64_t workspace_need(const Shape& s, uint32_t buckets)
     return space(s, d, buckets, s.dim <= 64 ? 64 : 128).bytes;
 }
 
+// Workgroups of attention_dkv_kernel but for the far ones.
+template <typename T>
+uint64_t near_blocks(const BwdArgs<T>& a)
+{
+    return a.splits > 1 ? uint64_t(a.slots) * a.splits * (a.s.heads / a.s.group) : a.keys.blocks(a.s);
+}
+
+// Whether the launches after the first fit theirs, too (dkv_sum_kernel has kBlock threads or half as many).
+template <typename T>
+bool launches_fit(const BwdArgs<T>& a)
+{
+    return near_blocks(a) + uint64_t(a.far_slots) * (a.s.heads / a.s.group) < kMostBlocks &&
+           uint64_t(a.splits > 1 ? a.slots : a.near_slots) * (kOwn / kSumRows) < kMostBlocks;
+}
+
 template <typename T, int DIM, int BIAS, bool DIRECT>
 int launch(const BwdArgs<T>& a, hipStream_t stream)
 {
-    const uint64_t near = a.splits > 1 ? uint64_t(a.slots) * a.splits * (a.s.heads / a.s.group) : a.keys.blocks(a.s);
+    const uint64_t near = near_blocks(a);
     const uint32_t kv = a.s.heads / a.s.group, table = BIAS == kTable ? table_size(a.b) * 4 : 0;
     const uint32_t sums = BIAS == kTable && a.partials ? (sums_at(a.b) + kWaves * (a.b.starts[a.b.count - 1] + kSkewSize<DIM>)) * 4 : 0;
     hipLaunchKernelGGL((attention_dq_kernel<T, DIM, BIAS, DIRECT>), dim3(uint32_t(a.queries.blocks(a.s))), dim3(kBlock),
@@ -942,6 +957,8 @@ int run(Heads<void> dq, Heads<void> dk, Heads<void> dv, Heads<const void> dout, 
     const BwdArgs<T> a{out(dq), out(dk), out(dv), in(dout), in(o), in(q), in(k), in(v), lse, reinterpret_cast<f32x2*>(workspace + p.stats),
                        part(p.units), dbias ? part(p.partials) : nullptr, part(p.near), part(p.far), s, b, uint32_t(d.slots), uint32_t(d.splits),
                        uint32_t(d.far_slots), uint32_t(d.near_slots), uint32_t(d.long_from), uint32_t(d.apart), Order(s, s.heads, d.slots), Order(s, s.heads / s.group, d.slots)};
+    if (!launches_fit(a))
+        return ZERO_ERANGE;
     auto go = [&](auto dim, auto way) {
         constexpr int kDim = decltype(dim)::value;
         constexpr bool kDirect = decltype(way)::value;
@@ -981,10 +998,11 @@ extern "C" size_t zero_attention_workspace_bytes(const zero_attention_t* params,
     Buckets b;
     if (!tokens || !sequences || !params)
         return 0;
-    // the larger of a call with offsets and one without, where there is one; the pointers are only tested for NULL
+    // the larger of a call with offsets and one without, where they are not refused; the pointers are only tested for NULL
     const void* bias = params->buckets ? params : nullptr;
     const int32_t* offsets = reinterpret_cast<const int32_t*>(params);
-    if (make_shape(params, tokens, offsets, sequences, ZERO_F16, bias, ZERO_F16, &s, &b))
+    if (make_shape(params, tokens, offsets, sequences, ZERO_F16, bias, ZERO_F16, &s, &b) &&
+        make_shape(params, tokens, nullptr, sequences, ZERO_F16, bias, ZERO_F16, &s, &b))
         return 0;
     return size_t(workspace_need(s, b.count));
 }

@@ -363,7 +363,12 @@ private:
         const uint64_t from = uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(b >> 32)))) << 32 |
                               uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(b)));
         to = __builtin_amdgcn_readfirstlane(to);
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(to), "v"(at), "s"(from) : "memory");
+        // m0 is a register that the compiler reserves, of which it warns; the clobber keeps it from taking over a value of its own
+        // that it set there before
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(to), "v"(at), "s"(from) : "memory", "m0");
+#pragma clang diagnostic pop
     }
 };
 

@@ -44,6 +44,8 @@ class WindowAttention:
         self.eps, self.interleaved = float(eps), bool(interleaved)
         self.dtype = torch.float16 if dtype is None else dtype
         self.device = torch.device(device)
+        if self.device.type == "cuda" and self.dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError(f"WindowAttention: attention takes torch.float16 or torch.bfloat16, not {self.dtype}")
         new = lambda h: torch.empty(self.max_tokens, h, dim, dtype=self.dtype, device=self.device)
         self._q, self._k, self._o = new(heads), new(kv_heads), new(heads)
         self._lse = torch.empty(heads * self.max_tokens, dtype=torch.float32, device=self.device)

@@ -800,6 +800,10 @@ int zero_attention_buckets(uint32_t* starts, uint32_t buckets, uint32_t max_dist
  * dtype, ZERO_F16 or ZERO_BF16.  lse: binary32, heads x tokens (NULL: not
  * kept; the backward pass needs it).  bias: heads x buckets of dtype or
  * ZERO_F32 (vec_dtype); NULL exactly where buckets is 0.
+ * A bucket is masked by a bias of -inf or of any value far below the others';
+ * a token that sees masked buckets alone gets NaN from -inf, and from finite
+ * ones what their scores give. (Scores are formed in units of log 2: from
+ * 2^127 log(2) on, 1.18e38, a finite one counts as infinite.)
  * dev_offsets: device, sequences + 1 ascending token indices: sequence n is
  * the tokens dev_offsets[n] ... dev_offsets[n+1]-1 (its length may be 0); rows
  * of o and lse outside all sequences stay as they are.  NULL: sequences of
@@ -840,6 +844,8 @@ size_t zero_attention_workspace_bytes(const zero_attention_t* params, uint64_t t
  *   p = exp(s - lse),   ds = p * (do_i . v_j - do_i . o_i),
  *   dq_i = scale * sum over j of ds k_j,   dk_j = scale * sum over i of ds q_i,
  *   dv_j = sum over i of p do_i,   dbias[h][b] = sum of ds over the pairs of b
+ * p is off relatively by about 2^-22 |lse|, so little is left of it in a row
+ * whose every score is far from 0, as by a bias of -1e9 at all that it sees.
  * dk and dv are sums over the query heads that share a key head, too.  p and
  * ds are rounded to dtype for the products (ds for binary16 in units that go
  * by the sizes of do, o and v, so that it does not overflow); dbias is a sum of the unrounded ds.  dbias (NULL: not

@@ -12,15 +12,15 @@
 // the lane's own but for one exchange, and the weights go from the first product's
 // registers to the second's operand.
 //
-// Bound by issue: the exponentials, masks and roundings of 32 x 32 scores (108
-// vector instructions at 64 columns, 150 at 128) and the products follow one
+// Bound by issue: the exponentials, masks and roundings of 32 x 32 scores (some
+// 110 vector instructions at 64 columns, 150 at 128) and the products follow one
 // another in a wave, and waves overlap little of them.  Left out in trials at
 // 8 x 1024 positions: both products, 60% of the time stays; the tiles' fetches,
 // 85%.  8 x 1024 positions, 25 heads of 64: 46-49 us, 549-582 TFLOP/s of the visible
 // pairs.  2 x 4096 positions, 64 heads of 128 on 8 of keys, window 512: 204-217 us,
 // 599-637 TFLOP/s.  Operands read further ahead, two tiles a turn of the loop and
-// wave priorities gave nothing; four waves a SIMD spill; no bank conflicts are
-// counted.
+// wave priorities gave nothing; no bank conflicts are counted.  64 columns take
+// 124 registers, four waves a SIMD; with the bias' table 130, three.
 #include <type_traits>
 #include <vector>
 

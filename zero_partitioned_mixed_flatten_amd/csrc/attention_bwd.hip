@@ -18,11 +18,11 @@
 // ds (2-norm, relative: 2.5e-3 to 1.7e-3 in bfloat16, 3.1e-4 to 2.1e-4 in binary16).
 //
 // Bound by issue, as the forward pass, with more products a pair of tiles.
-// 8 x 1024 positions, 25 heads of 64: dq 63-65 us, dk and dv 95-99, 408-427 TFLOP/s
+// 8 x 1024 positions, 25 heads of 64: dq 63-67 us, dk and dv 95-99, 408-427 TFLOP/s
 // of the formula's five products; 8191 packed positions, 64 heads of 128 on 8 of
-// keys, window 1024: 464-490 and 701-737 us under the profiler, 1062-1110 together
+// keys, window 1024: 463-502 and 689-765 us under the profiler, 1062-1110 together
 // without, 509-532 TFLOP/s.  The bias adds 15 us to dk and dv, and its gradient's
-// sums by distance 48 to dq at 25 heads of 64.
+// sums by distance 50 to dq at 25 heads of 64.
 #include <type_traits>
 
 #include "attention.hpp"
@@ -857,8 +857,8 @@ Deal deal(const Shape& s, bool ragged)
         d.near_slots = d.apart ? most : s.sequences;
     }
     // enough parts for two workgroups a CU, but none with fewer than four steps where a sequence has the mean length:
-    // a part costs a workgroup's start and 128 rows of binary32 sums written and read.  4099 positions, 3 key heads of
-    // 80, window 700: 105 items, five parts each: 74 us and 12 for the sums
+    // a part costs a workgroup's start and 128 rows of binary32 sums written and read.  4099 positions in 5, 3 key heads
+    // of 80, window 700: 99 pieces in 111 slots, five parts each: 74 us and 12 for the sums
     const uint64_t kv = s.heads / s.group, items = d.slots * kv;
     const uint64_t wanted = (kItems + items - 1) / items, most = most_splits(s, s.tokens / s.sequences + 1);
     d.splits = wanted < most ? wanted : most;

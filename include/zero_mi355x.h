@@ -802,8 +802,8 @@ int zero_attention_buckets(uint32_t* starts, uint32_t buckets, uint32_t max_dist
  * ZERO_F32 (vec_dtype); NULL exactly where buckets is 0.
  * A bucket is masked by a bias of -inf or of any value far below the others';
  * a token that sees masked buckets alone gets NaN from -inf, and from finite
- * ones what their scores give. (Scores are formed in units of log 2: from
- * 2^127 log(2) on, 1.18e38, a finite one counts as infinite.)
+ * ones what binary32 leaves of scores so far from 0.  (They are formed in units
+ * of log 2: of 2^127 log 2 or more in size, 1.18e38, a finite one counts as infinite.)
  * dev_offsets: device, sequences + 1 ascending token indices: sequence n is
  * the tokens dev_offsets[n] ... dev_offsets[n+1]-1 (its length may be 0); rows
  * of o and lse outside all sequences stay as they are.  NULL: sequences of
@@ -848,11 +848,12 @@ size_t zero_attention_workspace_bytes(const zero_attention_t* params, uint64_t t
  * whose every score is far from 0, as by a bias of -1e9 at all that it sees.
  * dk and dv are sums over the query heads that share a key head, too.  p and
  * ds are rounded to dtype for the products (ds for binary16 in units that go
- * by the sizes of do, o and v, so that it does not overflow); dbias is a sum of the unrounded ds.  dbias (NULL: not
- * wanted): heads x buckets of grad_dtype, dtype or ZERO_F32, stored, or with
- * accumulate added to what is there, then rounded once.  An inf or NaN anywhere
- * in a sequence may reach all gradients of that sequence, and dbias, as an
- * overflowed backward pass does; other sequences' rows take nothing from it.
+ * by the sizes of do, o and v, so that it does not overflow); dbias is a sum of
+ * the unrounded ds.  dbias (NULL: not wanted): heads x buckets of grad_dtype,
+ * dtype or ZERO_F32, stored, or with accumulate added to what is there, then
+ * rounded once.  An inf or NaN anywhere in a sequence may reach all gradients of
+ * that sequence, and dbias, as an overflowed backward pass does; other sequences'
+ * rows take nothing from it.
  * dq, dk and dv must not overlap an input or each other.  Rows outside all
  * sequences stay as they are.  workspace: device, 16-byte aligned, >=
  * zero_attention_workspace_bytes(params, tokens, sequences); contents need no

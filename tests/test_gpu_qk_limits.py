@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import attention_oracle as A
-from test_gpu_attention import F16, F32, close
+from test_gpu_attention import F16, close
 
 pytestmark = pytest.mark.gpu
 

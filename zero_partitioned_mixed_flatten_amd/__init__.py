@@ -47,4 +47,5 @@ __all__ = ["EXPORTS", "NORM_PARTIAL_BYTES", "STATE_BYTES", "ZERO_BF16", "ZERO_F1
            "zero_dropout_layernorm_fwd", "zero_dropout_layernorm_bwd", "zero_layer_workspace_bytes", "LayerRng",
            "ResidualNorm", "ZERO_MAX_BUCKETS", "AttentionParams", "attention_params", "zero_rope_table",
            "zero_qk_norm_rope_fwd", "zero_qk_workspace_bytes", "zero_qk_norm_rope_bwd", "zero_attention_buckets",
-           "zero_attention_fwd", "zero_attention_clear_rows", "zero_attention_workspace_bytes", "zero_attention_bwd", "WindowAttention"]
+           "zero_attention_fwd", "zero_attention_clear_rows", "zero_attention_workspace_bytes", "zero_attention_bwd",
+           "WindowAttention"]

@@ -893,8 +893,9 @@ Space space(const Shape& s, const Deal& d, uint32_t buckets, int dim)
 
 // Of a call with or without offsets, and of every smaller one: no more tokens in
 // no more sequences.  The slots of sequences of equal length are no more than
-// those with offsets (which hold for any lengths); fewer items may be cut into more parts, of which i items
-// have at most i + kItems - 1, and i times what the longest sequence allows.
+// those with offsets (which hold for any lengths); fewer items may be cut into
+// more parts, of which i items have at most i + kItems - 1, and i times what the
+// longest sequence allows.
 uint64_t workspace_need(const Shape& s, uint32_t buckets)
 {
     Deal d = deal(s, true);
@@ -940,7 +941,8 @@ int launch(const BwdArgs<T>& a, hipStream_t stream)
     rc = launch_status();
     if (rc || (a.splits == 1 && !a.far_slots))
         return rc;
-    hipLaunchKernelGGL((dkv_sum_kernel<T, DIM>), dim3((a.splits > 1 ? a.slots : a.near_slots) * (kOwn / kSumRows), kv), dim3(kSumRows * DIM / 8), 0, stream, a);
+    hipLaunchKernelGGL((dkv_sum_kernel<T, DIM>), dim3((a.splits > 1 ? a.slots : a.near_slots) * (kOwn / kSumRows), kv),
+                       dim3(kSumRows * DIM / 8), 0, stream, a);
     return launch_status();
 }
 
@@ -956,7 +958,8 @@ int run(Heads<void> dq, Heads<void> dk, Heads<void> dv, Heads<const void> dout, 
     auto part = [&](uint64_t at) { return reinterpret_cast<float*>(workspace + at); };
     const BwdArgs<T> a{out(dq), out(dk), out(dv), in(dout), in(o), in(q), in(k), in(v), lse, reinterpret_cast<f32x2*>(workspace + p.stats),
                        part(p.units), dbias ? part(p.partials) : nullptr, part(p.near), part(p.far), s, b, uint32_t(d.slots), uint32_t(d.splits),
-                       uint32_t(d.far_slots), uint32_t(d.near_slots), uint32_t(d.long_from), uint32_t(d.apart), Order(s, s.heads, d.slots), Order(s, s.heads / s.group, d.slots)};
+                       uint32_t(d.far_slots), uint32_t(d.near_slots), uint32_t(d.long_from), uint32_t(d.apart), Order(s, s.heads, d.slots),
+                       Order(s, s.heads / s.group, d.slots)};
     if (!launches_fit(a))
         return ZERO_ERANGE;
     auto go = [&](auto dim, auto way) {

@@ -717,6 +717,7 @@ int zero_dropout_layernorm_bwd(void* dx, uint64_t ld_dx, void* dr, uint64_t ld_d
  *   rot / 2 with the position's (cos, sin),
  *     (a, b) -> (a cos - b sin, b cos + a sin),
  *   elements (p, p + rot / 2), or with interleaved (2p, 2p + 1).
+ * The sum of squares is binary32's: of 2^128 or more it makes rstd 0.
  * dtype: ZERO_F16, ZERO_BF16 or ZERO_F32; wq and wk: dim elements of vec_dtype,
  * dtype or ZERO_F32.  dim even and at most 256, rot even and at most dim (0:
  * no rotation, table not looked at).  kv_heads may be 0 (k, k_out and wk NULL).

@@ -39,6 +39,15 @@ def test_large_values(size):
         assert all(bool(t.isfinite().all()) for t in got[:3])
 
 
+@pytest.mark.parametrize("dim", [8, 24, 40, 72, 80, 120])
+def test_large_values_at_other_head_sizes(dim):
+    for layout in ("plain", "joint", "odd", "heads"):
+        log("large values", dim, layout)
+        c = LargeValues([90, 1, 150], 4, 2, dim, F16, window=40, sinks=3, layout=layout, size=60000.0, after=2)
+        got = c.check_bwd(*c.check_fwd())
+        assert all(bool(t[:c.end].isfinite().all()) for t in got[:3])
+
+
 @pytest.mark.parametrize("starts", [[0, 1, 20], [0, 3, 601]])
 def test_large_values_with_a_bias(starts):
     """The gradient of the bias takes each ds once."""
